@@ -387,7 +387,7 @@ def _own_exchange(st):
     if c["step"] == "dispatch":
         zc.zc_dispatch_plan(st["ids"], t, k, e, st["workspace"], st["workspace"].numel(), st["offsets"],
                             st["plan_position"], st["plan_source"])
-        zc.zc_dispatch(st["x"], t, h, h, st["plan_source"], t * k, k, st["out"], h)
+        zc.zc_dispatch(st["x"], t, h, h, st["plan_position"], k, st["out"], t * k, h)
         return {"offsets": st["offsets"], "position": st["plan_position"], "source": st["plan_source"],
                 "payload": st["out"]}
     zc.zc_combine(st["z"], t * k, h, h, st["position"], st["weights"], t, k, st["y"], h)
