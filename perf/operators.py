@@ -408,16 +408,17 @@ def _own_product(st):
         (xq, xs), (wq, ws) = st["xq"], st["w"]
         zc.zc_fp8_quantize(st["x"], m, k, k, e4, 1, xq, xs)
         zc.zc_fp8_matmul(xq, xs, e4, m, wq, ws, e4, n, k, g, st["offsets"], st["out"], zc.ZC_BF16, n,
-                         st["workspace"], st["workspace"].numel())
+                         zc.ZC_FP8_SUM_FAST, st["workspace"], st["workspace"].numel())
         return {"y": st["out"]}
     gf = zc.ZC_FP8_E5M2 if c["grad"] == "e5m2" else e4
     (dq, ds), (dt, dts), (xt, xts), (wq, ws) = st["dyq"], st["dyt"], st["xt"], st["wt"]
     zc.zc_fp8_quantize(st["dy"], m, n, n, gf, 1, dq, ds)
     zc.zc_fp8_matmul(dq, ds, gf, m, wq, ws, e4, k, n, g, st["offsets"], st["dx"], zc.ZC_BF16, k,
-                     st["workspace"], st["workspace"].numel())
+                     zc.ZC_FP8_SUM_FAST, st["workspace"], st["workspace"].numel())
     zc.zc_fp8_quantize_t(st["dy"], None, zc.ZC_BF16, m, n, n, g, st["offsets"], gf, dt, dts, st["most"])
     zc.zc_fp8_quantize_t(st["xq"][0], st["xq"][1], e4, m, k, _up(k, BLOCK), g, st["offsets"], e4, xt, xts, st["most"])
-    zc.zc_fp8_matmul_wgrad(dt, dts, gf, n, xt, xts, e4, k, st["most"], m, g, st["offsets"], st["dw"], zc.ZC_BF16)
+    zc.zc_fp8_matmul_wgrad(dt, dts, gf, n, xt, xts, e4, k, st["most"], m, g, st["offsets"], st["dw"], zc.ZC_BF16,
+                           zc.ZC_FP8_SUM_FAST)
     return {"dx": st["dx"], "dw": st["dw"]}
 
 
