@@ -12,6 +12,10 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libzc.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("zc_compress.hip", "zc_decode.hip", "zc_reduce.hip", "zc_stats.hip",
                                             "zc_host.cpp")]
+# The mixture-of-experts operators (include/zc_moe.h): in the shipped library,
+# not in the codec's test and timeline builds.
+MOE_SOURCES = [os.path.join(CSRC, f) for f in ("zc_route.hip", "zc_exchange.hip", "zc_fp8.hip", "zc_matmul.hip",
+                                               "zc_swiglu.hip")]
 ARCH = "gfx950"
 
 # Packed-FP32 instructions stay disabled for every HIP translation unit.
@@ -32,7 +36,7 @@ def compile_command(out: str, extra=()) -> list:
 
 def build(verbose: bool = False) -> str:
     tmp = LIB + ".tmp%d" % os.getpid()
-    cmd = compile_command(tmp)
+    cmd = compile_command(tmp, extra=tuple(MOE_SOURCES))
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)

@@ -1,0 +1,393 @@
+// The token exchange around the experts, MI355X / gfx950: the order of the token
+// copies by expert (a stable counting sort), the payload in that order, the
+// weighted sum of a token's copies, and its gradients.
+#include "zc_moe_device.h"
+
+namespace zc {
+namespace moe {
+
+// ---------------------------------------------------------------------------
+// plan: stable counting sort of tokens * top_k expert ids
+// ---------------------------------------------------------------------------
+
+constexpr uint32_t kPlanThreads = 256;
+constexpr uint32_t kPlanWaves = kPlanThreads / kLanes;
+constexpr uint32_t kPlanChunk = 2048;  // copies a block ranks
+constexpr uint32_t kPlanPerWave = kPlanChunk / kPlanWaves;
+constexpr uint32_t kBins = ZC_MAX_EXPERTS + 1;  // one bin more for dropped copies
+
+struct PlanArgs {
+    const int32_t *ids;
+    uint32_t *hist;  // [chunks][experts + 1]
+    int32_t *offsets, *position, *source;
+    uint32_t copies, experts, chunks;
+};
+
+__device__ __forceinline__ uint32_t bin_of(const PlanArgs &a, uint32_t i) {
+    const int32_t id = a.ids[i];
+    return id >= 0 && (uint32_t)id < a.experts ? (uint32_t)id : a.experts;
+}
+
+// Copies of every expert in one chunk.
+__global__ __launch_bounds__(kPlanThreads) void plan_count_kernel(PlanArgs a) {
+    __shared__ uint32_t bins[kBins];
+    for (uint32_t e = threadIdx.x; e <= a.experts; e += kPlanThreads) bins[e] = 0;
+    __syncthreads();
+    const uint32_t i0 = blockIdx.x * kPlanChunk;
+    for (uint32_t j = threadIdx.x; j < kPlanChunk; j += kPlanThreads)
+        if (i0 + j < a.copies) atomicAdd(&bins[bin_of(a, i0 + j)], 1u);
+    __syncthreads();
+    uint32_t *row = a.hist + (uint64_t)blockIdx.x * (a.experts + 1);
+    for (uint32_t e = threadIdx.x; e <= a.experts; e += kPlanThreads) row[e] = bins[e];
+}
+
+// Ranks a chunk's copies.  A copy's row is the copies of lower experts (a scan
+// of the totals), the same expert's copies of earlier chunks, of earlier waves
+// of the chunk, and of earlier lanes of its wave: integer counts only, so the
+// order is that of the copies.
+__global__ __launch_bounds__(kPlanThreads) void plan_place_kernel(PlanArgs a) {
+    __shared__ uint32_t total[kBins + 3];           // copies of an expert, then of all lower experts
+    __shared__ uint32_t base[kPlanWaves][kBins + 3];  // a wave's next row of every expert
+    __shared__ uint32_t part[kPlanWaves];
+    const uint32_t tid = threadIdx.x, lane = lane_id(), wave = tid / kLanes, nb = a.experts + 1;
+    for (uint32_t e = tid; e < nb; e += kPlanThreads) {
+        uint32_t all = 0, before = 0;
+        for (uint32_t c = 0; c < a.chunks; ++c) {
+            const uint32_t v = a.hist[(uint64_t)c * nb + e];
+            before += c < blockIdx.x ? v : 0u;
+            all += v;
+        }
+        total[e] = all;
+        base[0][e] = before;
+#pragma unroll
+        for (uint32_t w = 1; w < kPlanWaves; ++w) base[w][e] = 0;
+    }
+    __syncthreads();
+    // copies of lower experts: each thread takes consecutive bins
+    const uint32_t per = (nb + kPlanThreads - 1) / kPlanThreads, e0 = tid * per, e1 = min(e0 + per, nb);
+    uint32_t mine = 0;
+    for (uint32_t e = e0; e < e1; ++e) mine += total[e];
+    const uint32_t incl = scan_sum(mine, lane);
+    if (lane == kLanes - 1) part[wave] = incl;
+    __syncthreads();
+    uint32_t run = incl - mine;
+    for (uint32_t w = 0; w < wave; ++w) run += part[w];
+    for (uint32_t e = e0; e < e1; ++e) {
+        const uint32_t n = total[e];
+        base[0][e] += run;
+        if (blockIdx.x == 0) a.offsets[e] = (int32_t)run;  // bin `experts` (dropped copies) ends the last expert's rows
+        run += n;
+    }
+    // the copies of each wave but the last, counted into the next wave's base
+    const uint32_t i0 = blockIdx.x * kPlanChunk + wave * kPlanPerWave;
+    if (wave + 1 < kPlanWaves)
+        for (uint32_t j = lane; j < kPlanPerWave; j += kLanes)
+            if (i0 + j < a.copies) atomicAdd(&base[wave + 1][bin_of(a, i0 + j)], 1u);
+    __syncthreads();
+    for (uint32_t e = tid; e < nb; e += kPlanThreads)
+#pragma unroll
+        for (uint32_t w = 1; w < kPlanWaves; ++w) base[w][e] += base[w - 1][e];
+    __syncthreads();
+    uint32_t *next = base[wave];
+    for (uint32_t j = 0; j < kPlanPerWave; j += kLanes) {
+        const uint32_t i = i0 + j + lane;
+        const bool in = i < a.copies;
+        const uint32_t b = in ? bin_of(a, i) : ZC_MAX_EXPERTS + 1u;  // a bin of its own for lanes past the end
+        // lanes of the same bin, one bit of the bin's number at a time
+        uint64_t same = ~0ull;
+#pragma unroll
+        for (uint32_t bit = 0; bit < 11; ++bit) {
+            const uint64_t on = __ballot((b >> bit) & 1u);
+            same &= ((b >> bit) & 1u) ? on : ~on;
+        }
+        const uint32_t rank = (uint32_t)__popcll(same & ((1ull << lane) - 1ull));
+        uint32_t p = 0;
+        if (in) p = next[b] + rank;
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // every lane has read before the counts move on
+        if (in && rank == 0) next[b] += (uint32_t)__popcll(same);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        if (in) {
+            const bool dropped = b == a.experts;
+            a.position[i] = dropped ? -1 : (int32_t)p;
+            if (a.source) a.source[p] = dropped ? -1 : (int32_t)i;
+        }
+    }
+}
+
+__global__ void plan_empty_kernel(int32_t *offsets, uint32_t n) {
+    for (uint32_t i = threadIdx.x; i < n; i += blockDim.x) offsets[i] = 0;
+}
+
+// ---------------------------------------------------------------------------
+// rows of BF16: V values an access (8: 16 bytes; 1 for rows that are not
+// aligned for that)
+// ---------------------------------------------------------------------------
+
+constexpr uint32_t kRowThreads = 256;
+
+template <uint32_t V>
+struct Vals {
+    float v[V];
+};
+
+template <uint32_t V>
+__device__ __forceinline__ Vals<V> load_vals(const uint16_t *p) {
+    Vals<V> r;
+    if (V == 8) {
+        const u32v4 w = *reinterpret_cast<const u32v4 *>(p);
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i) {
+            r.v[(2 * i) % V] = bf_lo(w[i]);
+            r.v[(2 * i + 1) % V] = bf_hi(w[i]);
+        }
+    } else {
+        r.v[0] = bf_one(*p);
+    }
+    return r;
+}
+
+template <uint32_t V>
+__device__ __forceinline__ void store_vals(uint16_t *p, const Vals<V> &r) {
+    if (V == 8) {
+        u32v4 w;
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i) w[i] = bf_pack(r.v[(2 * i) % V], r.v[(2 * i + 1) % V]);
+        *reinterpret_cast<u32v4 *>(p) = w;
+    } else {
+        *p = bf_round(r.v[0]);
+    }
+}
+
+struct RowArgs {
+    const uint16_t *x;   // dispatch: tokens; combine: the experts' rows
+    const uint16_t *dy;  // combine's backward
+    const int32_t *position;
+    const float *weights;
+    uint16_t *out;
+    float *dweights;
+    uint64_t xs, dys, os;
+    uint32_t tokens, top_k, rows, hidden;
+};
+
+// One block a token: the row is read once and written to each of its places.
+template <uint32_t V>
+__global__ __launch_bounds__(kRowThreads) void dispatch_kernel(RowArgs a) {
+    for (uint32_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
+        const int32_t *pos = a.position + (uint64_t)t * a.top_k;
+        const uint16_t *src = a.x + (uint64_t)t * a.xs;
+        for (uint32_t h = threadIdx.x * V; h < a.hidden; h += kRowThreads * V) {
+            if (V == 8) {
+                const u32v4 w = *reinterpret_cast<const u32v4 *>(src + h);
+                for (uint32_t k = 0; k < a.top_k; ++k) {
+                    const int32_t p = pos[k];
+                    if (p >= 0 && (uint32_t)p < a.rows) *reinterpret_cast<u32v4 *>(a.out + (uint64_t)p * a.os + h) = w;
+                }
+            } else {
+                const uint16_t w = src[h];
+                for (uint32_t k = 0; k < a.top_k; ++k) {
+                    const int32_t p = pos[k];
+                    if (p >= 0 && (uint32_t)p < a.rows) a.out[(uint64_t)p * a.os + h] = w;
+                }
+            }
+        }
+    }
+}
+
+// One block a token; the sums stay in 32 bits, k ascending.
+template <uint32_t V>
+__global__ __launch_bounds__(kRowThreads) void combine_kernel(RowArgs a) {
+    for (uint32_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
+        const int32_t *pos = a.position + (uint64_t)t * a.top_k;
+        for (uint32_t h = threadIdx.x * V; h < a.hidden; h += kRowThreads * V) {
+            Vals<V> sum;
+#pragma unroll
+            for (uint32_t i = 0; i < V; ++i) sum.v[i] = 0.0f;
+            for (uint32_t k = 0; k < a.top_k; ++k) {
+                const int32_t p = pos[k];
+                if (p < 0 || (uint32_t)p >= a.rows) continue;
+                const float w = a.weights ? a.weights[(uint64_t)t * a.top_k + k] : 1.0f;
+                const Vals<V> z = load_vals<V>(a.x + (uint64_t)p * a.xs + h);
+#pragma unroll
+                for (uint32_t i = 0; i < V; ++i) sum.v[i] = fmaf(w, z.v[i], sum.v[i]);
+            }
+            store_vals<V>(a.out + (uint64_t)t * a.os + h, sum);
+        }
+    }
+}
+
+// One block a token: dz = w dy and the products <dy, z>, each k's summed over
+// the block in an order fixed by the sizes.
+template <uint32_t V>
+__global__ __launch_bounds__(kRowThreads) void combine_backward_kernel(RowArgs a) {
+    __shared__ float part[kRowThreads / kLanes][ZC_MAX_TOP_K];
+    const uint32_t lane = lane_id(), wave = threadIdx.x / kLanes;
+    for (uint32_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
+        const uint64_t tk = (uint64_t)t * a.top_k;
+        for (uint32_t k = 0; k < a.top_k; ++k) {
+            const int32_t p = a.position[tk + k];
+            const bool on = p >= 0 && (uint32_t)p < a.rows;
+            const float w = a.weights && a.out ? a.weights[tk + k] : 1.0f;
+            float dot = 0.0f;
+            if (on)
+                for (uint32_t h = threadIdx.x * V; h < a.hidden; h += kRowThreads * V) {
+                    const Vals<V> dy = load_vals<V>(a.dy + (uint64_t)t * a.dys + h);
+                    if (a.dweights) {
+                        const Vals<V> z = load_vals<V>(a.x + (uint64_t)p * a.xs + h);
+#pragma unroll
+                        for (uint32_t i = 0; i < V; ++i) dot = fmaf(dy.v[i], z.v[i], dot);
+                    }
+                    if (a.out) {
+                        Vals<V> dz;
+#pragma unroll
+                        for (uint32_t i = 0; i < V; ++i) dz.v[i] = w * dy.v[i];
+                        store_vals<V>(a.out + (uint64_t)p * a.os + h, dz);
+                    }
+                }
+            dot = group_sum<64>(dot);
+            if (lane == 0) part[wave][k] = dot;
+        }
+        __syncthreads();
+        if (a.dweights && threadIdx.x < a.top_k) {
+            float s = 0.0f;
+#pragma unroll
+            for (uint32_t w = 0; w < kRowThreads / kLanes; ++w) s += part[w][threadIdx.x];
+            a.dweights[tk + threadIdx.x] = s;
+        }
+        __syncthreads();
+    }
+}
+
+static bool sizes_ok(uint64_t tokens, uint32_t top_k) {
+    return top_k >= 1 && top_k <= ZC_MAX_TOP_K && tokens <= kMaxRows && tokens * top_k <= kMaxRows;
+}
+static bool wide(const void *p, uint64_t stride) { return aligned(p, 16) && stride % 8 == 0; }
+static uint32_t token_blocks(uint32_t tokens) { return tokens < (1u << 20) ? tokens : (1u << 20); }
+
+}  // namespace moe
+}  // namespace zc
+
+using namespace zc::moe;
+
+extern "C" uint64_t zc_dispatch_workspace_bytes(uint64_t tokens, uint32_t top_k, uint32_t experts) {
+    if (!sizes_ok(tokens, top_k) || experts == 0 || experts > ZC_MAX_EXPERTS) return 0;
+    const uint64_t bytes = ceil_div(tokens * top_k, kPlanChunk) * (experts + 1) * 4;
+    return ceil_div(bytes + 1, 256) * 256;
+}
+
+extern "C" zc_status zc_dispatch_plan(const int32_t *d_ids, uint64_t tokens, uint32_t top_k, uint32_t experts,
+                                      void *d_workspace, uint64_t workspace_bytes, int32_t *d_offsets,
+                                      int32_t *d_position, int32_t *d_source, void *stream) {
+    if (!sizes_ok(tokens, top_k) || experts == 0 || experts > ZC_MAX_EXPERTS || !d_offsets ||
+        (tokens && (!d_ids || !d_position || !d_workspace)))
+        return ZC_ERR_INVALID_ARG;
+    if (!aligned(d_ids, 4) || !aligned(d_offsets, 4) || !aligned(d_position, 4) || !aligned(d_source, 4) ||
+        !aligned(d_workspace, 16))
+        return ZC_ERR_MISALIGNED;
+    if (tokens && workspace_bytes < zc_dispatch_workspace_bytes(tokens, top_k, experts)) return ZC_ERR_CAPACITY;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (!tokens) {
+        hipLaunchKernelGGL(plan_empty_kernel, dim3(1), dim3(256), 0, st, d_offsets, experts + 1);
+        return launched();
+    }
+    PlanArgs a = {d_ids, static_cast<uint32_t *>(d_workspace), d_offsets, d_position, d_source,
+                  (uint32_t)(tokens * top_k), experts, 0};
+    a.chunks = (uint32_t)ceil_div(a.copies, kPlanChunk);
+    hipLaunchKernelGGL(plan_count_kernel, dim3(a.chunks), dim3(kPlanThreads), 0, st, a);
+    hipLaunchKernelGGL(plan_place_kernel, dim3(a.chunks), dim3(kPlanThreads), 0, st, a);
+    return launched();
+}
+
+extern "C" zc_status zc_dispatch(const void *d_x, uint64_t tokens, uint64_t hidden, uint64_t x_stride,
+                                 const int32_t *d_position, uint32_t top_k, void *d_out, uint64_t rows,
+                                 uint64_t out_stride, void *stream) {
+    if (!sizes_ok(tokens, top_k) || rows > kMaxRows || hidden > kMaxCols || x_stride < hidden ||
+        x_stride > kMaxStride || out_stride < hidden || out_stride > kMaxStride)
+        return ZC_ERR_INVALID_ARG;
+    if (!tokens || !hidden || !rows) return ZC_OK;
+    if (!d_x || !d_position || !d_out) return ZC_ERR_INVALID_ARG;
+    if (!aligned(d_x, 2) || !aligned(d_position, 4) || !aligned(d_out, 2)) return ZC_ERR_MISALIGNED;
+    RowArgs a = {};
+    a.x = static_cast<const uint16_t *>(d_x);
+    a.position = d_position;
+    a.out = static_cast<uint16_t *>(d_out);
+    a.xs = x_stride;
+    a.os = out_stride;
+    a.tokens = (uint32_t)tokens;
+    a.top_k = top_k;
+    a.rows = (uint32_t)rows;
+    a.hidden = (uint32_t)hidden;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    const dim3 grid(token_blocks(a.tokens)), block(kRowThreads);
+    if (hidden % 8 == 0 && wide(d_x, x_stride) && wide(d_out, out_stride))
+        hipLaunchKernelGGL(dispatch_kernel<8>, grid, block, 0, st, a);
+    else
+        hipLaunchKernelGGL(dispatch_kernel<1>, grid, block, 0, st, a);
+    return launched();
+}
+
+extern "C" zc_status zc_combine(const void *d_z, uint64_t rows, uint64_t hidden, uint64_t z_stride,
+                                const int32_t *d_position, const float *d_weights, uint64_t tokens, uint32_t top_k,
+                                void *d_y, uint64_t y_stride, void *stream) {
+    if (!sizes_ok(tokens, top_k) || rows > kMaxRows || hidden > kMaxCols || z_stride < hidden ||
+        z_stride > kMaxStride || y_stride < hidden || y_stride > kMaxStride)
+        return ZC_ERR_INVALID_ARG;
+    if (!tokens || !hidden) return ZC_OK;
+    if ((rows && !d_z) || !d_position || !d_y) return ZC_ERR_INVALID_ARG;
+    if (!aligned(d_z, 2) || !aligned(d_position, 4) || !aligned(d_weights, 4) || !aligned(d_y, 2))
+        return ZC_ERR_MISALIGNED;
+    RowArgs a = {};
+    a.x = static_cast<const uint16_t *>(d_z);
+    a.position = d_position;
+    a.weights = d_weights;
+    a.out = static_cast<uint16_t *>(d_y);
+    a.xs = z_stride;
+    a.os = y_stride;
+    a.tokens = (uint32_t)tokens;
+    a.top_k = top_k;
+    a.rows = (uint32_t)rows;
+    a.hidden = (uint32_t)hidden;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    const dim3 grid(token_blocks(a.tokens)), block(kRowThreads);
+    if (hidden % 8 == 0 && wide(d_z, z_stride) && wide(d_y, y_stride))
+        hipLaunchKernelGGL(combine_kernel<8>, grid, block, 0, st, a);
+    else
+        hipLaunchKernelGGL(combine_kernel<1>, grid, block, 0, st, a);
+    return launched();
+}
+
+extern "C" zc_status zc_combine_backward(const void *d_dy, uint64_t dy_stride, const void *d_z, uint64_t rows,
+                                         uint64_t hidden, uint64_t z_stride, const int32_t *d_position,
+                                         const float *d_weights, uint64_t tokens, uint32_t top_k, void *d_dz,
+                                         uint64_t dz_stride, float *d_dweights, void *stream) {
+    if (!sizes_ok(tokens, top_k) || rows > kMaxRows || hidden > kMaxCols || dy_stride < hidden ||
+        dy_stride > kMaxStride || (d_dweights && (z_stride < hidden || z_stride > kMaxStride)) ||
+        (d_dz && (dz_stride < hidden || dz_stride > kMaxStride)))
+        return ZC_ERR_INVALID_ARG;
+    if (!tokens || (!d_dz && !d_dweights)) return ZC_OK;
+    if ((hidden && !d_dy) || !d_position || (d_dweights && rows && hidden && !d_z)) return ZC_ERR_INVALID_ARG;
+    if (!aligned(d_dy, 2) || !aligned(d_z, 2) || !aligned(d_position, 4) || !aligned(d_weights, 4) ||
+        !aligned(d_dz, 2) || !aligned(d_dweights, 4))
+        return ZC_ERR_MISALIGNED;
+    RowArgs a = {};
+    a.x = static_cast<const uint16_t *>(d_z);
+    a.dy = static_cast<const uint16_t *>(d_dy);
+    a.position = d_position;
+    a.weights = d_weights;
+    a.out = static_cast<uint16_t *>(d_dz);
+    a.dweights = d_dweights;
+    a.xs = z_stride;
+    a.dys = dy_stride;
+    a.os = dz_stride;
+    a.tokens = (uint32_t)tokens;
+    a.top_k = top_k;
+    a.rows = (uint32_t)rows;
+    a.hidden = (uint32_t)hidden;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    const dim3 grid(token_blocks(a.tokens)), block(kRowThreads);
+    if (hidden % 8 == 0 && wide(d_dy, dy_stride) && (!d_dweights || wide(d_z, z_stride)) &&
+        (!d_dz || wide(d_dz, dz_stride)))
+        hipLaunchKernelGGL(combine_backward_kernel<8>, grid, block, 0, st, a);
+    else
+        hipLaunchKernelGGL(combine_backward_kernel<1>, grid, block, 0, st, a);
+    return launched();
+}

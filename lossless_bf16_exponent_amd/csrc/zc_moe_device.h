@@ -1,0 +1,234 @@
+// Device and host helpers shared by the mixture-of-experts kernels (gfx950):
+// BF16 and 8-bit conversions, the block scale, wave-wide reductions, and the
+// lookup of a tile's expert in offsets that live on the device.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <stdint.h>
+
+#include "zc_moe.h"
+
+namespace zc {
+namespace moe {
+
+constexpr uint32_t kLanes = 64;
+constexpr uint32_t kBlock = ZC_FP8_BLOCK;
+
+typedef uint32_t u32v4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32v2 __attribute__((ext_vector_type(2)));
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+
+inline uint64_t ceil_div(uint64_t a, uint64_t b) { return a / b + (a % b != 0); }
+inline uint64_t stride8(uint64_t cols) { return ceil_div(cols, kBlock) * kBlock; }
+inline uint64_t scale_stride(uint64_t cols) { return ceil_div(ceil_div(cols, kBlock), 4) * 4; }
+inline bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+inline bool is_fp8(uint32_t t) { return t == ZC_FP8_E4M3 || t == ZC_FP8_E5M2; }
+
+// Row counts fit 31 bits with room to round up; row lengths are bounded so
+// that a row's bytes fit 32 bits.
+constexpr uint64_t kMaxRows = 0x7FFFFFFFull - ZC_MOE_ROW_SLACK;
+constexpr uint64_t kMaxCols = 1ull << 28;
+constexpr uint64_t kMaxStride = 1ull << 40;
+
+inline zc_status launched() { return hipGetLastError() == hipSuccess ? ZC_OK : ZC_ERR_HIP; }
+
+// ---------------------------------------------------------------------------
+// numbers
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+__device__ __forceinline__ float bf_one(uint16_t h) { return __uint_as_float((uint32_t)h << 16); }
+
+// Two floats as a pair of BF16, to nearest with ties to even (the conversion
+// instruction of gfx950; NaN stays NaN).
+__device__ __forceinline__ uint32_t bf_pack(float a, float b) {
+    typedef float f2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+    const f2 v = {a, b};
+    const b2 r = __builtin_convertvector(v, b2);
+    return __builtin_bit_cast(uint32_t, r);
+}
+__device__ __forceinline__ uint16_t bf_round(float a) { return (uint16_t)bf_pack(a, 0.0f); }
+
+// The scale byte of a block from the bits of its largest finite BF16 magnitude
+// (15 bits).  The largest value of both 8-bit types is 1.75 times a power of
+// two (2^8, 2^15), so the exponent of the scale is the magnitude's own minus 8
+// (or 15), plus one when its mantissa is above 1.75 (96 of 128): adding 31
+// carries into the exponent exactly then.
+__device__ __forceinline__ uint32_t scale_byte(uint32_t amax15, uint32_t top) {
+    const uint32_t e = (amax15 + 31u) >> 7;
+    return e > top ? e - top : 0u;
+}
+// 1 / scale = 2^(127 - byte), byte 0..247.
+__device__ __forceinline__ float scale_inverse(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
+// scale = 2^(byte - 127) (byte 0 is a subnormal number).
+__device__ __forceinline__ float scale_value(uint32_t byte) {
+    return __uint_as_float(byte ? byte << 23 : 0x00400000u);
+}
+
+template <uint32_t TYPE>
+struct Fp8;
+template <>
+struct Fp8<ZC_FP8_E4M3> {
+    static constexpr uint32_t kTop = 8;
+    static constexpr int kFormat = 0;  // the matrix instructions' code of the type
+    __device__ __forceinline__ static uint32_t pack4(float a, float b, float c, float d) {
+        int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+        return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
+    }
+    template <int I>
+    __device__ __forceinline__ static float value(uint32_t w) {
+        return __builtin_amdgcn_cvt_f32_fp8((int)w, I);
+    }
+};
+template <>
+struct Fp8<ZC_FP8_E5M2> {
+    static constexpr uint32_t kTop = 15;
+    static constexpr int kFormat = 1;
+    __device__ __forceinline__ static uint32_t pack4(float a, float b, float c, float d) {
+        int w = __builtin_amdgcn_cvt_pk_bf8_f32(a, b, 0, false);
+        return (uint32_t)__builtin_amdgcn_cvt_pk_bf8_f32(c, d, w, true);
+    }
+    template <int I>
+    __device__ __forceinline__ static float value(uint32_t w) {
+        return __builtin_amdgcn_cvt_f32_bf8((int)w, I);
+    }
+};
+
+// Larger magnitude (15 bits) of a BF16 pair, infinities and NaN left out.
+__device__ __forceinline__ uint32_t finite_max(uint32_t m, uint32_t pair) {
+    const uint32_t a = pair & 0x7FFFu, b = (pair >> 16) & 0x7FFFu;
+    m = max(m, a < 0x7F80u ? a : 0u);
+    return max(m, b < 0x7F80u ? b : 0u);
+}
+
+// ---------------------------------------------------------------------------
+// waves
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ uint32_t lane_id() { return threadIdx.x & (kLanes - 1); }
+
+// Maximum / sum over the 2^k lanes of an aligned group of WIDTH lanes.
+template <int WIDTH>
+__device__ __forceinline__ uint32_t group_max(uint32_t v) {
+#pragma unroll
+    for (int s = 1; s < WIDTH; s <<= 1) v = max(v, (uint32_t)__shfl_xor((int)v, s));
+    return v;
+}
+template <int WIDTH>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+    for (int s = 1; s < WIDTH; s <<= 1) v += __shfl_xor(v, s);
+    return v;
+}
+
+__device__ __forceinline__ uint32_t scan_sum(uint32_t v, uint32_t lane) {
+#pragma unroll
+    for (int s = 1; s < (int)kLanes; s <<= 1) {
+        const uint32_t o = (uint32_t)__shfl_up((int)v, s);
+        v += lane >= (uint32_t)s ? o : 0u;
+    }
+    return v;
+}
+__device__ __forceinline__ uint32_t scan_max(uint32_t v, uint32_t lane) {
+#pragma unroll
+    for (int s = 1; s < (int)kLanes; s <<= 1) {
+        const uint32_t o = (uint32_t)__shfl_up((int)v, s);
+        v = max(v, lane >= (uint32_t)s ? o : 0u);
+    }
+    return v;
+}
+
+// ---------------------------------------------------------------------------
+// groups of rows
+// ---------------------------------------------------------------------------
+
+struct Span {
+    uint32_t group;
+    uint32_t begin, end;  // the group's rows
+    uint32_t tile;        // index of the tile within the group
+    uint32_t blocks0;     // blocks of 128 rows of the groups before it, each group rounded up
+    bool found;
+};
+
+__device__ __forceinline__ uint32_t clamp_row(int32_t v, uint32_t rows) {
+    return v < 0 ? 0u : min((uint32_t)v, rows);
+}
+
+// The group that tile t falls into when every group's rows are cut into tiles
+// of `tile_rows`; t counts the tiles of all groups in order.  offsets NULL: one
+// group of all rows.  The offsets are clamped to 0..rows and to ascending order
+// (a running maximum), so that no value of them leads outside the arrays.  The
+// whole wave calls this; the result is uniform.  64 groups a round.
+__device__ __forceinline__ Span find_tile(const int32_t *offsets, uint32_t groups, uint32_t rows, uint32_t tile_rows,
+                                          uint32_t t) {
+    Span s = {0, 0, rows, t, 0, false};
+    if (!offsets) {
+        s.found = (uint64_t)t * tile_rows < rows;
+        return s;
+    }
+    const uint32_t lane = lane_id();
+    uint32_t tiles_before = 0, blocks_before = 0, high = 0;
+    for (uint32_t g0 = 0; g0 < groups; g0 += kLanes) {
+        const uint32_t g = g0 + lane;
+        const bool in = g < groups;
+        const uint32_t o0 = in ? clamp_row(offsets[g], rows) : 0u;
+        const uint32_t o1 = in ? clamp_row(offsets[g + 1], rows) : 0u;
+        const uint32_t begin = max(scan_max(o0, lane), high);
+        const uint32_t end = in ? max(begin, o1) : begin;
+        const uint32_t n = end - begin;
+        const uint32_t tiles = (n + tile_rows - 1) / tile_rows, blocks = (n + kBlock - 1) / kBlock;
+        const uint32_t tsum = scan_sum(tiles, lane), bsum = scan_sum(blocks, lane);
+        const uint32_t first = tiles_before + tsum - tiles;
+        const uint64_t hit = __ballot(in && t >= first && t < first + tiles);
+        if (hit) {
+            const int l = __builtin_ctzll(hit);
+            s.group = g0 + (uint32_t)l;
+            s.begin = (uint32_t)__builtin_amdgcn_readlane((int)begin, l);
+            s.end = (uint32_t)__builtin_amdgcn_readlane((int)end, l);
+            s.tile = t - (uint32_t)__builtin_amdgcn_readlane((int)first, l);
+            s.blocks0 = blocks_before + (uint32_t)__builtin_amdgcn_readlane((int)(bsum - blocks), l);
+            s.found = true;
+            return s;
+        }
+        tiles_before += (uint32_t)__builtin_amdgcn_readlane((int)tsum, kLanes - 1);
+        blocks_before += (uint32_t)__builtin_amdgcn_readlane((int)bsum, kLanes - 1);
+        high = (uint32_t)__builtin_amdgcn_readlane((int)end, kLanes - 1);
+    }
+    return s;
+}
+
+// Group g's rows and first block, for kernels whose grid is indexed by group.
+__device__ __forceinline__ Span find_group(const int32_t *offsets, uint32_t groups, uint32_t rows, uint32_t g) {
+    Span s = {g, 0, rows, 0, 0, true};
+    if (!offsets) return s;
+    const uint32_t lane = lane_id();
+    uint32_t blocks_before = 0, high = 0;
+    for (uint32_t g0 = 0; g0 <= g; g0 += kLanes) {
+        const uint32_t i = g0 + lane;
+        const bool in = i < groups;
+        const uint32_t o0 = in ? clamp_row(offsets[i], rows) : 0u;
+        const uint32_t o1 = in ? clamp_row(offsets[i + 1], rows) : 0u;
+        const uint32_t begin = max(scan_max(o0, lane), high);
+        const uint32_t end = in ? max(begin, o1) : begin;
+        const uint32_t blocks = (end - begin + kBlock - 1) / kBlock;
+        const uint32_t bsum = scan_sum(blocks, lane);
+        if (g < g0 + kLanes) {
+            const int l = (int)(g - g0);
+            s.begin = (uint32_t)__builtin_amdgcn_readlane((int)begin, l);
+            s.end = (uint32_t)__builtin_amdgcn_readlane((int)end, l);
+            s.blocks0 = blocks_before + (uint32_t)__builtin_amdgcn_readlane((int)(bsum - blocks), l);
+        }
+        blocks_before += (uint32_t)__builtin_amdgcn_readlane((int)bsum, kLanes - 1);
+        high = (uint32_t)__builtin_amdgcn_readlane((int)end, kLanes - 1);
+    }
+    return s;
+}
+
+}  // namespace moe
+}  // namespace zc
