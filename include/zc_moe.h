@@ -239,7 +239,8 @@ uint64_t zc_fp8_matmul_workspace_bytes(uint64_t m, uint64_t n, uint64_t k, uint3
  *      workspace smaller than zc_fp8_matmul_workspace_bytes is not used.
  *   sum_mode  ZC_FP8_SUM_FAST or ZC_FP8_SUM_FULL (products bound by reading the
  *      weights are summed in full in either mode)
- * a_type and b_type are each e4m3 or e5m2; k = 0 gives zeros. */
+ * a_type and b_type are each e4m3 or e5m2; k = 0 gives zeros; k is at most
+ * 2^24. */
 zc_status zc_fp8_matmul(const void *d_a, const uint8_t *d_a_scales, uint32_t a_type, uint64_t m, const void *d_b,
                         const uint8_t *d_b_scales, uint32_t b_type, uint64_t n, uint64_t k, uint32_t groups,
                         const int32_t *d_offsets, void *d_out, uint32_t out_type, uint64_t out_stride,
@@ -248,7 +249,7 @@ zc_status zc_fp8_matmul(const void *d_a, const uint8_t *d_a_scales, uint32_t a_t
 /* Weight gradients, one n x k matrix per group, contracted over the group's
  * rows: d_out[g, i, j] = sum over the rows r of group g of A[i, r] * B[j, r].
  *   A, B  n and k rows of padded_rows bytes from zc_fp8_quantize_t with the
- *         same rows, groups and d_offsets
+ *         same rows, groups and d_offsets (padded_rows at most 2^24)
  *   d_out groups x n x k values of out_type, contiguous; zeros for a group
  *         without rows */
 zc_status zc_fp8_matmul_wgrad(const void *d_a, const uint8_t *d_a_scales, uint32_t a_type, uint64_t n,

@@ -23,10 +23,10 @@ struct MatArgs {
     uint64_t ldo, out_group;             // elements
     uint32_t m, n, rows, blocks, groups;  // blocks of 128 along the contraction (forward); rows split into groups
     uint32_t b_shift;                    // rows of B that share a row of scales, as a shift
+    uint32_t out_bf16;
 };
 
 constexpr uint32_t kMThreads = 256;
-constexpr uint32_t kSimpleTile = 128;
 
 // sum_mode FULL: 32 8-bit values of a lane, times their scale, as BF16: exact,
 // since a BF16 has the exponents of a float and more digits than any 8-bit type.
@@ -53,150 +53,339 @@ __device__ __forceinline__ void widen(const i32v8 &w, uint32_t scale, bf16v8 (&o
         }
 }
 
+__device__ __forceinline__ i32v8 join(const u32v4 (&h)[2]) {
+    return __builtin_bit_cast(i32v8, __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
 template <int FA, int FB>
 __device__ __forceinline__ f32v16 mfma(const i32v8 &a, const i32v8 &b, const f32v16 &c, uint32_t sa, uint32_t sb) {
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, FA, FB, 0, (int)sa, 0, (int)sb);
 }
 
-// 128 x 128 tile, four waves of 64 x 64, one block of 128 along the contraction
-// at a time through LDS.
-template <bool WGRAD, int FA, int FB, bool OUT_BF16, bool FULL>
-__global__ __launch_bounds__(kMThreads) void simple_kernel(MatArgs p) {
-    __shared__ alignas(16) uint8_t sa[kSimpleTile][kBlock + 16];
-    __shared__ alignas(16) uint8_t sb[kSimpleTile][kBlock + 16];
-    const uint32_t tid = threadIdx.x, lane = lane_id(), wave = tid / kLanes;
-    const uint32_t wm = (wave & 1) * 64, wn = (wave >> 1) * 64;
-    const uint32_t ntiles = (p.n + kSimpleTile - 1) / kSimpleTile;
-    const uint32_t nt = blockIdx.x % ntiles, mt = blockIdx.x / ntiles;
-    Span sp;
+// ---------------------------------------------------------------------------
+// tiles: four waves, direct-to-LDS loads four stages deep
+// ---------------------------------------------------------------------------
+
+typedef __attribute__((address_space(3))) void lds_void;
+typedef uint32_t u32v4a4 __attribute__((ext_vector_type(4), aligned(4)));
+
+// A wave's loads straight into LDS (16 or 4 bytes a lane, the lanes' results one
+// after another from the wave-uniform address in M0), from a uniform base and a
+// 32-bit offset a lane.  Inline assembly, so that the compiler adds no waits of
+// its own: the kernel counts them.
+__device__ __forceinline__ void lds_load16(const uint8_t *base, uint32_t offset, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(offset), "s"(base)
+                 : "memory");
+}
+__device__ __forceinline__ void lds_load4(const uint8_t *base, uint32_t offset, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(offset), "s"(base)
+                 : "memory");
+}
+template <int VM>
+__device__ __forceinline__ void wait_and_meet() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(VM) : "memory");
+}
+
+constexpr uint32_t kStageBytes = 64;  // of every row: one 32x32x64 instruction's contraction
+constexpr uint32_t kStages = 4;
+
+// Where a row's 16-byte chunk c of a stage sits among its four: eight rows with
+// the same c fall into different 16-byte columns of 128 bytes, and sixteen into
+// different ones of 256, so that the fragments' reads meet no bank twice.
+__device__ __forceinline__ uint32_t swizzle(uint32_t row) {
+    const uint32_t p = (row >> 1) & 7u;
+    return (p & 3u) ^ (p >> 2);
+}
+
+template <uint32_t BM, uint32_t BN>
+struct TileShared {
+    uint8_t stage[kStages][(BM + BN) * kStageBytes];
+    uint32_t scale[2][BM + BN];  // four blocks' scale bytes of every row
+};
+
+// BM x BN tile of four waves (2 x 2).  A stage is 64 bytes of every row.  While
+// the matrix instructions work on one stage from registers, the next one's
+// fragments come out of LDS, the three after it are on their way into LDS, and
+// one barrier a stage frees the buffer of the stage just read.
+template <uint32_t BM, uint32_t BN, bool WGRAD, int FA, int FB, bool FULL>
+__global__ __launch_bounds__(kMThreads, (BM >= 256 ? 1 : 2)) void tile_kernel(MatArgs p) {
+    constexpr uint32_t MT = BM / 64, NT = BN / 64;         // 32 x 32 tiles of a wave
+    constexpr uint32_t LA = BM / 64, LB = BN / 64;         // 16-byte loads of a wave and stage
+    constexpr uint32_t LOADS = LA + LB;
+    __shared__ alignas(1024) TileShared<BM, BN> sh;
+    const uint32_t lane = lane_id(), wave = (uint32_t)__builtin_amdgcn_readfirstlane(threadIdx.x / kLanes);
+    const uint32_t ntiles = (p.n + BN - 1) / BN;
+    const uint32_t mtiles = WGRAD ? (p.m + BM - 1) / BM * p.groups : count_tiles(p.offsets, p.groups, p.rows, BM);
+
+    // Consecutive workgroups go to the eight XCDs in turn: each XCD gets a run of
+    // consecutive tiles, in bands of eight rows of tiles walked column by column,
+    // so that the tiles in flight on it share rows of A and B in its L2.
+    const uint32_t total = mtiles * ntiles, xcd = blockIdx.x % 8, local = blockIdx.x / 8;
+    const uint32_t per = total / 8, rest = total % 8;
+    if (local >= per + (xcd < rest)) return;
+    const uint32_t id = xcd * per + min(xcd, rest) + local;
+    const uint32_t band = id / (8 * ntiles), in_band = id % (8 * ntiles);
+    const uint32_t band_rows = min(8u, mtiles - 8 * band);
+    const uint32_t mt = 8 * band + in_band % band_rows, nt = in_band / band_rows;
+
     uint32_t m0, m1, kb0, kb1;
     const uint8_t *b = p.b, *bs = p.bs;
     uint64_t out0 = 0;
     if (WGRAD) {
-        const uint32_t mtiles = (p.m + kSimpleTile - 1) / kSimpleTile;
-        sp = find_group(p.offsets, p.groups, p.rows, mt / mtiles);
-        m0 = (mt % mtiles) * kSimpleTile;
+        const uint32_t per_group = (p.m + BM - 1) / BM;
+        const Span sp = find_group(p.offsets, p.groups, p.rows, mt / per_group);
+        m0 = (mt % per_group) * BM;
         m1 = p.m;
         kb0 = sp.blocks0;
         kb1 = kb0 + (sp.end - sp.begin + kBlock - 1) / kBlock;
         out0 = (uint64_t)sp.group * p.out_group;
     } else {
-        sp = find_tile(p.offsets, p.groups, p.rows, kSimpleTile, mt);
+        const Span sp = find_tile(p.offsets, p.groups, p.rows, BM, mt);
         if (!sp.found) return;
-        m0 = sp.begin + sp.tile * kSimpleTile;
+        m0 = sp.begin + sp.tile * BM;
         m1 = sp.end;
         kb0 = 0;
         kb1 = p.blocks;
         b += sp.group * p.b_group;
         bs += sp.group * p.bs_group;
     }
-    const uint32_t n0 = nt * kSimpleTile;
-    f32v16 acc[2][2];
+    const uint32_t n0 = nt * BN;
+    const uint32_t stages = 2 * (kb1 - kb0);
+
+    f32v16 acc[MT][NT];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (uint32_t i = 0; i < MT; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (uint32_t j = 0; j < NT; ++j)
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
-    for (uint32_t kb = kb0; kb < kb1; ++kb) {
-        __syncthreads();
+
+    const uint32_t wm = (wave & 1) * (BM / 2), wn = (wave >> 1) * (BN / 2);
+    if (stages) {
+        // where the lane's loads start: row lane / 4 of 16, and the chunk that its place in LDS holds; rows past the
+        // end repeat the last one (their results are not stored)
+        const uint32_t chunk = 16 * ((lane & 3u) ^ swizzle(lane / 4));
+        const uint8_t *ga = p.a + (uint64_t)m0 * p.lda + (uint64_t)kb0 * kBlock;
+        const uint8_t *gb = b + (uint64_t)n0 * p.ldb + (uint64_t)kb0 * kBlock;
+        uint32_t offa[LA], offb[LB];
 #pragma unroll
-        for (uint32_t i = 0; i < 4; ++i) {
-            const uint32_t r = i * 32 + tid / 8, c = (tid % 8) * 16;
-            const uint32_t ra = min(m0 + r, m1 - 1), rb = min(n0 + r, p.n - 1);
-            *reinterpret_cast<u32v4 *>(&sa[r][c]) =
-                *reinterpret_cast<const u32v4 *>(p.a + (uint64_t)ra * p.lda + (uint64_t)kb * kBlock + c);
-            *reinterpret_cast<u32v4 *>(&sb[r][c]) =
-                *reinterpret_cast<const u32v4 *>(b + (uint64_t)rb * p.ldb + (uint64_t)kb * kBlock + c);
+        for (uint32_t i = 0; i < LA; ++i)
+            offa[i] = min(wave * (BM / 4) + 16 * i + lane / 4, m1 - 1 - m0) * (uint32_t)p.lda + chunk;
+#pragma unroll
+        for (uint32_t i = 0; i < LB; ++i)
+            offb[i] = min(wave * (BN / 4) + 16 * i + lane / 4, p.n - 1 - n0) * (uint32_t)p.ldb + chunk;
+        const uint32_t lds0 = (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void *)&sh.stage[0][0]);
+        const uint32_t ldsa = lds0 + wave * (BM / 4) * kStageBytes;
+        const uint32_t ldsb = lds0 + BM * kStageBytes + wave * (BN / 4) * kStageBytes;
+        constexpr uint32_t kStageStep = (BM + BN) * kStageBytes;
+
+        // scales: four blocks of a row are a dword; rows of the wave: BM / 4 of A, BN / 4 of B, one a lane
+        const uint8_t *sa0 = p.as + (uint64_t)m0 * p.ldas;
+        const uint8_t *sb0 = bs + (uint64_t)(n0 >> p.b_shift) * p.ldbs;
+        const uint32_t sra = wave * (BM / 4) + min(lane, BM / 4 - 1), srb = wave * (BN / 4) + min(lane, BN / 4 - 1);
+        const uint32_t soffa = min(sra, m1 - 1 - m0) * (uint32_t)p.ldas;
+        const uint32_t soffb = ((min(n0 + srb, p.n - 1) >> p.b_shift) - (n0 >> p.b_shift)) * (uint32_t)p.ldbs;
+        const uint32_t ldss = (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void *)&sh.scale[0][0]);
+        const auto load_scales = [&](uint32_t c) {  // blocks 4c .. 4c + 3
+            const uint32_t at = ldss + (c & 1) * (BM + BN) * 4;
+            if (lane < BM / 4) lds_load4(sa0 + 4 * c, soffa, at + wave * BM);
+            if (lane < BN / 4) lds_load4(sb0 + 4 * c, soffb, at + 4 * BM + wave * BN);
+        };
+        const auto load_piece = [&](uint32_t s, uint32_t i) {  // the wave's i-th load of stage s
+            const uint32_t at = (s & (kStages - 1)) * kStageStep;
+            if (i < LA)
+                lds_load16(ga + (uint64_t)s * kStageBytes, offa[i % LA], ldsa + at + i * 1024);
+            else
+                lds_load16(gb + (uint64_t)s * kStageBytes, offb[(i - LA) % LB], ldsb + at + (i - LA) * 1024);
+        };
+
+        // fragments: lane l holds row l mod 32, chunks l / 32 and l / 32 + 2 (the order along the contraction does not
+        // matter as long as A and B agree)
+        const uint32_t fr = lane % 32, fc = lane / 32, sw = swizzle(fr);
+        const uint32_t ra0 = (wm + fr) * kStageBytes, rb0 = (BM + wn + fr) * kStageBytes;
+        const uint32_t c0 = 16 * (fc ^ sw), c1 = 16 * ((fc + 2) ^ sw);
+        u32v4 fa[2][MT][2], fb[2][NT][2];
+        uint32_t ea[MT], eb[NT];
+        const auto read_a = [&](uint32_t s, uint32_t i, uint32_t h) -> u32v4 {
+            return *reinterpret_cast<const u32v4 *>(&sh.stage[s & (kStages - 1)][ra0 + 32 * i * kStageBytes + (h ? c1 : c0)]);
+        };
+        const auto read_b = [&](uint32_t s, uint32_t j, uint32_t h) -> u32v4 {
+            return *reinterpret_cast<const u32v4 *>(&sh.stage[s & (kStages - 1)][rb0 + 32 * j * kStageBytes + (h ? c1 : c0)]);
+        };
+        const auto read_scales = [&](uint32_t c) {
+#pragma unroll
+            for (uint32_t i = 0; i < MT; ++i) ea[i] = sh.scale[c & 1][wm + 32 * i + fr];
+#pragma unroll
+            for (uint32_t j = 0; j < NT; ++j) eb[j] = sh.scale[c & 1][BM + wn + 32 * j + fr];
+        };
+
+        const uint32_t chunk0 = kb0 / 4, chunk_last = (kb1 - 1) / 4;
+        load_scales(chunk0);
+        if (chunk0 < chunk_last) load_scales(chunk0 + 1);
+#pragma unroll
+        for (uint32_t s = 0; s < kStages; ++s)
+            if (s < stages)
+#pragma unroll
+                for (uint32_t i = 0; i < LOADS; ++i) load_piece(s, i);
+        if (stages >= kStages)
+            wait_and_meet<(int)((kStages - 1) * LOADS)>();
+        else
+            wait_and_meet<0>();
+        read_scales(chunk0);
+#pragma unroll
+        for (uint32_t i = 0; i < MT; ++i) ea[i] >>= 8 * (kb0 & 3);
+#pragma unroll
+        for (uint32_t j = 0; j < NT; ++j) eb[j] >>= 8 * (kb0 & 3);
+#pragma unroll
+        for (uint32_t h = 0; h < 2; ++h) {
+#pragma unroll
+            for (uint32_t i = 0; i < MT; ++i) fa[0][i][h] = read_a(0, i, h);
+#pragma unroll
+            for (uint32_t j = 0; j < NT; ++j) fb[0][j][h] = read_b(0, j, h);
         }
-        __syncthreads();
-        uint32_t ea[2], eb[2];
+
+        for (uint32_t s0 = 0; s0 < stages; s0 += 2) {
 #pragma unroll
-        for (uint32_t i = 0; i < 2; ++i) {
-            const uint32_t ra = min(m0 + wm + 32 * i + lane % 32, m1 - 1);
-            const uint32_t rb = min(n0 + wn + 32 * i + lane % 32, p.n - 1);
-            ea[i] = p.as[(uint64_t)ra * p.ldas + kb];
-            eb[i] = bs[(uint64_t)(rb >> p.b_shift) * p.ldbs + kb];
-        }
+            for (uint32_t half = 0; half < 2; ++half) {
+                const uint32_t s = s0 + half;
+                // stage s + 1 has landed (two younger stages may be on their way), and every wave holds stage s
+                if (s + kStages - 1 < stages)
+                    wait_and_meet<(int)((kStages - 2) * LOADS)>();
+                else
+                    wait_and_meet<0>();
+                const bool more = s + kStages < stages;
+                const uint32_t cur = half, nxt = half ^ 1;
+                const uint32_t kb = kb0 + s0 / 2;
+                if (half == 0 && (kb & 3) == 0 && kb / 4 > chunk0 && kb / 4 < chunk_last) load_scales(kb / 4 + 1);
+                const auto piece = [&](uint32_t slot) {  // what goes between the matrix instructions
+                    if (slot < 2 * MT)
+                        fa[nxt][slot / 2 % MT][slot & 1] = read_a(s + 1, slot / 2 % MT, slot & 1);
+                    else if (slot < 2 * (MT + NT))
+                        fb[nxt][(slot / 2 - MT) % NT][slot & 1] = read_b(s + 1, (slot / 2 - MT) % NT, slot & 1);
+                };
+                bf16v8 wb[FULL ? NT : 1][4];
+                if (FULL)
 #pragma unroll
-        for (uint32_t half = 0; half < 2; ++half) {
-            i32v8 fa[2], fb[2];
+                    for (uint32_t j = 0; j < NT; ++j) widen<FB>(join(fb[cur][j]), eb[j] & 0xFFu, wb[j % (FULL ? NT : 1)]);
 #pragma unroll
-            for (uint32_t i = 0; i < 2; ++i) {
-                fa[i] = *reinterpret_cast<const i32v8 *>(&sa[wm + 32 * i + lane % 32][half * 64 + (lane / 32) * 32]);
-                fb[i] = *reinterpret_cast<const i32v8 *>(&sb[wn + 32 * i + lane % 32][half * 64 + (lane / 32) * 32]);
-            }
-            // B in the place of the left matrix: a lane then holds four consecutive columns of one row
-            if (FULL) {
-                bf16v8 wa[2][4], wb[2][4];
+                for (uint32_t i = 0; i < MT; ++i) {
+                    bf16v8 wa[4];
+                    if (FULL) widen<FA>(join(fa[cur][i]), ea[i] & 0xFFu, wa);
 #pragma unroll
-                for (uint32_t i = 0; i < 2; ++i) {
-                    widen<FA>(fa[i], ea[i], wa[i]);
-                    widen<FB>(fb[i], eb[i], wb[i]);
+                    for (uint32_t j = 0; j < NT; ++j) {
+                        if (FULL) {
+#pragma unroll
+                            for (uint32_t q = 0; q < 4; ++q)
+                                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wb[j % (FULL ? NT : 1)][q], wa[q],
+                                                                                   acc[i][j], 0, 0, 0);
+                        } else {
+                            // B in the place of the left matrix: a lane then holds four consecutive columns of one row
+                            acc[i][j] = mfma<FB, FA>(join(fb[cur][j]), join(fa[cur][i]), acc[i][j], eb[j], ea[i]);
+                        }
+                        constexpr uint32_t kSlots = MT * NT, kPieces = 2 * (MT + NT);
+                        const uint32_t slot = i * NT + j;
+#pragma unroll
+                        for (uint32_t q = slot * kPieces / kSlots; q < (slot + 1) * kPieces / kSlots; ++q) piece(q);
+#pragma unroll
+                        for (uint32_t q = slot * LOADS / kSlots; q < (slot + 1) * LOADS / kSlots; ++q)
+                            if (more) load_piece(s + kStages, q);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
                 }
+                if (half == 1) {  // the next block's scales
+                    if (((kb + 1) & 3) == 0 && kb + 1 < kb1) {
+                        read_scales((kb + 1) / 4);
+                    } else {
 #pragma unroll
-                for (uint32_t i = 0; i < 2; ++i)
+                        for (uint32_t i = 0; i < MT; ++i) ea[i] >>= 8;
 #pragma unroll
-                    for (uint32_t j = 0; j < 2; ++j)
-#pragma unroll
-                        for (uint32_t q = 0; q < 4; ++q)
-                            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wb[j][q], wa[i][q], acc[i][j], 0, 0, 0);
-            } else {
-#pragma unroll
-                for (uint32_t i = 0; i < 2; ++i)
-#pragma unroll
-                    for (uint32_t j = 0; j < 2; ++j) acc[i][j] = mfma<FB, FA>(fb[j], fa[i], acc[i][j], eb[j], ea[i]);
+                        for (uint32_t j = 0; j < NT; ++j) eb[j] >>= 8;
+                    }
+                }
             }
         }
     }
-#pragma unroll
-    for (uint32_t i = 0; i < 2; ++i)
-#pragma unroll
-        for (uint32_t j = 0; j < 2; ++j)
-#pragma unroll
-            for (uint32_t e = 0; e < 16; ++e) {
-                const uint32_t r = m0 + wm + 32 * i + lane % 32;
-                const uint32_t c = n0 + wn + 32 * j + 8 * (e / 4) + 4 * (lane / 32) + e % 4;
-                if (r < m1 && c < p.n) {
-                    const uint64_t o = out0 + (uint64_t)r * p.ldo + c;
-                    if (OUT_BF16)
-                        static_cast<uint16_t *>(p.out)[o] = bf_round(acc[i][j][e]);
-                    else
-                        static_cast<float *>(p.out)[o] = acc[i][j][e];
-                }
-            }
-}
 
-template <bool WGRAD, int FA, int FB, bool FULL>
-static void launch_out(const MatArgs &p, bool bf16, uint32_t grid, hipStream_t st) {
-    if (bf16)
-        hipLaunchKernelGGL((simple_kernel<WGRAD, FA, FB, true, FULL>), dim3(grid), dim3(kMThreads), 0, st, p);
-    else
-        hipLaunchKernelGGL((simple_kernel<WGRAD, FA, FB, false, FULL>), dim3(grid), dim3(kMThreads), 0, st, p);
+    // Results through LDS, 32 rows of a wave at a time, so that a row's BN / 2
+    // columns leave as whole lines.
+    wait_and_meet<0>();
+    constexpr uint32_t kRowBytes = BN / 2 * 4 + 16;
+    static_assert(sizeof(sh.stage) >= 4 * 32 * kRowBytes, "room for 32 rows of every wave");
+    uint8_t *mine = &sh.stage[0][0] + wave * 32 * kRowBytes;
+    const bool bf16 = p.out_bf16 != 0;
+    const uint32_t es = bf16 ? 2 : 4;
+    const bool fast = (p.ldo * es) % 4 == 0 && (out0 * es) % 4 == 0;  // the base is aligned to its element, 4 checked below
+    const bool fast_out = fast && (reinterpret_cast<uintptr_t>(p.out) & 3) == 0;
+#pragma unroll
+    for (uint32_t i = 0; i < MT; ++i) {
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+        for (uint32_t j = 0; j < NT; ++j)
+#pragma unroll
+            for (uint32_t e = 0; e < 16; e += 4) {
+                const uint32_t c = 32 * j + 2 * e + 4 * (lane / 32);
+                uint8_t *w = mine + (lane % 32) * kRowBytes + c * es;
+                if (bf16)
+                    *reinterpret_cast<u32v2 *>(w) =
+                        u32v2{bf_pack(acc[i][j][e], acc[i][j][e + 1]), bf_pack(acc[i][j][e + 2], acc[i][j][e + 3])};
+                else
+                    *reinterpret_cast<u32v4 *>(w) =
+                        u32v4{__float_as_uint(acc[i][j][e]), __float_as_uint(acc[i][j][e + 1]),
+                              __float_as_uint(acc[i][j][e + 2]), __float_as_uint(acc[i][j][e + 3])};
+            }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        const uint32_t row_chunks = BN / 2 * es / 16, per_chunk = 16 / es;
+        for (uint32_t q = lane; q < 32 * row_chunks; q += kLanes) {
+            const uint32_t rr = q / row_chunks, cc = q % row_chunks;
+            const uint32_t r = m0 + wm + 32 * i + rr, c = n0 + wn + cc * per_chunk;
+            if (r >= m1 || c >= p.n) continue;
+            const u32v4 v = *reinterpret_cast<const u32v4 *>(mine + rr * kRowBytes + cc * 16);
+            const uint64_t o = out0 + (uint64_t)r * p.ldo + c;
+            if (fast_out && c + per_chunk <= p.n) {
+                *reinterpret_cast<u32v4a4 *>(static_cast<uint8_t *>(p.out) + o * es) = v;
+            } else if (bf16) {
+                for (uint32_t k = 0; k < 8 && c + k < p.n; ++k)
+                    static_cast<uint16_t *>(p.out)[o + k] = (uint16_t)(v[k / 2] >> (16 * (k & 1)));
+            } else {
+                for (uint32_t k = 0; k < 4 && c + k < p.n; ++k) static_cast<uint32_t *>(p.out)[o + k] = v[k];
+            }
+        }
+    }
 }
 
 template <bool WGRAD, int FA, int FB>
-static void launch_sum(const MatArgs &p, bool bf16, bool full, uint32_t grid, hipStream_t st) {
+static void launch_tile(const MatArgs &p, bool full, bool large, uint32_t grid, hipStream_t st) {
     if (full)
-        launch_out<WGRAD, FA, FB, true>(p, bf16, grid, st);
+        hipLaunchKernelGGL((tile_kernel<128, 128, WGRAD, FA, FB, true>), dim3(grid), dim3(kMThreads), 0, st, p);
+    else if (large)
+        hipLaunchKernelGGL((tile_kernel<256, 256, WGRAD, FA, FB, false>), dim3(grid), dim3(kMThreads), 0, st, p);
     else
-        launch_out<WGRAD, FA, FB, false>(p, bf16, grid, st);
+        hipLaunchKernelGGL((tile_kernel<128, 128, WGRAD, FA, FB, false>), dim3(grid), dim3(kMThreads), 0, st, p);
 }
 
 template <bool WGRAD>
-static zc_status launch(const MatArgs &p, uint32_t ta, uint32_t tb, bool bf16, bool full, hipStream_t st) {
-    const uint64_t ntiles = ceil_div(p.n, kSimpleTile);
-    const uint64_t mtiles = WGRAD ? ceil_div(p.m, kSimpleTile) * p.groups
-                                  : p.rows / kSimpleTile + (p.rows < p.groups ? p.rows : p.groups);
-    if (ntiles * mtiles > 0xFFFFFFu) return ZC_ERR_INVALID_ARG;
-    const uint32_t grid = (uint32_t)(ntiles * mtiles);
+static uint64_t tiles_of(const MatArgs &p, uint32_t tile) {
+    const uint64_t mtiles = WGRAD ? ceil_div(p.m, tile) * p.groups : p.rows / tile + (p.rows < p.groups ? p.rows : p.groups);
+    return ceil_div(p.n, tile) * mtiles;
+}
+
+template <bool WGRAD>
+static zc_status launch(MatArgs p, uint32_t ta, uint32_t tb, bool bf16, bool full, hipStream_t st) {
+    p.out_bf16 = bf16;
+    const bool large = !full && tiles_of<WGRAD>(p, 256) >= 192;
+    const uint64_t tiles = tiles_of<WGRAD>(p, large ? 256 : 128);
+    if (tiles > 0xFFFFF0u) return ZC_ERR_INVALID_ARG;
+    const uint32_t grid = (uint32_t)ceil_div(tiles, 8) * 8;
     const int fa = ta == ZC_FP8_E5M2, fb = tb == ZC_FP8_E5M2;
-    if (!fa && !fb) launch_sum<WGRAD, 0, 0>(p, bf16, full, grid, st);
-    if (!fa && fb) launch_sum<WGRAD, 0, 1>(p, bf16, full, grid, st);
-    if (fa && !fb) launch_sum<WGRAD, 1, 0>(p, bf16, full, grid, st);
-    if (fa && fb) launch_sum<WGRAD, 1, 1>(p, bf16, full, grid, st);
+    if (!fa && !fb) launch_tile<WGRAD, 0, 0>(p, full, large, grid, st);
+    if (!fa && fb) launch_tile<WGRAD, 0, 1>(p, full, large, grid, st);
+    if (fa && !fb) launch_tile<WGRAD, 1, 0>(p, full, large, grid, st);
+    if (fa && fb) launch_tile<WGRAD, 1, 1>(p, full, large, grid, st);
     return launched();
 }
+
+// A tile's rows are reached by 32-bit offsets from its first: 256 rows of at most 2^24 bytes.
+constexpr uint64_t kMaxContraction = 1ull << 24;
 
 static bool types_ok(uint32_t ta, uint32_t tb, uint32_t to, uint32_t sum) {
     return is_fp8(ta) && is_fp8(tb) && (to == ZC_F32 || to == ZC_BF16) && sum <= ZC_FP8_SUM_FULL;
@@ -221,7 +410,7 @@ extern "C" zc_status zc_fp8_matmul(const void *d_a, const uint8_t *d_a_scales, u
                                    uint32_t out_type, uint64_t out_stride, uint32_t sum_mode,
                                    void *d_workspace, uint64_t workspace_bytes, void *stream) {
     (void)workspace_bytes;
-    if (!types_ok(a_type, b_type, out_type, sum_mode) || m > kMaxRows || n > kMaxCols || k > kMaxCols || groups == 0 ||
+    if (!types_ok(a_type, b_type, out_type, sum_mode) || m > kMaxRows || n > kMaxCols || k > kMaxContraction || groups == 0 ||
         groups > ZC_MAX_EXPERTS || (!d_offsets && groups != 1) || out_stride < n || out_stride > kMaxStride)
         return ZC_ERR_INVALID_ARG;
     if (!m || !n) return ZC_OK;
@@ -257,7 +446,7 @@ extern "C" zc_status zc_fp8_matmul_wgrad(const void *d_a, const uint8_t *d_a_sca
                                          uint32_t sum_mode, void *stream) {
     if (!types_ok(a_type, b_type, out_type, sum_mode) || rows > kMaxRows || n > kMaxCols || k > kMaxCols || groups == 0 ||
         groups > ZC_MAX_EXPERTS || (!d_offsets && groups != 1) || padded_rows % kBlock ||
-        padded_rows > kMaxRows + ZC_MOE_ROW_SLACK)
+        padded_rows > kMaxContraction)
         return ZC_ERR_INVALID_ARG;
     if (padded_rows < zc_fp8_padded_rows(rows, groups)) return ZC_ERR_CAPACITY;
     if (!n || !k) return ZC_OK;

@@ -203,6 +203,26 @@ __device__ __forceinline__ Span find_tile(const int32_t *offsets, uint32_t group
     return s;
 }
 
+// Tiles of `tile_rows` rows over all groups.
+__device__ __forceinline__ uint32_t count_tiles(const int32_t *offsets, uint32_t groups, uint32_t rows,
+                                                uint32_t tile_rows) {
+    if (!offsets) return (rows + tile_rows - 1) / tile_rows;
+    const uint32_t lane = lane_id();
+    uint32_t total = 0, high = 0;
+    for (uint32_t g0 = 0; g0 < groups; g0 += kLanes) {
+        const uint32_t g = g0 + lane;
+        const bool in = g < groups;
+        const uint32_t o0 = in ? clamp_row(offsets[g], rows) : 0u;
+        const uint32_t o1 = in ? clamp_row(offsets[g + 1], rows) : 0u;
+        const uint32_t begin = max(scan_max(o0, lane), high);
+        const uint32_t end = in ? max(begin, o1) : begin;
+        const uint32_t sum = scan_sum((end - begin + tile_rows - 1) / tile_rows, lane);
+        total += (uint32_t)__builtin_amdgcn_readlane((int)sum, kLanes - 1);
+        high = (uint32_t)__builtin_amdgcn_readlane((int)end, kLanes - 1);
+    }
+    return total;
+}
+
 // Group g's rows and first block, for kernels whose grid is indexed by group.
 __device__ __forceinline__ Span find_group(const int32_t *offsets, uint32_t groups, uint32_t rows, uint32_t g) {
     Span s = {g, 0, rows, 0, 0, true};
