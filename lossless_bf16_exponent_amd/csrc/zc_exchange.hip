@@ -67,7 +67,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_place_kernel(PlanArgs a) {
     const uint32_t per = (nb + kPlanThreads - 1) / kPlanThreads, e0 = tid * per, e1 = min(e0 + per, nb);
     uint32_t mine = 0;
     for (uint32_t e = e0; e < e1; ++e) mine += total[e];
-    const uint32_t incl = scan_sum(mine, lane);
+    const uint32_t incl = scan_sum(mine);
     if (lane == kLanes - 1) part[wave] = incl;
     __syncthreads();
     uint32_t run = incl - mine;

@@ -130,7 +130,7 @@ __global__ __launch_bounds__(kQThreads) void quantize_t_kernel(TransArgs a) {
     __shared__ uint32_t part[4][kTCols];
     const uint32_t tid = threadIdx.x;
     const uint32_t ct = blockIdx.x % a.col_tiles, t = blockIdx.x / a.col_tiles;
-    const Span sp = find_tile(a.offsets, a.groups, a.rows, kBlock, t);
+    const Span sp = find_tile(a.offsets, a.groups, a.rows, kBlock, [&](uint32_t) { return t; });
     if (!sp.found) return;
     const uint32_t row0 = sp.begin + sp.tile * kBlock, c0 = ct * kTCols;
     const uint32_t rows = min(sp.end - row0, kBlock);

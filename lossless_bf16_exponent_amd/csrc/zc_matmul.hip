@@ -4,6 +4,8 @@
 //   gradient  out[g, i, j] = sum over the rows r of group g of A[i, r] B[j, r]
 // The scaled matrix instructions apply the scales: 2^(a - 127) 2^(b - 127) for
 // every lane's 32 values, in the 32-bit sum, at no cost of their own.
+#include <type_traits>
+
 #include "zc_moe_device.h"
 
 namespace zc {
@@ -23,7 +25,6 @@ struct MatArgs {
     uint64_t ldo, out_group;             // elements
     uint32_t m, n, rows, blocks, groups;  // blocks of 128 along the contraction (forward); rows split into groups
     uint32_t b_shift;                    // rows of B that share a row of scales, as a shift
-    uint32_t out_bf16;
 };
 
 constexpr uint32_t kMThreads = 256;
@@ -86,53 +87,58 @@ __device__ __forceinline__ void wait_and_meet() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(VM) : "memory");
 }
 
-constexpr uint32_t kStageBytes = 64;  // of every row: one 32x32x64 instruction's contraction
-constexpr uint32_t kStages = 4;
-
-// Where a row's 16-byte chunk c of a stage sits among its four: eight rows with
-// the same c fall into different 16-byte columns of 128 bytes, and sixteen into
-// different ones of 256, so that the fragments' reads meet no bank twice.
-__device__ __forceinline__ uint32_t swizzle(uint32_t row) {
-    const uint32_t p = (row >> 1) & 7u;
-    return (p & 3u) ^ (p >> 2);
-}
+// A stage is one block of 128 along the contraction: 128 bytes of every row, a
+// whole cache line each.  (Stages of 64 bytes, four deep, asked the L2 for twice
+// as many half lines and took 1.3 times as long.)
+constexpr uint32_t kStages = 2;
 
 template <uint32_t BM, uint32_t BN>
 struct TileShared {
-    uint8_t stage[kStages][(BM + BN) * kStageBytes];
+    uint8_t stage[kStages][(BM + BN) * kBlock];
     uint32_t scale[2][BM + BN];  // four blocks' scale bytes of every row
 };
 
-// BM x BN tile of four waves (2 x 2).  A stage is 64 bytes of every row.  While
-// the matrix instructions work on one stage from registers, the next one's
-// fragments come out of LDS, the three after it are on their way into LDS, and
-// one barrier a stage frees the buffer of the stage just read.
-template <uint32_t BM, uint32_t BN, bool WGRAD, int FA, int FB, bool FULL>
+// BM x BN tile of four waves (2 x 2).  The fragments of half a block are in
+// registers while the other half's come out of LDS.  In the middle of a block
+// every wave holds the rest of it, and one barrier then frees its buffer for the
+// block after the next and hands over the next one.  T: uint16_t for BF16 results, uint32_t for
+// floats.
+template <uint32_t BM, uint32_t BN, bool WGRAD, int FA, int FB, bool FULL, typename T>
 __global__ __launch_bounds__(kMThreads, (BM >= 256 ? 1 : 2)) void tile_kernel(MatArgs p) {
     constexpr uint32_t MT = BM / 64, NT = BN / 64;         // 32 x 32 tiles of a wave
-    constexpr uint32_t LA = BM / 64, LB = BN / 64;         // 16-byte loads of a wave and stage
+    constexpr uint32_t LA = BM / 32, LB = BN / 32;         // 16-byte loads of a wave and block, 8 rows each
     constexpr uint32_t LOADS = LA + LB;
     __shared__ alignas(1024) TileShared<BM, BN> sh;
     const uint32_t lane = lane_id(), wave = (uint32_t)__builtin_amdgcn_readfirstlane(threadIdx.x / kLanes);
     const uint32_t ntiles = (p.n + BN - 1) / BN;
-    const uint32_t mtiles = WGRAD ? (p.m + BM - 1) / BM * p.groups : count_tiles(p.offsets, p.groups, p.rows, BM);
 
-    // Consecutive workgroups go to the eight XCDs in turn: each XCD gets a run of
-    // consecutive tiles, in bands of eight rows of tiles walked column by column,
-    // so that the tiles in flight on it share rows of A and B in its L2.
-    const uint32_t total = mtiles * ntiles, xcd = blockIdx.x % 8, local = blockIdx.x / 8;
-    const uint32_t per = total / 8, rest = total % 8;
-    if (local >= per + (xcd < rest)) return;
-    const uint32_t id = xcd * per + min(xcd, rest) + local;
-    const uint32_t band = id / (8 * ntiles), in_band = id % (8 * ntiles);
-    const uint32_t band_rows = min(8u, mtiles - 8 * band);
-    const uint32_t mt = 8 * band + in_band % band_rows, nt = in_band / band_rows;
+    // Consecutive workgroups go to the eight XCDs in turn.  The tiles are walked
+    // in bands of eight rows of tiles, column by column: 32 consecutive ones, as many
+    // as an XCD has CUs, are 8 x 4 tiles that share rows of A and B in its L2
+    // (bands of 4 or 16 took 1.05 and 1.1 times as long).  Forward, an XCD gets one
+    // run of tiles, away from the others' rows (runs of 32 in turn: 1.05 times as
+    // long); the weight gradient's tiles take longer in groups of many rows, which
+    // runs of 32 in turn spread over the XCDs (one run each: 2.1 times as long on
+    // groups between 290 and 3500 rows).
+    uint32_t nt = 0;
+    const auto pick = [&](uint32_t mtiles) -> uint32_t {
+        const uint32_t total = mtiles * ntiles, xcd = blockIdx.x % 8, local = blockIdx.x / 8;
+        const uint32_t per = total / 8, rest = total % 8;
+        const uint32_t id = WGRAD ? (local / 32 * 8 + xcd) * 32 + local % 32 : xcd * per + min(xcd, rest) + local;
+        if (id >= total || (!WGRAD && local >= per + (xcd < rest))) return ~0u;
+        const uint32_t band = id / (8 * ntiles), in_band = id % (8 * ntiles);
+        const uint32_t band_rows = min(8u, mtiles - 8 * band);
+        nt = in_band / band_rows;
+        return 8 * band + in_band % band_rows;
+    };
 
-    uint32_t m0, m1, kb0, kb1;
+    uint32_t mt, m0, m1, kb0, kb1;
     const uint8_t *b = p.b, *bs = p.bs;
     uint64_t out0 = 0;
     if (WGRAD) {
         const uint32_t per_group = (p.m + BM - 1) / BM;
+        mt = pick(per_group * p.groups);
+        if (mt == ~0u) return;
         const Span sp = find_group(p.offsets, p.groups, p.rows, mt / per_group);
         m0 = (mt % per_group) * BM;
         m1 = p.m;
@@ -140,7 +146,7 @@ __global__ __launch_bounds__(kMThreads, (BM >= 256 ? 1 : 2)) void tile_kernel(Ma
         kb1 = kb0 + (sp.end - sp.begin + kBlock - 1) / kBlock;
         out0 = (uint64_t)sp.group * p.out_group;
     } else {
-        const Span sp = find_tile(p.offsets, p.groups, p.rows, BM, mt);
+        const Span sp = find_tile(p.offsets, p.groups, p.rows, BM, [&](uint32_t total) { return mt = pick(total); });
         if (!sp.found) return;
         m0 = sp.begin + sp.tile * BM;
         m1 = sp.end;
@@ -150,7 +156,7 @@ __global__ __launch_bounds__(kMThreads, (BM >= 256 ? 1 : 2)) void tile_kernel(Ma
         bs += sp.group * p.bs_group;
     }
     const uint32_t n0 = nt * BN;
-    const uint32_t stages = 2 * (kb1 - kb0);
+    const uint32_t blocks = kb1 - kb0;
 
     f32v16 acc[MT][NT];
 #pragma unroll
@@ -161,23 +167,25 @@ __global__ __launch_bounds__(kMThreads, (BM >= 256 ? 1 : 2)) void tile_kernel(Ma
             for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
 
     const uint32_t wm = (wave & 1) * (BM / 2), wn = (wave >> 1) * (BN / 2);
-    if (stages) {
-        // where the lane's loads start: row lane / 4 of 16, and the chunk that its place in LDS holds; rows past the
-        // end repeat the last one (their results are not stored)
-        const uint32_t chunk = 16 * ((lane & 3u) ^ swizzle(lane / 4));
+    if (blocks) {
+        // where the lane's loads start: row lane / 8 of 8, and the 16-byte chunk that its place in LDS holds.  Chunk c of
+        // row r sits at c ^ (r / 2 mod 8): sixteen lanes read 256 bytes at a time, and the same chunk of sixteen rows then
+        // lies in sixteen different columns of banks (with r mod 8 every read took twice its four cycles).  Rows past
+        // the end repeat the last one (their results are not stored)
+        const uint32_t chunk = 16 * ((lane & 7u) ^ (lane / 16));
         const uint8_t *ga = p.a + (uint64_t)m0 * p.lda + (uint64_t)kb0 * kBlock;
         const uint8_t *gb = b + (uint64_t)n0 * p.ldb + (uint64_t)kb0 * kBlock;
         uint32_t offa[LA], offb[LB];
 #pragma unroll
         for (uint32_t i = 0; i < LA; ++i)
-            offa[i] = min(wave * (BM / 4) + 16 * i + lane / 4, m1 - 1 - m0) * (uint32_t)p.lda + chunk;
+            offa[i] = min(wave * (BM / 4) + 8 * i + lane / 8, m1 - 1 - m0) * (uint32_t)p.lda + (chunk ^ (64 * (i & 1)));
 #pragma unroll
         for (uint32_t i = 0; i < LB; ++i)
-            offb[i] = min(wave * (BN / 4) + 16 * i + lane / 4, p.n - 1 - n0) * (uint32_t)p.ldb + chunk;
+            offb[i] = min(wave * (BN / 4) + 8 * i + lane / 8, p.n - 1 - n0) * (uint32_t)p.ldb + (chunk ^ (64 * (i & 1)));
         const uint32_t lds0 = (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void *)&sh.stage[0][0]);
-        const uint32_t ldsa = lds0 + wave * (BM / 4) * kStageBytes;
-        const uint32_t ldsb = lds0 + BM * kStageBytes + wave * (BN / 4) * kStageBytes;
-        constexpr uint32_t kStageStep = (BM + BN) * kStageBytes;
+        const uint32_t ldsa = lds0 + wave * (BM / 4) * kBlock;
+        const uint32_t ldsb = lds0 + BM * kBlock + wave * (BN / 4) * kBlock;
+        constexpr uint32_t kStageStep = (BM + BN) * kBlock;
 
         // scales: four blocks of a row are a dword; rows of the wave: BM / 4 of A, BN / 4 of B, one a lane
         const uint8_t *sa0 = p.as + (uint64_t)m0 * p.ldas;
@@ -191,86 +199,88 @@ __global__ __launch_bounds__(kMThreads, (BM >= 256 ? 1 : 2)) void tile_kernel(Ma
             if (lane < BM / 4) lds_load4(sa0 + 4 * c, soffa, at + wave * BM);
             if (lane < BN / 4) lds_load4(sb0 + 4 * c, soffb, at + 4 * BM + wave * BN);
         };
-        const auto load_piece = [&](uint32_t s, uint32_t i) {  // the wave's i-th load of stage s
-            const uint32_t at = (s & (kStages - 1)) * kStageStep;
+        const auto load_piece = [&](uint32_t t, uint32_t i) {  // the wave's i-th load of block kb0 + t
+            const uint32_t at = (t & 1) * kStageStep;
             if (i < LA)
-                lds_load16(ga + (uint64_t)s * kStageBytes, offa[i % LA], ldsa + at + i * 1024);
+                lds_load16(ga + (uint64_t)t * kBlock, offa[i % LA], ldsa + at + i * 1024);
             else
-                lds_load16(gb + (uint64_t)s * kStageBytes, offb[(i - LA) % LB], ldsb + at + (i - LA) * 1024);
+                lds_load16(gb + (uint64_t)t * kBlock, offb[(i - LA) % LB], ldsb + at + (i - LA) * 1024);
         };
 
-        // fragments: lane l holds row l mod 32, chunks l / 32 and l / 32 + 2 (the order along the contraction does not
-        // matter as long as A and B agree)
-        const uint32_t fr = lane % 32, fc = lane / 32, sw = swizzle(fr);
-        const uint32_t ra0 = (wm + fr) * kStageBytes, rb0 = (BM + wn + fr) * kStageBytes;
-        const uint32_t c0 = 16 * (fc ^ sw), c1 = 16 * ((fc + 2) ^ sw);
-        u32v4 fa[2][MT][2], fb[2][NT][2];
+        // fragments: lane l holds row l mod 32, of the half block's four chunks l / 32 and l / 32 + 2 (the order along the
+        // contraction does not matter as long as A and B agree)
+        const uint32_t fr = lane % 32, fc = lane / 32, sw = fr / 2 & 7u;
+        const uint32_t ra0 = (wm + fr) * kBlock, rb0 = (BM + wn + fr) * kBlock;
+        u32v4 fa[2][MT][2], fb[2][NT][2];  // [half of the block]
         uint32_t ea[MT], eb[NT];
-        const auto read_a = [&](uint32_t s, uint32_t i, uint32_t h) -> u32v4 {
-            return *reinterpret_cast<const u32v4 *>(&sh.stage[s & (kStages - 1)][ra0 + 32 * i * kStageBytes + (h ? c1 : c0)]);
+        const auto read_a = [&](uint32_t t, uint32_t half, uint32_t i, uint32_t h) -> u32v4 {
+            return *reinterpret_cast<const u32v4 *>(
+                &sh.stage[t & 1][ra0 + 32 * i * kBlock + 16 * ((4 * half + 2 * h + fc) ^ sw)]);
         };
-        const auto read_b = [&](uint32_t s, uint32_t j, uint32_t h) -> u32v4 {
-            return *reinterpret_cast<const u32v4 *>(&sh.stage[s & (kStages - 1)][rb0 + 32 * j * kStageBytes + (h ? c1 : c0)]);
+        const auto read_b = [&](uint32_t t, uint32_t half, uint32_t j, uint32_t h) -> u32v4 {
+            return *reinterpret_cast<const u32v4 *>(
+                &sh.stage[t & 1][rb0 + 32 * j * kBlock + 16 * ((4 * half + 2 * h + fc) ^ sw)]);
         };
-        const auto read_scales = [&](uint32_t c) {
+        // the q-th of the 2 (MT + NT) reads of a half
+        constexpr uint32_t kReads = 2 * (MT + NT);
+        const auto read_piece = [&](uint32_t t, uint32_t half, uint32_t q) {
+            if (q < 2 * MT)
+                fa[half][q / 2 % MT][q & 1] = read_a(t, half, q / 2 % MT, q & 1);
+            else
+                fb[half][(q / 2 - MT) % NT][q & 1] = read_b(t, half, (q / 2 - MT) % NT, q & 1);
+        };
+        uint32_t wa4[MT], wb4[NT];  // four blocks' scales of the lane's rows
+        const auto read_scales = [&](uint32_t kb) {
 #pragma unroll
-            for (uint32_t i = 0; i < MT; ++i) ea[i] = sh.scale[c & 1][wm + 32 * i + fr];
+            for (uint32_t i = 0; i < MT; ++i) wa4[i] = sh.scale[kb / 4 & 1][wm + 32 * i + fr];
 #pragma unroll
-            for (uint32_t j = 0; j < NT; ++j) eb[j] = sh.scale[c & 1][BM + wn + 32 * j + fr];
+            for (uint32_t j = 0; j < NT; ++j) wb4[j] = sh.scale[kb / 4 & 1][BM + wn + 32 * j + fr];
+        };
+        const auto take_scales = [&](uint32_t kb) {  // block kb's in the low byte
+#pragma unroll
+            for (uint32_t i = 0; i < MT; ++i) ea[i] = wa4[i] >> (8 * (kb & 3));
+#pragma unroll
+            for (uint32_t j = 0; j < NT; ++j) eb[j] = wb4[j] >> (8 * (kb & 3));
         };
 
         const uint32_t chunk0 = kb0 / 4, chunk_last = (kb1 - 1) / 4;
         load_scales(chunk0);
         if (chunk0 < chunk_last) load_scales(chunk0 + 1);
 #pragma unroll
-        for (uint32_t s = 0; s < kStages; ++s)
-            if (s < stages)
+        for (uint32_t i = 0; i < LOADS; ++i) load_piece(0, i);
+        if (blocks > 1) {
 #pragma unroll
-                for (uint32_t i = 0; i < LOADS; ++i) load_piece(s, i);
-        if (stages >= kStages)
-            wait_and_meet<(int)((kStages - 1) * LOADS)>();
-        else
+            for (uint32_t i = 0; i < LOADS; ++i) load_piece(1, i);
+            wait_and_meet<(int)LOADS>();
+        } else {
             wait_and_meet<0>();
-        read_scales(chunk0);
-#pragma unroll
-        for (uint32_t i = 0; i < MT; ++i) ea[i] >>= 8 * (kb0 & 3);
-#pragma unroll
-        for (uint32_t j = 0; j < NT; ++j) eb[j] >>= 8 * (kb0 & 3);
-#pragma unroll
-        for (uint32_t h = 0; h < 2; ++h) {
-#pragma unroll
-            for (uint32_t i = 0; i < MT; ++i) fa[0][i][h] = read_a(0, i, h);
-#pragma unroll
-            for (uint32_t j = 0; j < NT; ++j) fb[0][j][h] = read_b(0, j, h);
         }
+        read_scales(kb0);
+        take_scales(kb0);
+#pragma unroll
+        for (uint32_t q = 0; q < kReads; ++q) read_piece(0, 0, q);
 
-        for (uint32_t s0 = 0; s0 < stages; s0 += 2) {
+        // one block; MORE: the block after the next is there to load
+        const auto step = [&](uint32_t t, auto more) {
+            constexpr bool MORE = decltype(more)::value;
+            const uint32_t kb = kb0 + t;
 #pragma unroll
             for (uint32_t half = 0; half < 2; ++half) {
-                const uint32_t s = s0 + half;
-                // stage s + 1 has landed (two younger stages may be on their way), and every wave holds stage s
-                if (s + kStages - 1 < stages)
-                    wait_and_meet<(int)((kStages - 2) * LOADS)>();
-                else
+                if (half == 1) {
+                    // block t + 1 has landed, and every wave holds the rest of block t
                     wait_and_meet<0>();
-                const bool more = s + kStages < stages;
-                const uint32_t cur = half, nxt = half ^ 1;
-                const uint32_t kb = kb0 + s0 / 2;
-                if (half == 0 && (kb & 3) == 0 && kb / 4 > chunk0 && kb / 4 < chunk_last) load_scales(kb / 4 + 1);
-                const auto piece = [&](uint32_t slot) {  // what goes between the matrix instructions
-                    if (slot < 2 * MT)
-                        fa[nxt][slot / 2 % MT][slot & 1] = read_a(s + 1, slot / 2 % MT, slot & 1);
-                    else if (slot < 2 * (MT + NT))
-                        fb[nxt][(slot / 2 - MT) % NT][slot & 1] = read_b(s + 1, (slot / 2 - MT) % NT, slot & 1);
-                };
+                    // the next four blocks' scales, again with every block (the same bytes): a branch here would
+                    // let the compiler move the matrix instructions behind it, away from the loads they hide
+                    if (MORE) load_scales(min(kb / 4 + 1, chunk_last));
+                }
                 bf16v8 wb[FULL ? NT : 1][4];
                 if (FULL)
 #pragma unroll
-                    for (uint32_t j = 0; j < NT; ++j) widen<FB>(join(fb[cur][j]), eb[j] & 0xFFu, wb[j % (FULL ? NT : 1)]);
+                    for (uint32_t j = 0; j < NT; ++j) widen<FB>(join(fb[half][j]), eb[j] & 0xFFu, wb[j % (FULL ? NT : 1)]);
 #pragma unroll
                 for (uint32_t i = 0; i < MT; ++i) {
                     bf16v8 wa[4];
-                    if (FULL) widen<FA>(join(fa[cur][i]), ea[i] & 0xFFu, wa);
+                    if (FULL) widen<FA>(join(fa[half][i]), ea[i] & 0xFFu, wa);
 #pragma unroll
                     for (uint32_t j = 0; j < NT; ++j) {
                         if (FULL) {
@@ -280,87 +290,100 @@ __global__ __launch_bounds__(kMThreads, (BM >= 256 ? 1 : 2)) void tile_kernel(Ma
                                                                                    acc[i][j], 0, 0, 0);
                         } else {
                             // B in the place of the left matrix: a lane then holds four consecutive columns of one row
-                            acc[i][j] = mfma<FB, FA>(join(fb[cur][j]), join(fa[cur][i]), acc[i][j], eb[j], ea[i]);
+                            acc[i][j] = mfma<FB, FA>(join(fb[half][j]), join(fa[half][i]), acc[i][j], eb[j], ea[i]);
                         }
-                        constexpr uint32_t kSlots = MT * NT, kPieces = 2 * (MT + NT);
+                        // between the matrix instructions of the first part of a half: the reads of the other half, and
+                        // the loads of the block after the next
+                        constexpr uint32_t kSlots = MT * NT;
                         const uint32_t slot = i * NT + j;
+                        if (slot < kSlots) {
+                            if (MORE && half == 1)
 #pragma unroll
-                        for (uint32_t q = slot * kPieces / kSlots; q < (slot + 1) * kPieces / kSlots; ++q) piece(q);
+                                for (uint32_t q = slot * LOADS / kSlots; q < (slot + 1) * LOADS / kSlots; ++q)
+                                    load_piece(t + 2, q);
 #pragma unroll
-                        for (uint32_t q = slot * LOADS / kSlots; q < (slot + 1) * LOADS / kSlots; ++q)
-                            if (more) load_piece(s + kStages, q);
+                            for (uint32_t q = slot * kReads / kSlots; q < (slot + 1) * kReads / kSlots; ++q)
+                                read_piece(t + half, half ^ 1, q);
+                            if (half == 1 && slot + 1 == kSlots) read_scales(kb + 1);
+                        }
                         __builtin_amdgcn_sched_barrier(0);
                     }
                 }
-                if (half == 1) {  // the next block's scales
-                    if (((kb + 1) & 3) == 0 && kb + 1 < kb1) {
-                        read_scales((kb + 1) / 4);
-                    } else {
+            }
+            take_scales(kb + 1);
+        };
+        uint32_t t = 0;
+        for (; t + 2 < blocks; ++t) step(t, std::true_type{});
+        for (; t < blocks; ++t) step(t, std::false_type{});
+    }
+
+    // Results through LDS, 64 (or 32) rows of a wave at a time, so that a row's BN / 2
+    // columns leave as whole lines.
+    wait_and_meet<0>();
+    uint8_t *const room = reinterpret_cast<uint8_t *>(&sh);
+    constexpr uint32_t es = sizeof(T), row_bytes = BN / 2 * es + 16, chunks = BN / 2 * es / 16, per = 16 / es;
+    constexpr uint32_t tiles = sizeof(sh) >= 4 * 64 * row_bytes ? 2 : 1, rounds = MT / tiles, rows = 32 * tiles;
+    static_assert(sizeof(sh) >= 4 * rows * row_bytes, "room for a round of every wave");
+    uint8_t *mine = room + wave * rows * row_bytes;
+    T *out = static_cast<T *>(p.out) + out0;
+    const bool dwords = (p.ldo * es) % 4 == 0 && (reinterpret_cast<uintptr_t>(out) & 3) == 0;
 #pragma unroll
-                        for (uint32_t i = 0; i < MT; ++i) ea[i] >>= 8;
+    for (uint32_t round = 0; round < rounds; ++round) {
 #pragma unroll
-                        for (uint32_t j = 0; j < NT; ++j) eb[j] >>= 8;
-                    }
+        for (uint32_t i = 0; i < tiles; ++i)
+#pragma unroll
+            for (uint32_t j = 0; j < NT; ++j)
+#pragma unroll
+                for (uint32_t e = 0; e < 16; e += 4) {
+                    const f32v16 &v = acc[round * tiles + i][j];
+                    uint8_t *w = mine + (32 * i + lane % 32) * row_bytes + (32 * j + 2 * e + 4 * (lane / 32)) * es;
+                    if (es == 2)
+                        *reinterpret_cast<u32v2 *>(w) = u32v2{bf_pack(v[e], v[e + 1]), bf_pack(v[e + 2], v[e + 3])};
+                    else
+                        *reinterpret_cast<u32v4 *>(w) = u32v4{__float_as_uint(v[e]), __float_as_uint(v[e + 1]),
+                                                              __float_as_uint(v[e + 2]), __float_as_uint(v[e + 3])};
+                }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        // a row's chunks go to consecutive lanes
+        constexpr uint32_t step = kLanes / chunks;
+        static_assert(kLanes % chunks == 0, "whole rows a step");
+        const uint32_t cc = lane % chunks, c = n0 + wn + cc * per;
+        uint32_t r = m0 + wm + round * rows + lane / chunks;
+        const uint8_t *from = mine + (lane / chunks) * row_bytes + cc * 16;
+        T *o = out + (uint64_t)r * p.ldo + c;
+        const bool whole = dwords && c + per <= p.n;
+#pragma unroll 4
+        for (uint32_t q = 0; q < rows / step; ++q, r += step, from += step * row_bytes, o += step * p.ldo) {
+            const u32v4 v = *reinterpret_cast<const u32v4 *>(from);
+            if (r < m1 && c < p.n) {
+                if (whole) {
+                    *reinterpret_cast<u32v4a4 *>(o) = v;
+                } else {
+                    for (uint32_t k = 0; k < per && c + k < p.n; ++k)
+                        o[k] = (T)(v[k * es / 4] >> (8 * es * k % 32));
                 }
             }
         }
-    }
-
-    // Results through LDS, 32 rows of a wave at a time, so that a row's BN / 2
-    // columns leave as whole lines.
-    wait_and_meet<0>();
-    constexpr uint32_t kRowBytes = BN / 2 * 4 + 16;
-    static_assert(sizeof(sh.stage) >= 4 * 32 * kRowBytes, "room for 32 rows of every wave");
-    uint8_t *mine = &sh.stage[0][0] + wave * 32 * kRowBytes;
-    const bool bf16 = p.out_bf16 != 0;
-    const uint32_t es = bf16 ? 2 : 4;
-    const bool fast = (p.ldo * es) % 4 == 0 && (out0 * es) % 4 == 0;  // the base is aligned to its element, 4 checked below
-    const bool fast_out = fast && (reinterpret_cast<uintptr_t>(p.out) & 3) == 0;
-#pragma unroll
-    for (uint32_t i = 0; i < MT; ++i) {
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-#pragma unroll
-        for (uint32_t j = 0; j < NT; ++j)
-#pragma unroll
-            for (uint32_t e = 0; e < 16; e += 4) {
-                const uint32_t c = 32 * j + 2 * e + 4 * (lane / 32);
-                uint8_t *w = mine + (lane % 32) * kRowBytes + c * es;
-                if (bf16)
-                    *reinterpret_cast<u32v2 *>(w) =
-                        u32v2{bf_pack(acc[i][j][e], acc[i][j][e + 1]), bf_pack(acc[i][j][e + 2], acc[i][j][e + 3])};
-                else
-                    *reinterpret_cast<u32v4 *>(w) =
-                        u32v4{__float_as_uint(acc[i][j][e]), __float_as_uint(acc[i][j][e + 1]),
-                              __float_as_uint(acc[i][j][e + 2]), __float_as_uint(acc[i][j][e + 3])};
-            }
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        const uint32_t row_chunks = BN / 2 * es / 16, per_chunk = 16 / es;
-        for (uint32_t q = lane; q < 32 * row_chunks; q += kLanes) {
-            const uint32_t rr = q / row_chunks, cc = q % row_chunks;
-            const uint32_t r = m0 + wm + 32 * i + rr, c = n0 + wn + cc * per_chunk;
-            if (r >= m1 || c >= p.n) continue;
-            const u32v4 v = *reinterpret_cast<const u32v4 *>(mine + rr * kRowBytes + cc * 16);
-            const uint64_t o = out0 + (uint64_t)r * p.ldo + c;
-            if (fast_out && c + per_chunk <= p.n) {
-                *reinterpret_cast<u32v4a4 *>(static_cast<uint8_t *>(p.out) + o * es) = v;
-            } else if (bf16) {
-                for (uint32_t k = 0; k < 8 && c + k < p.n; ++k)
-                    static_cast<uint16_t *>(p.out)[o + k] = (uint16_t)(v[k / 2] >> (16 * (k & 1)));
-            } else {
-                for (uint32_t k = 0; k < 4 && c + k < p.n; ++k) static_cast<uint32_t *>(p.out)[o + k] = v[k];
-            }
-        }
     }
 }
 
-template <bool WGRAD, int FA, int FB>
+template <bool WGRAD, int FA, int FB, typename T>
 static void launch_tile(const MatArgs &p, bool full, bool large, uint32_t grid, hipStream_t st) {
     if (full)
-        hipLaunchKernelGGL((tile_kernel<128, 128, WGRAD, FA, FB, true>), dim3(grid), dim3(kMThreads), 0, st, p);
+        hipLaunchKernelGGL((tile_kernel<128, 128, WGRAD, FA, FB, true, T>), dim3(grid), dim3(kMThreads), 0, st, p);
     else if (large)
-        hipLaunchKernelGGL((tile_kernel<256, 256, WGRAD, FA, FB, false>), dim3(grid), dim3(kMThreads), 0, st, p);
+        hipLaunchKernelGGL((tile_kernel<256, 256, WGRAD, FA, FB, false, T>), dim3(grid), dim3(kMThreads), 0, st, p);
     else
-        hipLaunchKernelGGL((tile_kernel<128, 128, WGRAD, FA, FB, false>), dim3(grid), dim3(kMThreads), 0, st, p);
+        hipLaunchKernelGGL((tile_kernel<128, 128, WGRAD, FA, FB, false, T>), dim3(grid), dim3(kMThreads), 0, st, p);
+}
+
+template <bool WGRAD, int FA, int FB>
+static void launch_out(const MatArgs &p, bool bf16, bool full, bool large, uint32_t grid, hipStream_t st) {
+    if (bf16)
+        launch_tile<WGRAD, FA, FB, uint16_t>(p, full, large, grid, st);
+    else
+        launch_tile<WGRAD, FA, FB, uint32_t>(p, full, large, grid, st);
 }
 
 template <bool WGRAD>
@@ -370,17 +393,16 @@ static uint64_t tiles_of(const MatArgs &p, uint32_t tile) {
 }
 
 template <bool WGRAD>
-static zc_status launch(MatArgs p, uint32_t ta, uint32_t tb, bool bf16, bool full, hipStream_t st) {
-    p.out_bf16 = bf16;
+static zc_status launch(const MatArgs &p, uint32_t ta, uint32_t tb, bool bf16, bool full, hipStream_t st) {
     const bool large = !full && tiles_of<WGRAD>(p, 256) >= 192;
     const uint64_t tiles = tiles_of<WGRAD>(p, large ? 256 : 128);
     if (tiles > 0xFFFFF0u) return ZC_ERR_INVALID_ARG;
-    const uint32_t grid = (uint32_t)ceil_div(tiles, 8) * 8;
+    const uint32_t grid = (uint32_t)ceil_div(tiles, 256) * 256;
     const int fa = ta == ZC_FP8_E5M2, fb = tb == ZC_FP8_E5M2;
-    if (!fa && !fb) launch_tile<WGRAD, 0, 0>(p, full, large, grid, st);
-    if (!fa && fb) launch_tile<WGRAD, 0, 1>(p, full, large, grid, st);
-    if (fa && !fb) launch_tile<WGRAD, 1, 0>(p, full, large, grid, st);
-    if (fa && fb) launch_tile<WGRAD, 1, 1>(p, full, large, grid, st);
+    if (!fa && !fb) launch_out<WGRAD, 0, 0>(p, bf16, full, large, grid, st);
+    if (!fa && fb) launch_out<WGRAD, 0, 1>(p, bf16, full, large, grid, st);
+    if (fa && !fb) launch_out<WGRAD, 1, 0>(p, bf16, full, large, grid, st);
+    if (fa && fb) launch_out<WGRAD, 1, 1>(p, bf16, full, large, grid, st);
     return launched();
 }
 

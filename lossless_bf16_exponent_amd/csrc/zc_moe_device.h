@@ -127,22 +127,24 @@ __device__ __forceinline__ float group_sum(float v) {
     return v;
 }
 
-__device__ __forceinline__ uint32_t scan_sum(uint32_t v, uint32_t lane) {
-#pragma unroll
-    for (int s = 1; s < (int)kLanes; s <<= 1) {
-        const uint32_t o = (uint32_t)__shfl_up((int)v, s);
-        v += lane >= (uint32_t)s ? o : 0u;
+// Inclusive scans over the wave in DPP moves: shifts of 1, 2, 4 and 8 lanes
+// inside the rows of 16, then the last lane of a row into the rows after it.  A
+// lane without a source keeps 0.
+#define ZC_MOE_SCAN(name, combine)                                                                            \
+    __device__ __forceinline__ uint32_t name(uint32_t v) {                                                    \
+        v = combine(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xF, 0xF, false));             \
+        v = combine(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xF, 0xF, false));             \
+        v = combine(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xF, 0xF, false));             \
+        v = combine(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xF, 0xF, false));             \
+        v = combine(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xA, 0xF, false));             \
+        v = combine(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xC, 0xF, false));             \
+        return v;                                                                                             \
     }
-    return v;
-}
-__device__ __forceinline__ uint32_t scan_max(uint32_t v, uint32_t lane) {
-#pragma unroll
-    for (int s = 1; s < (int)kLanes; s <<= 1) {
-        const uint32_t o = (uint32_t)__shfl_up((int)v, s);
-        v = max(v, lane >= (uint32_t)s ? o : 0u);
-    }
-    return v;
-}
+__device__ __forceinline__ uint32_t add_u32(uint32_t a, uint32_t b) { return a + b; }
+__device__ __forceinline__ uint32_t max_u32(uint32_t a, uint32_t b) { return a > b ? a : b; }
+ZC_MOE_SCAN(scan_sum, add_u32)
+ZC_MOE_SCAN(scan_max, max_u32)
+#undef ZC_MOE_SCAN
 
 // ---------------------------------------------------------------------------
 // groups of rows
@@ -160,92 +162,101 @@ __device__ __forceinline__ uint32_t clamp_row(int32_t v, uint32_t rows) {
     return v < 0 ? 0u : min((uint32_t)v, rows);
 }
 
-// The group that tile t falls into when every group's rows are cut into tiles
-// of `tile_rows`; t counts the tiles of all groups in order.  offsets NULL: one
-// group of all rows.  The offsets are clamped to 0..rows and to ascending order
-// (a running maximum), so that no value of them leads outside the arrays.  The
-// whole wave calls this; the result is uniform.  64 groups a round.
-__device__ __forceinline__ Span find_tile(const int32_t *offsets, uint32_t groups, uint32_t rows, uint32_t tile_rows,
-                                          uint32_t t) {
-    Span s = {0, 0, rows, t, 0, false};
-    if (!offsets) {
-        s.found = (uint64_t)t * tile_rows < rows;
-        return s;
-    }
-    const uint32_t lane = lane_id();
-    uint32_t tiles_before = 0, blocks_before = 0, high = 0;
-    for (uint32_t g0 = 0; g0 < groups; g0 += kLanes) {
-        const uint32_t g = g0 + lane;
-        const bool in = g < groups;
-        const uint32_t o0 = in ? clamp_row(offsets[g], rows) : 0u;
-        const uint32_t o1 = in ? clamp_row(offsets[g + 1], rows) : 0u;
-        const uint32_t begin = max(scan_max(o0, lane), high);
-        const uint32_t end = in ? max(begin, o1) : begin;
-        const uint32_t n = end - begin;
-        const uint32_t tiles = (n + tile_rows - 1) / tile_rows, blocks = (n + kBlock - 1) / kBlock;
-        const uint32_t tsum = scan_sum(tiles, lane), bsum = scan_sum(blocks, lane);
-        const uint32_t first = tiles_before + tsum - tiles;
-        const uint64_t hit = __ballot(in && t >= first && t < first + tiles);
-        if (hit) {
-            const int l = __builtin_ctzll(hit);
-            s.group = g0 + (uint32_t)l;
-            s.begin = (uint32_t)__builtin_amdgcn_readlane((int)begin, l);
-            s.end = (uint32_t)__builtin_amdgcn_readlane((int)end, l);
-            s.tile = t - (uint32_t)__builtin_amdgcn_readlane((int)first, l);
-            s.blocks0 = blocks_before + (uint32_t)__builtin_amdgcn_readlane((int)(bsum - blocks), l);
-            s.found = true;
-            return s;
-        }
-        tiles_before += (uint32_t)__builtin_amdgcn_readlane((int)tsum, kLanes - 1);
-        blocks_before += (uint32_t)__builtin_amdgcn_readlane((int)bsum, kLanes - 1);
-        high = (uint32_t)__builtin_amdgcn_readlane((int)end, kLanes - 1);
-    }
-    return s;
+// 64 groups of a list, one a lane: rows, tiles and blocks, and their running
+// sums.  The offsets are clamped to 0..rows and to ascending order (a running
+// maximum, `high` so far), so that no value of them leads outside the arrays.
+struct Groups {
+    uint32_t begin, end, tiles, blocks, tile_sum, block_sum;
+    bool in;
+};
+__device__ __forceinline__ Groups load_groups(const int32_t *offsets, uint32_t groups, uint32_t rows,
+                                              uint32_t tile_rows, uint32_t g0, uint32_t high) {
+    Groups r;
+    const uint32_t g = g0 + lane_id();
+    r.in = g < groups;
+    const uint32_t o0 = r.in ? clamp_row(offsets[g], rows) : 0u;
+    const uint32_t o1 = r.in ? clamp_row(offsets[g + 1], rows) : 0u;
+    r.begin = max(scan_max(o0), high);
+    r.end = r.in ? max(r.begin, o1) : r.begin;
+    const uint32_t n = r.end - r.begin;
+    r.tiles = (n + tile_rows - 1) / tile_rows;
+    r.blocks = (n + kBlock - 1) / kBlock;
+    r.tile_sum = scan_sum(r.tiles);
+    r.block_sum = scan_sum(r.blocks);
+    return r;
+}
+__device__ __forceinline__ uint32_t last_lane(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, kLanes - 1);
+}
+// Tile t among these 64 groups, whose first tile and block are the given ones.
+__device__ __forceinline__ bool tile_among(const Groups &r, uint32_t g0, uint32_t tiles0, uint32_t blocks0, uint32_t t,
+                                           Span &s) {
+    const uint32_t first = tiles0 + r.tile_sum - r.tiles;
+    const uint64_t hit = __ballot(r.in && t >= first && t < first + r.tiles);
+    if (!hit) return false;
+    const int l = __builtin_ctzll(hit);
+    s.group = g0 + (uint32_t)l;
+    s.begin = (uint32_t)__builtin_amdgcn_readlane((int)r.begin, l);
+    s.end = (uint32_t)__builtin_amdgcn_readlane((int)r.end, l);
+    s.tile = t - (uint32_t)__builtin_amdgcn_readlane((int)first, l);
+    s.blocks0 = blocks0 + (uint32_t)__builtin_amdgcn_readlane((int)(r.block_sum - r.blocks), l);
+    s.found = true;
+    return true;
 }
 
-// Tiles of `tile_rows` rows over all groups.
-__device__ __forceinline__ uint32_t count_tiles(const int32_t *offsets, uint32_t groups, uint32_t rows,
-                                                uint32_t tile_rows) {
-    if (!offsets) return (rows + tile_rows - 1) / tile_rows;
-    const uint32_t lane = lane_id();
+// The tile that pick(total tiles) names, when every group's rows are cut into
+// tiles of `tile_rows` and the tiles of all groups are counted in order; not
+// found when it names none of them.  offsets NULL: one group of all rows.  The
+// whole wave calls this; the result is uniform.  Up to 64 groups cost one load.
+template <typename Pick>
+__device__ __forceinline__ Span find_tile(const int32_t *offsets, uint32_t groups, uint32_t rows, uint32_t tile_rows,
+                                          Pick pick) {
+    Span s = {0, 0, rows, 0, 0, false};
+    if (!offsets) {
+        const uint32_t total = (rows + tile_rows - 1) / tile_rows;
+        s.tile = pick(total);
+        s.found = s.tile < total;
+        return s;
+    }
+    if (groups <= kLanes) {
+        const Groups r = load_groups(offsets, groups, rows, tile_rows, 0, 0);
+        tile_among(r, 0, 0, 0, pick(last_lane(r.tile_sum)), s);
+        return s;
+    }
     uint32_t total = 0, high = 0;
     for (uint32_t g0 = 0; g0 < groups; g0 += kLanes) {
-        const uint32_t g = g0 + lane;
-        const bool in = g < groups;
-        const uint32_t o0 = in ? clamp_row(offsets[g], rows) : 0u;
-        const uint32_t o1 = in ? clamp_row(offsets[g + 1], rows) : 0u;
-        const uint32_t begin = max(scan_max(o0, lane), high);
-        const uint32_t end = in ? max(begin, o1) : begin;
-        const uint32_t sum = scan_sum((end - begin + tile_rows - 1) / tile_rows, lane);
-        total += (uint32_t)__builtin_amdgcn_readlane((int)sum, kLanes - 1);
-        high = (uint32_t)__builtin_amdgcn_readlane((int)end, kLanes - 1);
+        const Groups r = load_groups(offsets, groups, rows, tile_rows, g0, high);
+        total += last_lane(r.tile_sum);
+        high = last_lane(r.end);
     }
-    return total;
+    const uint32_t t = pick(total);
+    uint32_t tiles = 0, blocks = 0;
+    high = 0;
+    for (uint32_t g0 = 0; g0 < groups; g0 += kLanes) {
+        const Groups r = load_groups(offsets, groups, rows, tile_rows, g0, high);
+        if (tile_among(r, g0, tiles, blocks, t, s)) return s;
+        tiles += last_lane(r.tile_sum);
+        blocks += last_lane(r.block_sum);
+        high = last_lane(r.end);
+    }
+    return s;
 }
 
 // Group g's rows and first block, for kernels whose grid is indexed by group.
 __device__ __forceinline__ Span find_group(const int32_t *offsets, uint32_t groups, uint32_t rows, uint32_t g) {
     Span s = {g, 0, rows, 0, 0, true};
     if (!offsets) return s;
-    const uint32_t lane = lane_id();
-    uint32_t blocks_before = 0, high = 0;
+    uint32_t blocks = 0, high = 0;
     for (uint32_t g0 = 0; g0 <= g; g0 += kLanes) {
-        const uint32_t i = g0 + lane;
-        const bool in = i < groups;
-        const uint32_t o0 = in ? clamp_row(offsets[i], rows) : 0u;
-        const uint32_t o1 = in ? clamp_row(offsets[i + 1], rows) : 0u;
-        const uint32_t begin = max(scan_max(o0, lane), high);
-        const uint32_t end = in ? max(begin, o1) : begin;
-        const uint32_t blocks = (end - begin + kBlock - 1) / kBlock;
-        const uint32_t bsum = scan_sum(blocks, lane);
+        const Groups r = load_groups(offsets, groups, rows, kBlock, g0, high);
         if (g < g0 + kLanes) {
             const int l = (int)(g - g0);
-            s.begin = (uint32_t)__builtin_amdgcn_readlane((int)begin, l);
-            s.end = (uint32_t)__builtin_amdgcn_readlane((int)end, l);
-            s.blocks0 = blocks_before + (uint32_t)__builtin_amdgcn_readlane((int)(bsum - blocks), l);
+            s.begin = (uint32_t)__builtin_amdgcn_readlane((int)r.begin, l);
+            s.end = (uint32_t)__builtin_amdgcn_readlane((int)r.end, l);
+            s.blocks0 = blocks + (uint32_t)__builtin_amdgcn_readlane((int)(r.block_sum - r.blocks), l);
         }
-        blocks_before += (uint32_t)__builtin_amdgcn_readlane((int)bsum, kLanes - 1);
-        high = (uint32_t)__builtin_amdgcn_readlane((int)end, kLanes - 1);
+        blocks += last_lane(r.block_sum);
+        high = last_lane(r.end);
     }
     return s;
 }
