@@ -96,6 +96,7 @@ template <uint32_t BM, uint32_t BN>
 struct TileShared {
     uint8_t stage[kStages][(BM + BN) * kBlock];
     uint32_t scale[2][BM + BN];  // four blocks' scale bytes of every row
+    uint32_t touched[4][kLanes];  // what the touches of later blocks bring, never read
 };
 
 // BM x BN tile of four waves (2 x 2).  The fragments of half a block are in
@@ -199,6 +200,16 @@ __global__ __launch_bounds__(kMThreads, (BM >= 256 ? 1 : 2)) void tile_kernel(Ma
             if (lane < BM / 4) lds_load4(sa0 + 4 * c, soffa, at + wave * BM);
             if (lane < BN / 4) lds_load4(sb0 + 4 * c, soffb, at + 4 * BM + wave * BN);
         };
+        // A touch brings one line per row of a later block into the L2: a quarter of A's rows and an eighth of B's, since
+        // the four and eight tiles beside this one that share them touch the others.  Three blocks ahead: 3 % of the
+        // time where the operands come from HBM (65536 x 4096 x 7168, 32 groups), nothing where they do not.
+        const uint32_t part = wave < 2 ? (nt & 3) * (BM / 4) + wave * (BM / 8) : (mt & 7) * (BN / 8) + (wave - 2) * (BN / 16);
+        const uint32_t touch_row = part + min(lane, (wave < 2 ? BM / 8 : BN / 16) - 1);
+        const uint32_t touch_off = wave < 2 ? min(touch_row, m1 - 1 - m0) * (uint32_t)p.lda
+                                            : min(touch_row, p.n - 1 - n0) * (uint32_t)p.ldb;
+        const uint8_t *const touch_base = wave < 2 ? ga : gb;
+        const uint32_t ldst = (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void *)&sh.touched[wave][0]);
+        const auto touch = [&](uint32_t t) { lds_load4(touch_base + (uint64_t)min(t, blocks - 1) * kBlock, touch_off, ldst); };
         const auto load_piece = [&](uint32_t t, uint32_t i) {  // the wave's i-th load of block kb0 + t
             const uint32_t at = (t & 1) * kStageStep;
             if (i < LA)
@@ -255,6 +266,7 @@ __global__ __launch_bounds__(kMThreads, (BM >= 256 ? 1 : 2)) void tile_kernel(Ma
         } else {
             wait_and_meet<0>();
         }
+        touch(2);
         read_scales(kb0);
         take_scales(kb0);
 #pragma unroll
@@ -267,8 +279,9 @@ __global__ __launch_bounds__(kMThreads, (BM >= 256 ? 1 : 2)) void tile_kernel(Ma
 #pragma unroll
             for (uint32_t half = 0; half < 2; ++half) {
                 if (half == 1) {
-                    // block t + 1 has landed, and every wave holds the rest of block t
-                    wait_and_meet<0>();
+                    // block t + 1 has landed (only the last touch may be on its way), and every wave holds the rest of
+                    // block t
+                    wait_and_meet<1>();
                     // the next four blocks' scales, again with every block (the same bytes): a branch here would
                     // let the compiler move the matrix instructions behind it, away from the loads they hide
                     if (MORE) load_scales(min(kb / 4 + 1, chunk_last));
@@ -304,7 +317,10 @@ __global__ __launch_bounds__(kMThreads, (BM >= 256 ? 1 : 2)) void tile_kernel(Ma
 #pragma unroll
                             for (uint32_t q = slot * kReads / kSlots; q < (slot + 1) * kReads / kSlots; ++q)
                                 read_piece(t + half, half ^ 1, q);
-                            if (half == 1 && slot + 1 == kSlots) read_scales(kb + 1);
+                            if (half == 1 && slot + 1 == kSlots) {
+                                read_scales(kb + 1);
+                                touch(t + 3);
+                            }
                         }
                         __builtin_amdgcn_sched_barrier(0);
                     }
