@@ -125,6 +125,27 @@ def test_near_ties_are_decided_in_64_bits(zc):
     assert np.array_equal(ids, want_ids)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("group_score", [1, 2])
+def test_near_tied_groups_are_decided_in_64_bits(zc, score, group_score):
+    """Groups whose scores differ by less than 32 bits show; in the last rows their second and third experts do too."""
+    g = np.random.default_rng(31)
+    groups, per = 8, 32
+    cfg = zc.route_config(groups * per, 6, score, groups=groups, group_top=3, group_score=group_score)
+    x = np.empty((24, groups, per), dtype=np.float32)
+    for r in range(24):
+        x[r] = g.standard_normal((groups, per)).astype(np.float32) * 0.25 - 2
+        x[r, :, 5] = np.float32(1.5) + g.permutation(groups).astype(np.float32) * np.float32(2.0 ** -23)
+        x[r, :, 9] = np.float32(1.0)
+        if r >= 16:
+            x[r, :, 20] = np.float32(1.0) + g.integers(-1, 2, groups).astype(np.float32) * np.float32(2.0 ** -23)
+    x = x.reshape(24, -1).astype(np.float64)
+    ids, w, _ = run(zc, x, cfg)
+    want_ids, want_w, _ = ref.route(x, None, cfg)
+    assert np.array_equal(ids, want_ids)
+    close(w, want_w, weight_tolerance(want_w, 6), "weights")
+
+
 def backward(zc, x, cfg, ids, dw, bf16, logits):
     t, e = x.shape
     out = Out((t, e + 5), torch.bfloat16 if bf16 else torch.float32)
