@@ -12,15 +12,15 @@ namespace moe {
 
 constexpr uint32_t kPlanThreads = 256;
 constexpr uint32_t kPlanWaves = kPlanThreads / kLanes;
-constexpr uint32_t kPlanChunk = 2048;  // copies a block ranks
-constexpr uint32_t kPlanPerWave = kPlanChunk / kPlanWaves;
+constexpr uint32_t kPlanChunk = 1024;      // a block ranks this many copies, or a multiple
+constexpr uint32_t kPlanMaxChunks = 256;   // every block reads every chunk's counts: keeps their number bounded
 constexpr uint32_t kBins = ZC_MAX_EXPERTS + 1;  // one bin more for dropped copies
 
 struct PlanArgs {
     const int32_t *ids;
     uint32_t *hist;  // [chunks][experts + 1]
     int32_t *offsets, *position, *source;
-    uint32_t copies, experts, chunks;
+    uint32_t copies, experts, chunks, per_chunk;
 };
 
 __device__ __forceinline__ uint32_t bin_of(const PlanArgs &a, uint32_t i) {
@@ -33,9 +33,9 @@ __global__ __launch_bounds__(kPlanThreads) void plan_count_kernel(PlanArgs a) {
     __shared__ uint32_t bins[kBins];
     for (uint32_t e = threadIdx.x; e <= a.experts; e += kPlanThreads) bins[e] = 0;
     __syncthreads();
-    const uint32_t i0 = blockIdx.x * kPlanChunk;
-    for (uint32_t j = threadIdx.x; j < kPlanChunk; j += kPlanThreads)
-        if (i0 + j < a.copies) atomicAdd(&bins[bin_of(a, i0 + j)], 1u);
+    const uint32_t i0 = blockIdx.x * a.per_chunk, i1 = min(i0 + a.per_chunk, a.copies);
+#pragma unroll 4
+    for (uint32_t i = i0 + threadIdx.x; i < i1; i += kPlanThreads) atomicAdd(&bins[bin_of(a, i)], 1u);
     __syncthreads();
     uint32_t *row = a.hist + (uint64_t)blockIdx.x * (a.experts + 1);
     for (uint32_t e = threadIdx.x; e <= a.experts; e += kPlanThreads) row[e] = bins[e];
@@ -44,25 +44,45 @@ __global__ __launch_bounds__(kPlanThreads) void plan_count_kernel(PlanArgs a) {
 // Ranks a chunk's copies.  A copy's row is the copies of lower experts (a scan
 // of the totals), the same expert's copies of earlier chunks, of earlier waves
 // of the chunk, and of earlier lanes of its wave: integer counts only, so the
-// order is that of the copies.
+// order is that of the copies.  Bound by the latency of those steps: 65,536
+// copies to 256 experts take 11 us with the counts (chunks of 2048, whose counts
+// were read one after another: 24 us).  A single chunk needs no counts of others.
 __global__ __launch_bounds__(kPlanThreads) void plan_place_kernel(PlanArgs a) {
-    __shared__ uint32_t total[kBins + 3];           // copies of an expert, then of all lower experts
-    __shared__ uint32_t base[kPlanWaves][kBins + 3];  // a wave's next row of every expert
+    __shared__ uint32_t total[kBins + 3];              // copies of an expert in all chunks
+    __shared__ uint32_t base[kPlanWaves + 1][kBins + 3];  // a wave's next row of every expert; below: counts of wave w at w + 1
     __shared__ uint32_t part[kPlanWaves];
     const uint32_t tid = threadIdx.x, lane = lane_id(), wave = tid / kLanes, nb = a.experts + 1;
-    for (uint32_t e = tid; e < nb; e += kPlanThreads) {
-        uint32_t all = 0, before = 0;
-        for (uint32_t c = 0; c < a.chunks; ++c) {
-            const uint32_t v = a.hist[(uint64_t)c * nb + e];
-            before += c < blockIdx.x ? v : 0u;
-            all += v;
-        }
-        total[e] = all;
-        base[0][e] = before;
+    for (uint32_t e = tid; e < nb; e += kPlanThreads)
 #pragma unroll
-        for (uint32_t w = 1; w < kPlanWaves; ++w) base[w][e] = 0;
-    }
+        for (uint32_t w = 0; w <= kPlanWaves; ++w) base[w][e] = 0;
     __syncthreads();
+    const uint32_t per_wave = a.per_chunk / kPlanWaves;
+    const uint32_t i0 = min(blockIdx.x * a.per_chunk + wave * per_wave, a.copies), i1 = min(i0 + per_wave, a.copies);
+#pragma unroll 4
+    for (uint32_t i = i0 + lane; i < i1; i += kLanes) atomicAdd(&base[wave + 1][bin_of(a, i)], 1u);
+    if (a.chunks > 1) {
+        for (uint32_t e = tid; e < nb; e += kPlanThreads) {
+            uint32_t all = 0, before = 0;
+#pragma unroll 16
+            for (uint32_t c = 0; c < a.chunks; ++c) {
+                const uint32_t v = a.hist[(uint64_t)c * nb + e];
+                before += c < blockIdx.x ? v : 0u;
+                all += v;
+            }
+            total[e] = all;
+            base[0][e] = before;
+        }
+        __syncthreads();
+    } else {
+        __syncthreads();
+        for (uint32_t e = tid; e < nb; e += kPlanThreads) {
+            uint32_t all = 0;
+#pragma unroll
+            for (uint32_t w = 1; w <= kPlanWaves; ++w) all += base[w][e];
+            total[e] = all;
+        }
+        __syncthreads();
+    }
     // copies of lower experts: each thread takes consecutive bins
     const uint32_t per = (nb + kPlanThreads - 1) / kPlanThreads, e0 = tid * per, e1 = min(e0 + per, nb);
     uint32_t mine = 0;
@@ -73,30 +93,23 @@ __global__ __launch_bounds__(kPlanThreads) void plan_place_kernel(PlanArgs a) {
     uint32_t run = incl - mine;
     for (uint32_t w = 0; w < wave; ++w) run += part[w];
     for (uint32_t e = e0; e < e1; ++e) {
-        const uint32_t n = total[e];
-        base[0][e] += run;
+        uint32_t next = base[0][e] + run;
         if (blockIdx.x == 0) a.offsets[e] = (int32_t)run;  // bin `experts` (dropped copies) ends the last expert's rows
-        run += n;
-    }
-    // the copies of each wave but the last, counted into the next wave's base
-    const uint32_t i0 = blockIdx.x * kPlanChunk + wave * kPlanPerWave;
-    if (wave + 1 < kPlanWaves)
-        for (uint32_t j = lane; j < kPlanPerWave; j += kLanes)
-            if (i0 + j < a.copies) atomicAdd(&base[wave + 1][bin_of(a, i0 + j)], 1u);
-    __syncthreads();
-    for (uint32_t e = tid; e < nb; e += kPlanThreads)
+        run += total[e];
+        base[0][e] = next;
 #pragma unroll
-        for (uint32_t w = 1; w < kPlanWaves; ++w) base[w][e] += base[w - 1][e];
+        for (uint32_t w = 1; w < kPlanWaves; ++w) base[w][e] = next += base[w][e];
+    }
     __syncthreads();
     uint32_t *next = base[wave];
-    for (uint32_t j = 0; j < kPlanPerWave; j += kLanes) {
-        const uint32_t i = i0 + j + lane;
-        const bool in = i < a.copies;
-        const uint32_t b = in ? bin_of(a, i) : ZC_MAX_EXPERTS + 1u;  // a bin of its own for lanes past the end
+    const uint32_t bits = 32 - __builtin_clz(a.experts + 1);  // of the largest bin, the one for lanes past the end
+    for (uint32_t j = i0; j < i1; j += kLanes) {
+        const uint32_t i = j + lane;
+        const bool in = i < i1;
+        const uint32_t b = in ? bin_of(a, i) : a.experts + 1;
         // lanes of the same bin, one bit of the bin's number at a time
         uint64_t same = ~0ull;
-#pragma unroll
-        for (uint32_t bit = 0; bit < 11; ++bit) {
+        for (uint32_t bit = 0; bit < bits; ++bit) {
             const uint64_t on = __ballot((b >> bit) & 1u);
             same &= ((b >> bit) & 1u) ? on : ~on;
         }
@@ -112,6 +125,12 @@ __global__ __launch_bounds__(kPlanThreads) void plan_place_kernel(PlanArgs a) {
             if (a.source) a.source[p] = dropped ? -1 : (int32_t)i;
         }
     }
+}
+
+// Copies of a chunk: kPlanChunk, or the multiple of it that leaves at most
+// kPlanMaxChunks chunks.
+static uint32_t per_chunk_of(uint64_t copies) {
+    return (uint32_t)(ceil_div(copies, (uint64_t)kPlanChunk * kPlanMaxChunks) * kPlanChunk);
 }
 
 __global__ void plan_empty_kernel(int32_t *offsets, uint32_t n) {
@@ -270,8 +289,9 @@ using namespace zc::moe;
 
 extern "C" uint64_t zc_dispatch_workspace_bytes(uint64_t tokens, uint32_t top_k, uint32_t experts) {
     if (!sizes_ok(tokens, top_k) || experts == 0 || experts > ZC_MAX_EXPERTS) return 0;
-    const uint64_t bytes = ceil_div(tokens * top_k, kPlanChunk) * (experts + 1) * 4;
-    return ceil_div(bytes + 1, 256) * 256;
+    if (!tokens) return 256;
+    const uint64_t chunks = ceil_div(tokens * top_k, per_chunk_of(tokens * top_k));
+    return ceil_div(chunks * (experts + 1) * 4, 256) * 256;
 }
 
 extern "C" zc_status zc_dispatch_plan(const int32_t *d_ids, uint64_t tokens, uint32_t top_k, uint32_t experts,
@@ -290,9 +310,9 @@ extern "C" zc_status zc_dispatch_plan(const int32_t *d_ids, uint64_t tokens, uin
         return launched();
     }
     PlanArgs a = {d_ids, static_cast<uint32_t *>(d_workspace), d_offsets, d_position, d_source,
-                  (uint32_t)(tokens * top_k), experts, 0};
-    a.chunks = (uint32_t)ceil_div(a.copies, kPlanChunk);
-    hipLaunchKernelGGL(plan_count_kernel, dim3(a.chunks), dim3(kPlanThreads), 0, st, a);
+                  (uint32_t)(tokens * top_k), experts, 0, per_chunk_of(tokens * top_k)};
+    a.chunks = (uint32_t)ceil_div(a.copies, a.per_chunk);
+    if (a.chunks > 1) hipLaunchKernelGGL(plan_count_kernel, dim3(a.chunks), dim3(kPlanThreads), 0, st, a);
     hipLaunchKernelGGL(plan_place_kernel, dim3(a.chunks), dim3(kPlanThreads), 0, st, a);
     return launched();
 }
