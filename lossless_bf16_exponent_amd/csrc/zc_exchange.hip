@@ -143,38 +143,60 @@ __global__ void plan_empty_kernel(int32_t *offsets, uint32_t n) {
 // ---------------------------------------------------------------------------
 
 constexpr uint32_t kRowThreads = 256;
+constexpr uint32_t kCopies = 8;  // copies of a token whose rows are on their way at once
 
+// V values as they lie in memory.
 template <uint32_t V>
-struct Vals {
-    float v[V];
+struct Raw;
+template <>
+struct Raw<8> {
+    u32v4 w;
+    __device__ __forceinline__ float value(uint32_t i) const { return (i & 1) ? bf_hi(w[i / 2]) : bf_lo(w[i / 2]); }
+    __device__ __forceinline__ void set(uint32_t i, float lo, float hi) { w[i / 2] = bf_pack(lo, hi); }
+};
+template <>
+struct Raw<1> {
+    uint16_t w;
+    __device__ __forceinline__ float value(uint32_t) const { return bf_one(w); }
 };
 
+// Rows that are read or written once carry the non-temporal hint (the weighted
+// sum of 8192 x 8 rows of 7168: 246 -> 213 us).
 template <uint32_t V>
-__device__ __forceinline__ Vals<V> load_vals(const uint16_t *p) {
-    Vals<V> r;
-    if (V == 8) {
-        const u32v4 w = *reinterpret_cast<const u32v4 *>(p);
-#pragma unroll
-        for (uint32_t i = 0; i < 4; ++i) {
-            r.v[(2 * i) % V] = bf_lo(w[i]);
-            r.v[(2 * i + 1) % V] = bf_hi(w[i]);
-        }
-    } else {
-        r.v[0] = bf_one(*p);
-    }
+__device__ __forceinline__ Raw<V> load_once(const uint16_t *p) {
+    Raw<V> r;
+    if constexpr (V == 8)
+        r.w = __builtin_nontemporal_load(reinterpret_cast<const u32v4 *>(p));
+    else
+        r.w = __builtin_nontemporal_load(p);
     return r;
 }
-
 template <uint32_t V>
-__device__ __forceinline__ void store_vals(uint16_t *p, const Vals<V> &r) {
-    if (V == 8) {
-        u32v4 w;
+__device__ __forceinline__ Raw<V> load_row(const uint16_t *p) {
+    Raw<V> r;
+    if constexpr (V == 8)
+        r.w = *reinterpret_cast<const u32v4 *>(p);
+    else
+        r.w = *p;
+    return r;
+}
+template <uint32_t V>
+__device__ __forceinline__ void store_raw(uint16_t *p, const Raw<V> &r) {
+    if constexpr (V == 8)
+        *reinterpret_cast<u32v4 *>(p) = r.w;
+    else
+        *p = r.w;
+}
+template <uint32_t V>
+__device__ __forceinline__ Raw<V> pack_vals(const float (&v)[V]) {
+    Raw<V> r;
+    if constexpr (V == 8) {
 #pragma unroll
-        for (uint32_t i = 0; i < 4; ++i) w[i] = bf_pack(r.v[(2 * i) % V], r.v[(2 * i + 1) % V]);
-        *reinterpret_cast<u32v4 *>(p) = w;
+        for (uint32_t i = 0; i < V; i += 2) r.set(i, v[i], v[i + 1]);
     } else {
-        *p = bf_round(r.v[0]);
+        r.w = bf_round(v[0]);
     }
+    return r;
 }
 
 struct RowArgs {
@@ -188,91 +210,115 @@ struct RowArgs {
     uint32_t tokens, top_k, rows, hidden;
 };
 
-// One block a token: the row is read once and written to each of its places.
+// The row of copy k of token t, -1 if it has none (uniform).
+__device__ __forceinline__ int32_t row_of(const RowArgs &a, uint64_t t, uint32_t k) {
+    if (k >= a.top_k) return -1;
+    const int32_t p = __builtin_amdgcn_readfirstlane(a.position[t * a.top_k + k]);
+    return p >= 0 && (uint32_t)p < a.rows ? p : -1;
+}
+
+// The row is read once and written to each of its places.  Block (t, y): the
+// y-th 256 V values of the row and every gridDim.y-th after it.
 template <uint32_t V>
 __global__ __launch_bounds__(kRowThreads) void dispatch_kernel(RowArgs a) {
-    for (uint32_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
-        const int32_t *pos = a.position + (uint64_t)t * a.top_k;
-        const uint16_t *src = a.x + (uint64_t)t * a.xs;
-        for (uint32_t h = threadIdx.x * V; h < a.hidden; h += kRowThreads * V) {
-            if (V == 8) {
-                const u32v4 w = *reinterpret_cast<const u32v4 *>(src + h);
-                for (uint32_t k = 0; k < a.top_k; ++k) {
-                    const int32_t p = pos[k];
-                    if (p >= 0 && (uint32_t)p < a.rows) *reinterpret_cast<u32v4 *>(a.out + (uint64_t)p * a.os + h) = w;
-                }
-            } else {
-                const uint16_t w = src[h];
-                for (uint32_t k = 0; k < a.top_k; ++k) {
-                    const int32_t p = pos[k];
-                    if (p >= 0 && (uint32_t)p < a.rows) a.out[(uint64_t)p * a.os + h] = w;
-                }
+    for (uint64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
+        const uint16_t *src = a.x + t * a.xs;
+        for (uint32_t h = (blockIdx.y * kRowThreads + threadIdx.x) * V; h < a.hidden; h += gridDim.y * kRowThreads * V) {
+            const Raw<V> w = load_row<V>(src + h);
+            for (uint32_t k = 0; k < a.top_k; ++k) {
+                const int32_t p = row_of(a, t, k);
+                if (p >= 0) store_raw<V>(a.out + (uint64_t)p * a.os + h, w);
             }
         }
     }
 }
 
-// One block a token; the sums stay in 32 bits, k ascending.
+// The sums stay in 32 bits, k ascending; eight copies' rows are on their way at
+// once.  Blocks as in dispatch_kernel.
 template <uint32_t V>
 __global__ __launch_bounds__(kRowThreads) void combine_kernel(RowArgs a) {
-    for (uint32_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
-        const int32_t *pos = a.position + (uint64_t)t * a.top_k;
-        for (uint32_t h = threadIdx.x * V; h < a.hidden; h += kRowThreads * V) {
-            Vals<V> sum;
+    for (uint64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
+        for (uint32_t h = (blockIdx.y * kRowThreads + threadIdx.x) * V; h < a.hidden; h += gridDim.y * kRowThreads * V) {
+            float sum[V];
 #pragma unroll
-            for (uint32_t i = 0; i < V; ++i) sum.v[i] = 0.0f;
-            for (uint32_t k = 0; k < a.top_k; ++k) {
-                const int32_t p = pos[k];
-                if (p < 0 || (uint32_t)p >= a.rows) continue;
-                const float w = a.weights ? a.weights[(uint64_t)t * a.top_k + k] : 1.0f;
-                const Vals<V> z = load_vals<V>(a.x + (uint64_t)p * a.xs + h);
+            for (uint32_t i = 0; i < V; ++i) sum[i] = 0.0f;
+            for (uint32_t k0 = 0; k0 < a.top_k; k0 += kCopies) {
+                Raw<V> z[kCopies];
+                int32_t p[kCopies];
+                float w[kCopies];
 #pragma unroll
-                for (uint32_t i = 0; i < V; ++i) sum.v[i] = fmaf(w, z.v[i], sum.v[i]);
+                for (uint32_t j = 0; j < kCopies; ++j) p[j] = row_of(a, t, k0 + j);
+#pragma unroll
+                for (uint32_t j = 0; j < kCopies; ++j) {
+                    w[j] = p[j] >= 0 && a.weights ? a.weights[t * a.top_k + k0 + j] : 1.0f;
+                    if (p[j] >= 0) z[j] = load_once<V>(a.x + (uint64_t)p[j] * a.xs + h);
+                }
+#pragma unroll
+                for (uint32_t j = 0; j < kCopies; ++j)
+                    if (p[j] >= 0)
+#pragma unroll
+                        for (uint32_t i = 0; i < V; ++i) sum[i] = fmaf(w[j], z[j].value(i), sum[i]);
             }
-            store_vals<V>(a.out + (uint64_t)t * a.os + h, sum);
+            store_raw<V>(a.out + t * a.os + h, pack_vals<V>(sum));
         }
     }
 }
 
-// One block a token: dz = w dy and the products <dy, z>, each k's summed over
+// One block a token: dz = w dy and the products <dy, z>, each copy's summed over
 // the block in an order fixed by the sizes.
 template <uint32_t V>
 __global__ __launch_bounds__(kRowThreads) void combine_backward_kernel(RowArgs a) {
-    __shared__ float part[kRowThreads / kLanes][ZC_MAX_TOP_K];
+    __shared__ float part[kRowThreads / kLanes][kCopies];
     const uint32_t lane = lane_id(), wave = threadIdx.x / kLanes;
-    for (uint32_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
-        const uint64_t tk = (uint64_t)t * a.top_k;
-        for (uint32_t k = 0; k < a.top_k; ++k) {
-            const int32_t p = a.position[tk + k];
-            const bool on = p >= 0 && (uint32_t)p < a.rows;
-            const float w = a.weights && a.out ? a.weights[tk + k] : 1.0f;
-            float dot = 0.0f;
-            if (on)
-                for (uint32_t h = threadIdx.x * V; h < a.hidden; h += kRowThreads * V) {
-                    const Vals<V> dy = load_vals<V>(a.dy + (uint64_t)t * a.dys + h);
-                    if (a.dweights) {
-                        const Vals<V> z = load_vals<V>(a.x + (uint64_t)p * a.xs + h);
+    for (uint64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
+        for (uint32_t k0 = 0; k0 < a.top_k; k0 += kCopies) {
+            int32_t p[kCopies];
+            float w[kCopies], dot[kCopies];
 #pragma unroll
-                        for (uint32_t i = 0; i < V; ++i) dot = fmaf(dy.v[i], z.v[i], dot);
-                    }
-                    if (a.out) {
-                        Vals<V> dz;
+            for (uint32_t j = 0; j < kCopies; ++j) p[j] = row_of(a, t, k0 + j);
 #pragma unroll
-                        for (uint32_t i = 0; i < V; ++i) dz.v[i] = w * dy.v[i];
-                        store_vals<V>(a.out + (uint64_t)p * a.os + h, dz);
-                    }
-                }
-            dot = group_sum<64>(dot);
-            if (lane == 0) part[wave][k] = dot;
+            for (uint32_t j = 0; j < kCopies; ++j) {
+                w[j] = p[j] >= 0 && a.weights && a.out ? a.weights[t * a.top_k + k0 + j] : 1.0f;
+                dot[j] = 0.0f;
+            }
+            for (uint32_t h = threadIdx.x * V; h < a.hidden; h += kRowThreads * V) {
+                const Raw<V> dy = load_row<V>(a.dy + t * a.dys + h);
+                Raw<V> z[kCopies];
+                if (a.dweights)
+#pragma unroll
+                    for (uint32_t j = 0; j < kCopies; ++j)
+                        if (p[j] >= 0) z[j] = load_once<V>(a.x + (uint64_t)p[j] * a.xs + h);
+                if (a.out)
+#pragma unroll
+                    for (uint32_t j = 0; j < kCopies; ++j)
+                        if (p[j] >= 0) {
+                            float dz[V];
+#pragma unroll
+                            for (uint32_t i = 0; i < V; ++i) dz[i] = w[j] * dy.value(i);
+                            store_raw<V>(a.out + (uint64_t)p[j] * a.os + h, pack_vals<V>(dz));
+                        }
+                if (a.dweights)
+#pragma unroll
+                    for (uint32_t j = 0; j < kCopies; ++j)
+                        if (p[j] >= 0)
+#pragma unroll
+                            for (uint32_t i = 0; i < V; ++i) dot[j] = fmaf(dy.value(i), z[j].value(i), dot[j]);
+            }
+            if (!a.dweights) continue;
+#pragma unroll
+            for (uint32_t j = 0; j < kCopies; ++j) {
+                const float d = wave_sum_f(dot[j]);
+                if (lane == 0) part[wave][j] = d;
+            }
+            __syncthreads();
+            if (threadIdx.x < kCopies && k0 + threadIdx.x < a.top_k) {
+                float s = 0.0f;
+#pragma unroll
+                for (uint32_t v = 0; v < kRowThreads / kLanes; ++v) s += part[v][threadIdx.x];
+                a.dweights[t * a.top_k + k0 + threadIdx.x] = s;
+            }
+            __syncthreads();
         }
-        __syncthreads();
-        if (a.dweights && threadIdx.x < a.top_k) {
-            float s = 0.0f;
-#pragma unroll
-            for (uint32_t w = 0; w < kRowThreads / kLanes; ++w) s += part[w][threadIdx.x];
-            a.dweights[tk + threadIdx.x] = s;
-        }
-        __syncthreads();
     }
 }
 
@@ -281,6 +327,12 @@ static bool sizes_ok(uint64_t tokens, uint32_t top_k) {
 }
 static bool wide(const void *p, uint64_t stride) { return aligned(p, 16) && stride % 8 == 0; }
 static uint32_t token_blocks(uint32_t tokens) { return tokens < (1u << 20) ? tokens : (1u << 20); }
+// Blocks of a row of `hidden` values, V an access: one for each 256 V values, so
+// that a few tokens spread over the device too, at most 16.
+static dim3 row_grid(uint32_t tokens, uint32_t hidden, uint32_t v) {
+    const uint64_t pieces = ceil_div(hidden, (uint64_t)kRowThreads * v);
+    return dim3(token_blocks(tokens), (uint32_t)(pieces < 16 ? pieces : 16));
+}
 
 }  // namespace moe
 }  // namespace zc
@@ -337,11 +389,11 @@ extern "C" zc_status zc_dispatch(const void *d_x, uint64_t tokens, uint64_t hidd
     a.rows = (uint32_t)rows;
     a.hidden = (uint32_t)hidden;
     hipStream_t st = static_cast<hipStream_t>(stream);
-    const dim3 grid(token_blocks(a.tokens)), block(kRowThreads);
+    const dim3 block(kRowThreads);
     if (hidden % 8 == 0 && wide(d_x, x_stride) && wide(d_out, out_stride))
-        hipLaunchKernelGGL(dispatch_kernel<8>, grid, block, 0, st, a);
+        hipLaunchKernelGGL(dispatch_kernel<8>, row_grid(a.tokens, a.hidden, 8), block, 0, st, a);
     else
-        hipLaunchKernelGGL(dispatch_kernel<1>, grid, block, 0, st, a);
+        hipLaunchKernelGGL(dispatch_kernel<1>, row_grid(a.tokens, a.hidden, 1), block, 0, st, a);
     return launched();
 }
 
@@ -367,11 +419,11 @@ extern "C" zc_status zc_combine(const void *d_z, uint64_t rows, uint64_t hidden,
     a.rows = (uint32_t)rows;
     a.hidden = (uint32_t)hidden;
     hipStream_t st = static_cast<hipStream_t>(stream);
-    const dim3 grid(token_blocks(a.tokens)), block(kRowThreads);
+    const dim3 block(kRowThreads);
     if (hidden % 8 == 0 && wide(d_z, z_stride) && wide(d_y, y_stride))
-        hipLaunchKernelGGL(combine_kernel<8>, grid, block, 0, st, a);
+        hipLaunchKernelGGL(combine_kernel<8>, row_grid(a.tokens, a.hidden, 8), block, 0, st, a);
     else
-        hipLaunchKernelGGL(combine_kernel<1>, grid, block, 0, st, a);
+        hipLaunchKernelGGL(combine_kernel<1>, row_grid(a.tokens, a.hidden, 1), block, 0, st, a);
     return launched();
 }
 

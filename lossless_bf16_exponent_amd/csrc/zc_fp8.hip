@@ -23,7 +23,7 @@ template <bool WIDE>
 __device__ __forceinline__ u32v4 load8(const uint16_t *row, uint32_t c, uint32_t cols) {
     u32v4 w = {0u, 0u, 0u, 0u};
     if (WIDE) {  // cols is a multiple of 8: the eight exist together
-        if (c < cols) w = *reinterpret_cast<const u32v4 *>(row + c);
+        if (c < cols) w = __builtin_nontemporal_load(reinterpret_cast<const u32v4 *>(row + c));
     } else {
 #pragma unroll
         for (uint32_t i = 0; i < 8; ++i) {

@@ -127,6 +127,20 @@ __device__ __forceinline__ float group_sum(float v) {
     return v;
 }
 
+// Sum over the wave, in an order of its own that does not change.
+__device__ __forceinline__ float wave_sum_f(float v) {
+#define ZC_MOE_ADD(ctrl, rows) \
+    v += __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), ctrl, rows, 0xF, false))
+    ZC_MOE_ADD(0x111, 0xF);  // shifts of 1, 2, 4, 8 lanes inside the rows of 16; then a row's last lane into the rows after it
+    ZC_MOE_ADD(0x112, 0xF);
+    ZC_MOE_ADD(0x114, 0xF);
+    ZC_MOE_ADD(0x118, 0xF);
+    ZC_MOE_ADD(0x142, 0xA);
+    ZC_MOE_ADD(0x143, 0xC);
+#undef ZC_MOE_ADD
+    return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
+}
+
 // Inclusive scans over the wave in DPP moves: shifts of 1, 2, 4 and 8 lanes
 // inside the rows of 16, then the last lane of a row into the rows after it.  A
 // lane without a source keeps 0.
