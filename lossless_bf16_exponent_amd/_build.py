@@ -36,7 +36,7 @@ def compile_command(out: str, extra=()) -> list:
 
 def build(verbose: bool = False) -> str:
     tmp = LIB + ".tmp%d" % os.getpid()
-    cmd = compile_command(tmp, extra=tuple(MOE_SOURCES))
+    cmd = compile_command(tmp, extra=(*MOE_SOURCES, "-parallel-jobs=8"))
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)

@@ -25,6 +25,7 @@ struct MatArgs {
     uint64_t ldo, out_group;             // elements
     uint32_t m, n, rows, blocks, groups;  // blocks of 128 along the contraction (forward); rows split into groups
     uint32_t b_shift;                    // rows of B that share a row of scales, as a shift
+    uint64_t split_stride;               // elements of one part of a split contraction; gridDim.y parts
 };
 
 constexpr uint32_t kMThreads = 256;
@@ -89,12 +90,10 @@ __device__ __forceinline__ void wait_and_meet() {
 
 // A stage is one block of 128 along the contraction: 128 bytes of every row, a
 // whole cache line each.  (Stages of 64 bytes, four deep, asked the L2 for twice
-// as many half lines and took 1.3 times as long.)
-constexpr uint32_t kStages = 2;
-
-template <uint32_t BM, uint32_t BN>
+// as many half lines and took 1.3 times as long.)  As many as fit 160 KiB of LDS.
+template <uint32_t BM, uint32_t BN, uint32_t STAGES>
 struct TileShared {
-    uint8_t stage[kStages][(BM + BN) * kBlock];
+    uint8_t stage[STAGES][(BM + BN) * kBlock];
     uint32_t scale[2][BM + BN];  // four blocks' scale bytes of every row
     uint32_t touched[4][kLanes];  // what the touches of later blocks bring, never read
 };
@@ -102,14 +101,14 @@ struct TileShared {
 // BM x BN tile of four waves (2 x 2).  The fragments of half a block are in
 // registers while the other half's come out of LDS.  In the middle of a block
 // every wave holds the rest of it, and one barrier then frees its buffer for the
-// block after the next and hands over the next one.  T: uint16_t for BF16 results, uint32_t for
+// block STAGES after it and hands over the next one.  T: uint16_t for BF16 results, uint32_t for
 // floats.
-template <uint32_t BM, uint32_t BN, bool WGRAD, int FA, int FB, bool FULL, typename T>
-__global__ __launch_bounds__(kMThreads, (BM >= 256 ? 1 : 2)) void tile_kernel(MatArgs p) {
+template <uint32_t BM, uint32_t BN, uint32_t STAGES, bool WGRAD, int FA, int FB, bool FULL, typename T>
+__global__ __launch_bounds__(kMThreads, (sizeof(TileShared<BM, BN, STAGES>) > 80 * 1024 ? 1 : 2)) void tile_kernel(MatArgs p) {
     constexpr uint32_t MT = BM / 64, NT = BN / 64;         // 32 x 32 tiles of a wave
     constexpr uint32_t LA = BM / 32, LB = BN / 32;         // 16-byte loads of a wave and block, 8 rows each
     constexpr uint32_t LOADS = LA + LB;
-    __shared__ alignas(1024) TileShared<BM, BN> sh;
+    __shared__ alignas(1024) TileShared<BM, BN, STAGES> sh;
     const uint32_t lane = lane_id(), wave = (uint32_t)__builtin_amdgcn_readfirstlane(threadIdx.x / kLanes);
     const uint32_t ntiles = (p.n + BN - 1) / BN;
 
@@ -151,10 +150,11 @@ __global__ __launch_bounds__(kMThreads, (BM >= 256 ? 1 : 2)) void tile_kernel(Ma
         if (!sp.found) return;
         m0 = sp.begin + sp.tile * BM;
         m1 = sp.end;
-        kb0 = 0;
-        kb1 = p.blocks;
+        kb0 = (uint32_t)((uint64_t)p.blocks * blockIdx.y / gridDim.y);
+        kb1 = (uint32_t)((uint64_t)p.blocks * (blockIdx.y + 1) / gridDim.y);
         b += sp.group * p.b_group;
         bs += sp.group * p.bs_group;
+        out0 = blockIdx.y * p.split_stride;
     }
     const uint32_t n0 = nt * BN;
     const uint32_t blocks = kb1 - kb0;
@@ -210,8 +210,7 @@ __global__ __launch_bounds__(kMThreads, (BM >= 256 ? 1 : 2)) void tile_kernel(Ma
         const uint8_t *const touch_base = wave < 2 ? ga : gb;
         const uint32_t ldst = (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void *)&sh.touched[wave][0]);
         const auto touch = [&](uint32_t t) { lds_load4(touch_base + (uint64_t)min(t, blocks - 1) * kBlock, touch_off, ldst); };
-        const auto load_piece = [&](uint32_t t, uint32_t i) {  // the wave's i-th load of block kb0 + t
-            const uint32_t at = (t & 1) * kStageStep;
+        const auto load_piece = [&](uint32_t t, uint32_t at, uint32_t i) {  // the wave's i-th load of block kb0 + t
             if (i < LA)
                 lds_load16(ga + (uint64_t)t * kBlock, offa[i % LA], ldsa + at + i * 1024);
             else
@@ -224,21 +223,22 @@ __global__ __launch_bounds__(kMThreads, (BM >= 256 ? 1 : 2)) void tile_kernel(Ma
         const uint32_t ra0 = (wm + fr) * kBlock, rb0 = (BM + wn + fr) * kBlock;
         u32v4 fa[2][MT][2], fb[2][NT][2];  // [half of the block]
         uint32_t ea[MT], eb[NT];
-        const auto read_a = [&](uint32_t t, uint32_t half, uint32_t i, uint32_t h) -> u32v4 {
+        const uint8_t *const stages = &sh.stage[0][0];
+        const auto read_a = [&](uint32_t at, uint32_t half, uint32_t i, uint32_t h) -> u32v4 {
             return *reinterpret_cast<const u32v4 *>(
-                &sh.stage[t & 1][ra0 + 32 * i * kBlock + 16 * ((4 * half + 2 * h + fc) ^ sw)]);
+                stages + (at + ra0 + 32 * i * kBlock + 16 * ((4 * half + 2 * h + fc) ^ sw)));
         };
-        const auto read_b = [&](uint32_t t, uint32_t half, uint32_t j, uint32_t h) -> u32v4 {
+        const auto read_b = [&](uint32_t at, uint32_t half, uint32_t j, uint32_t h) -> u32v4 {
             return *reinterpret_cast<const u32v4 *>(
-                &sh.stage[t & 1][rb0 + 32 * j * kBlock + 16 * ((4 * half + 2 * h + fc) ^ sw)]);
+                stages + (at + rb0 + 32 * j * kBlock + 16 * ((4 * half + 2 * h + fc) ^ sw)));
         };
         // the q-th of the 2 (MT + NT) reads of a half
         constexpr uint32_t kReads = 2 * (MT + NT);
-        const auto read_piece = [&](uint32_t t, uint32_t half, uint32_t q) {
+        const auto read_piece = [&](uint32_t at, uint32_t half, uint32_t q) {
             if (q < 2 * MT)
-                fa[half][q / 2 % MT][q & 1] = read_a(t, half, q / 2 % MT, q & 1);
+                fa[half][q / 2 % MT][q & 1] = read_a(at, half, q / 2 % MT, q & 1);
             else
-                fb[half][(q / 2 - MT) % NT][q & 1] = read_b(t, half, (q / 2 - MT) % NT, q & 1);
+                fb[half][(q / 2 - MT) % NT][q & 1] = read_b(at, half, (q / 2 - MT) % NT, q & 1);
         };
         uint32_t wa4[MT], wb4[NT];  // four blocks' scales of the lane's rows
         const auto read_scales = [&](uint32_t kb) {
@@ -258,30 +258,32 @@ __global__ __launch_bounds__(kMThreads, (BM >= 256 ? 1 : 2)) void tile_kernel(Ma
         load_scales(chunk0);
         if (chunk0 < chunk_last) load_scales(chunk0 + 1);
 #pragma unroll
-        for (uint32_t i = 0; i < LOADS; ++i) load_piece(0, i);
-        if (blocks > 1) {
+        for (uint32_t t = 0; t < STAGES; ++t)
+            if (t < blocks)
 #pragma unroll
-            for (uint32_t i = 0; i < LOADS; ++i) load_piece(1, i);
-            wait_and_meet<(int)LOADS>();
-        } else {
+                for (uint32_t i = 0; i < LOADS; ++i) load_piece(t, t * kStageStep, i);
+        if (blocks >= STAGES)
+            wait_and_meet<(int)((STAGES - 1) * LOADS)>();
+        else
             wait_and_meet<0>();
-        }
-        touch(2);
+        touch(STAGES);
         read_scales(kb0);
         take_scales(kb0);
 #pragma unroll
         for (uint32_t q = 0; q < kReads; ++q) read_piece(0, 0, q);
 
-        // one block; MORE: the block after the next is there to load
+        uint32_t at0 = 0, at1 = kStageStep;  // where blocks t and t + 1 are
+        // one block; MORE: there is a block to load into its place
         const auto step = [&](uint32_t t, auto more) {
             constexpr bool MORE = decltype(more)::value;
+            // younger than block t + 1 are at least the loads of the STAGES - 2 blocks after it and one touch
+            constexpr int kYounger = MORE ? 1 + (int)((STAGES - 2) * LOADS) : 0;
             const uint32_t kb = kb0 + t;
 #pragma unroll
             for (uint32_t half = 0; half < 2; ++half) {
                 if (half == 1) {
-                    // block t + 1 has landed (only the last touch may be on its way), and every wave holds the rest of
-                    // block t
-                    wait_and_meet<1>();
+                    // block t + 1 has landed, and every wave holds the rest of block t
+                    wait_and_meet<kYounger>();
                     // the next four blocks' scales, again with every block (the same bytes): a branch here would
                     // let the compiler move the matrix instructions behind it, away from the loads they hide
                     if (MORE) load_scales(min(kb / 4 + 1, chunk_last));
@@ -313,13 +315,13 @@ __global__ __launch_bounds__(kMThreads, (BM >= 256 ? 1 : 2)) void tile_kernel(Ma
                             if (MORE && half == 1)
 #pragma unroll
                                 for (uint32_t q = slot * LOADS / kSlots; q < (slot + 1) * LOADS / kSlots; ++q)
-                                    load_piece(t + 2, q);
+                                    load_piece(t + STAGES, at0, q);
 #pragma unroll
                             for (uint32_t q = slot * kReads / kSlots; q < (slot + 1) * kReads / kSlots; ++q)
-                                read_piece(t + half, half ^ 1, q);
+                                read_piece(half ? at1 : at0, half ^ 1, q);
                             if (half == 1 && slot + 1 == kSlots) {
                                 read_scales(kb + 1);
-                                touch(t + 3);
+                                touch(t + STAGES + 1);
                             }
                         }
                         __builtin_amdgcn_sched_barrier(0);
@@ -327,9 +329,11 @@ __global__ __launch_bounds__(kMThreads, (BM >= 256 ? 1 : 2)) void tile_kernel(Ma
                 }
             }
             take_scales(kb + 1);
+            at0 = at1;
+            at1 = at1 == (STAGES - 1) * kStageStep ? 0 : at1 + kStageStep;
         };
         uint32_t t = 0;
-        for (; t + 2 < blocks; ++t) step(t, std::true_type{});
+        for (; t + STAGES < blocks; ++t) step(t, std::true_type{});
         for (; t < blocks; ++t) step(t, std::false_type{});
     }
 
@@ -384,41 +388,289 @@ __global__ __launch_bounds__(kMThreads, (BM >= 256 ? 1 : 2)) void tile_kernel(Ma
     }
 }
 
+// The parts of a split contraction, added in order.
+template <typename T>
+__global__ __launch_bounds__(256) void add_parts_kernel(const float *parts, uint32_t splits, uint64_t stride, T *out,
+                                                        uint32_t m, uint32_t n, uint64_t ldo, const int32_t *offsets,
+                                                        uint32_t groups) {
+    // rows of no group have no parts and are left as they are
+    const uint32_t lo = offsets ? clamp_row(offsets[0], m) : 0u;
+    uint32_t hi = m;
+    if (offsets) {
+        uint32_t high = lo;
+        for (uint32_t g = lane_id(); g <= groups; g += kLanes) high = max(high, clamp_row(offsets[g], m));
+        hi = last_lane(scan_max(high));
+    }
+    const uint32_t per_row = (n + 3) / 4;
+    const uint64_t all = (uint64_t)(hi - lo) * per_row;
+    for (uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (uint64_t)gridDim.x * 256) {
+        const uint64_t r = lo + i / per_row;
+        const uint32_t c = (uint32_t)(i % per_row) * 4;
+        const float *src = parts + r * n + c;
+        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        const uint32_t k = min(n - c, 4u);
+        if (k == 4 && n % 4 == 0) {
+            for (uint32_t s = 0; s < splits; ++s) {
+                const u32v4 w = *reinterpret_cast<const u32v4 *>(src + s * stride);
+#pragma unroll
+                for (uint32_t j = 0; j < 4; ++j) v[j] += __uint_as_float(w[j]);
+            }
+        } else {
+            for (uint32_t s = 0; s < splits; ++s)
+                for (uint32_t j = 0; j < k; ++j) v[j] += src[s * stride + j];
+        }
+        T *o = out + r * ldo + c;
+        for (uint32_t j = 0; j < k; ++j) {
+            if constexpr (sizeof(T) == 2)
+                o[j] = bf_round(v[j]);
+            else
+                o[j] = __float_as_uint(v[j]);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// few rows: bound by reading the weights
+// ---------------------------------------------------------------------------
+
+typedef float f32v4 __attribute__((ext_vector_type(4)));
+
+// 16 rows of B against 16 MT rows of A.  The waves of a block take the blocks of
+// the contraction in turn, STEP at a time, straight from memory into the
+// registers of the matrix instructions (a row's 64 bytes by four lanes), and add
+// their sums through LDS.  Values are widened to BF16 with their scale, so the
+// products are exact; the conversions take a fraction of the time of the loads.
+template <uint32_t MT, uint32_t WAVES, uint32_t STEP, int FA, int FB, typename T>
+__global__ __launch_bounds__(WAVES * 64) void rows_kernel(MatArgs p) {
+    __shared__ f32v4 part[WAVES][MT][kLanes];
+    const uint32_t lane = lane_id(), wave = (uint32_t)__builtin_amdgcn_readfirstlane(threadIdx.x / kLanes);
+    const uint32_t ntiles = (p.n + 15) / 16, nt = blockIdx.x % ntiles, mt = blockIdx.x / ntiles;
+    const Span sp = find_tile(p.offsets, p.groups, p.rows, 16 * MT, [&](uint32_t) { return mt; });
+    if (!sp.found) return;
+    const uint32_t m0 = sp.begin + sp.tile * 16 * MT, m1 = sp.end, n0 = nt * 16;
+    const uint32_t fr = lane % 16, fc = 16 * (lane / 16);
+    const uint8_t *b = p.b + sp.group * p.b_group + (uint64_t)min(n0 + fr, p.n - 1) * p.ldb + fc;
+    const uint8_t *bs = p.bs + sp.group * p.bs_group + (uint64_t)(n0 >> p.b_shift) * p.ldbs;
+    const uint8_t *a[MT], *as[MT];
+#pragma unroll
+    for (uint32_t i = 0; i < MT; ++i) {
+        const uint64_t r = min(m0 + 16 * i + fr, m1 - 1);
+        a[i] = p.a + r * p.lda + fc;
+        as[i] = p.as + r * p.ldas;
+    }
+    f32v4 acc[MT];
+#pragma unroll
+    for (uint32_t i = 0; i < MT; ++i) acc[i] = f32v4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (uint32_t kb = wave * STEP; kb < p.blocks; kb += WAVES * STEP) {
+        // STEP blocks: their scales are bytes of one dword
+        const uint32_t sb = *reinterpret_cast<const uint32_t *>(bs + (kb & ~3u)) >> (8 * (kb & 3));
+        u32v4 fb[STEP][2], fa[STEP][MT][2];
+        uint32_t sa[MT];
+#pragma unroll
+        for (uint32_t u = 0; u < STEP; ++u) {
+            const uint64_t at = (uint64_t)min(kb + u, p.blocks - 1) * kBlock;
+#pragma unroll
+            for (uint32_t h = 0; h < 2; ++h) {
+                fb[u][h] = *reinterpret_cast<const u32v4 *>(b + at + 64 * h);
+#pragma unroll
+                for (uint32_t i = 0; i < MT; ++i) fa[u][i][h] = *reinterpret_cast<const u32v4 *>(a[i] + at + 64 * h);
+            }
+        }
+#pragma unroll
+        for (uint32_t i = 0; i < MT; ++i) sa[i] = *reinterpret_cast<const uint32_t *>(as[i] + (kb & ~3u)) >> (8 * (kb & 3));
+#pragma unroll
+        for (uint32_t u = 0; u < STEP; ++u) {
+            if (kb + u >= p.blocks) break;
+            bf16v8 wb[4];
+            widen<FB>(join(fb[u]), (sb >> (8 * u)) & 0xFFu, wb);
+#pragma unroll
+            for (uint32_t i = 0; i < MT; ++i) {
+                bf16v8 wa[4];
+                widen<FA>(join(fa[u][i]), (sa[i] >> (8 * u)) & 0xFFu, wa);
+#pragma unroll
+                for (uint32_t q = 0; q < 4; ++q)
+                    acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[q], wa[q], acc[i], 0, 0, 0);
+            }
+        }
+    }
+#pragma unroll
+    for (uint32_t i = 0; i < MT; ++i) part[wave][i][lane] = acc[i];
+    __syncthreads();
+    for (uint32_t i = wave; i < MT; i += WAVES) {
+        f32v4 v = part[0][i][lane];
+#pragma unroll
+        for (uint32_t w = 1; w < WAVES; ++w) v += part[w][i][lane];
+        // a lane holds four consecutive columns of one row
+        const uint32_t r = m0 + 16 * i + fr, c = n0 + 4 * (lane / 16);
+        if (r < m1) {
+            T *o = static_cast<T *>(p.out) + (uint64_t)r * p.ldo + c;
+#pragma unroll
+            for (uint32_t j = 0; j < 4; ++j)
+                if (c + j < p.n) {
+                    if constexpr (sizeof(T) == 2)
+                        o[j] = bf_round(v[j]);
+                    else
+                        o[j] = __float_as_uint(v[j]);
+                }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// which kernel
+// ---------------------------------------------------------------------------
+
+// kTile128: two workgroups on a CU, two stages each; kTile128Deep: one, three stages.
+enum Shape { kTile128, kTile128Deep, kTile256x128, kTile256 };
+
 template <bool WGRAD, int FA, int FB, typename T>
-static void launch_tile(const MatArgs &p, bool full, bool large, uint32_t grid, hipStream_t st) {
+static void launch_tile(const MatArgs &p, bool full, Shape shape, dim3 grid, hipStream_t st) {
+    const dim3 block(kMThreads);
     if (full)
-        hipLaunchKernelGGL((tile_kernel<128, 128, WGRAD, FA, FB, true, T>), dim3(grid), dim3(kMThreads), 0, st, p);
-    else if (large)
-        hipLaunchKernelGGL((tile_kernel<256, 256, WGRAD, FA, FB, false, T>), dim3(grid), dim3(kMThreads), 0, st, p);
+        hipLaunchKernelGGL((tile_kernel<128, 128, 2, WGRAD, FA, FB, true, T>), grid, block, 0, st, p);
+    else if (shape == kTile256)
+        hipLaunchKernelGGL((tile_kernel<256, 256, 2, WGRAD, FA, FB, false, T>), grid, block, 0, st, p);
+    else if (!WGRAD && shape == kTile256x128)
+        hipLaunchKernelGGL((tile_kernel<256, 128, 3, WGRAD, FA, FB, false, T>), grid, block, 0, st, p);
+    else if (!WGRAD && shape == kTile128Deep)
+        hipLaunchKernelGGL((tile_kernel<128, 128, 3, WGRAD, FA, FB, false, T>), grid, block, 0, st, p);
     else
-        hipLaunchKernelGGL((tile_kernel<128, 128, WGRAD, FA, FB, false, T>), dim3(grid), dim3(kMThreads), 0, st, p);
+        hipLaunchKernelGGL((tile_kernel<128, 128, 2, WGRAD, FA, FB, false, T>), grid, block, 0, st, p);
 }
 
-template <bool WGRAD, int FA, int FB>
-static void launch_out(const MatArgs &p, bool bf16, bool full, bool large, uint32_t grid, hipStream_t st) {
+template <int FA, int FB, typename T>
+static void launch_rows(const MatArgs &p, uint32_t mt, dim3 grid, hipStream_t st) {
+    if (mt == 1)
+        hipLaunchKernelGGL((rows_kernel<1, 8, 4, FA, FB, T>), grid, dim3(512), 0, st, p);
+    else
+        hipLaunchKernelGGL((rows_kernel<2, 8, 4, FA, FB, T>), grid, dim3(512), 0, st, p);
+}
+
+// Upper bound of the tiles of `tile` rows over all groups.
+static uint64_t row_tiles(uint64_t rows, uint64_t groups, uint64_t tile) {
+    return rows / tile + (rows < groups ? rows : groups);
+}
+
+struct Choice {
+    uint32_t rows_mt;  // > 0: rows_kernel with this many 16-row tiles
+    Shape shape;
+    uint32_t splits;
+};
+
+// Few rows a group: rows_kernel.  At n = 4096, k = 7168 it takes 6.9 us for 1 row
+// (tiles 12.2), 8.8 for 16 (13.7), 12.7 for 32 (14.9), 19.6 for 64 (16.0); with 8
+// groups of 1 row 34 (57), of 16 rows 53 (58), with 32 groups of 16 rows 236 (200).
+// Else the shape with the least time by this model: a round of workgroups over the
+// 256 CUs takes, for each block of the contraction, 1.2 us with tiles of 256 x 256,
+// 0.85 with 256 x 128, 0.55 with 128 x 128 alone on a CU, and 1.1 with two of those
+// on it (512 x 4096 x 7168: 67, 45, 29, 40 us; 4096 x 4096 x 7168: 92, 117, 137,
+// 122), and 4 to 9 us for its start and end.  With few tiles of 128 x 128 the contraction is split, at the cost of
+// writing and adding the parts (4 us and their bytes).  Groups are taken to have equally many rows.
+static Choice choose(uint64_t m, uint64_t n, uint64_t k, uint64_t groups, bool full) {
+    Choice c = {0, kTile128, 1};
+    const uint64_t used = m < groups ? m : groups, per_group = used ? ceil_div(m, used) : 0;
+    if (per_group <= 12 || (used == 1 && per_group <= 32)) {
+        c.rows_mt = per_group <= 16 ? 1 : 2;
+        return c;
+    }
+    const double blocks = (double)ceil_div(k, kBlock);
+    const auto tiles = [&](uint64_t tm, uint64_t tn) { return used * ceil_div(per_group, tm) * ceil_div(n, tn); };
+    const auto time = [](uint64_t t, uint64_t at_once, double us) { return (double)ceil_div(t, at_once) * us; };
+    const uint64_t t128 = tiles(128, 128);
+    double best = time(t128, 512, 1.1 * blocks + 4.0);
+    const auto offer = [&](Shape shape, uint32_t splits, double us) {
+        if (us < best) {
+            best = us;
+            c.shape = shape;
+            c.splits = splits;
+        }
+    };
+    if (!full) {
+        offer(kTile256, 1, time(tiles(256, 256), 256, 1.2 * blocks + 9.0));
+        offer(kTile256x128, 1, time(tiles(256, 128), 256, 0.85 * blocks + 6.0));
+        offer(kTile128Deep, 1, time(t128, 256, 0.55 * blocks + 4.0));
+    }
+    for (uint32_t s = 2; s <= 8; s *= 2) {
+        const uint64_t bytes = m * n * 4 * s;
+        if (bytes > ZC_FP8_MATMUL_WORKSPACE_MAX || blocks < 4 * s) break;
+        const double add = 4.0 + 2.0 * (double)bytes / 4.0e6;
+        if (full)
+            offer(kTile128, s, time(t128 * s, 512, 1.1 * blocks / s + 4.0) + add);
+        else
+            offer(kTile128Deep, s, time(t128 * s, 256, 0.55 * blocks / s + 4.0) + add);
+    }
+    return c;
+}
+
+template <int FA, int FB>
+static void launch_forward(MatArgs p, bool bf16, bool full, const Choice &c, float *ws, dim3 grid, hipStream_t st) {
+    if (c.rows_mt) {
+        if (bf16)
+            launch_rows<FA, FB, uint16_t>(p, c.rows_mt, grid, st);
+        else
+            launch_rows<FA, FB, uint32_t>(p, c.rows_mt, grid, st);
+        return;
+    }
+    if (c.splits == 1) {
+        if (bf16)
+            launch_tile<false, FA, FB, uint16_t>(p, full, c.shape, grid, st);
+        else
+            launch_tile<false, FA, FB, uint32_t>(p, full, c.shape, grid, st);
+        return;
+    }
+    void *out = p.out;
+    const uint64_t ldo = p.ldo;
+    p.out = ws;
+    p.ldo = p.n;
+    p.split_stride = (uint64_t)p.rows * p.n;
+    grid.y = c.splits;
+    launch_tile<false, FA, FB, uint32_t>(p, full, c.shape, grid, st);
+    const uint64_t units = ceil_div((uint64_t)p.rows * ceil_div(p.n, 4), 256);
+    const dim3 add((uint32_t)(units < 4096 ? units : 4096));
     if (bf16)
-        launch_tile<WGRAD, FA, FB, uint16_t>(p, full, large, grid, st);
+        hipLaunchKernelGGL(add_parts_kernel<uint16_t>, add, dim3(256), 0, st, ws, c.splits, p.split_stride,
+                           static_cast<uint16_t *>(out), p.rows, p.n, ldo, p.offsets, p.groups);
     else
-        launch_tile<WGRAD, FA, FB, uint32_t>(p, full, large, grid, st);
+        hipLaunchKernelGGL(add_parts_kernel<uint32_t>, add, dim3(256), 0, st, ws, c.splits, p.split_stride,
+                           static_cast<uint32_t *>(out), p.rows, p.n, ldo, p.offsets, p.groups);
 }
 
-template <bool WGRAD>
-static uint64_t tiles_of(const MatArgs &p, uint32_t tile) {
-    const uint64_t mtiles = WGRAD ? ceil_div(p.m, tile) * p.groups : p.rows / tile + (p.rows < p.groups ? p.rows : p.groups);
-    return ceil_div(p.n, tile) * mtiles;
-}
-
-template <bool WGRAD>
-static zc_status launch(const MatArgs &p, uint32_t ta, uint32_t tb, bool bf16, bool full, hipStream_t st) {
-    const bool large = !full && tiles_of<WGRAD>(p, 256) >= 192;
-    const uint64_t tiles = tiles_of<WGRAD>(p, large ? 256 : 128);
-    if (tiles > 0xFFFFF0u) return ZC_ERR_INVALID_ARG;
-    const uint32_t grid = (uint32_t)ceil_div(tiles, 256) * 256;
+static zc_status launch_forward(const MatArgs &p, uint32_t ta, uint32_t tb, bool bf16, bool full, Choice c, float *ws,
+                                hipStream_t st) {
+    if (!ws) c.splits = 1;
+    const uint64_t tm = c.rows_mt ? 16 * c.rows_mt : c.shape == kTile128 || c.shape == kTile128Deep ? 128 : 256;
+    const uint64_t tn = c.rows_mt ? 16 : c.shape == kTile256 ? 256 : 128;
+    const uint64_t tiles = row_tiles(p.rows, p.groups, tm) * ceil_div(p.n, tn);
+    const uint32_t threads = c.rows_mt ? 512 : kMThreads;
+    if (tiles > 0xFFFFFFFFull / threads - 256) return ZC_ERR_INVALID_ARG;
+    const dim3 grid((uint32_t)(c.rows_mt ? tiles : ceil_div(tiles, 8) * 8));
     const int fa = ta == ZC_FP8_E5M2, fb = tb == ZC_FP8_E5M2;
-    if (!fa && !fb) launch_out<WGRAD, 0, 0>(p, bf16, full, large, grid, st);
-    if (!fa && fb) launch_out<WGRAD, 0, 1>(p, bf16, full, large, grid, st);
-    if (fa && !fb) launch_out<WGRAD, 1, 0>(p, bf16, full, large, grid, st);
-    if (fa && fb) launch_out<WGRAD, 1, 1>(p, bf16, full, large, grid, st);
+    if (!fa && !fb) launch_forward<0, 0>(p, bf16, full, c, ws, grid, st);
+    if (!fa && fb) launch_forward<0, 1>(p, bf16, full, c, ws, grid, st);
+    if (fa && !fb) launch_forward<1, 0>(p, bf16, full, c, ws, grid, st);
+    if (fa && fb) launch_forward<1, 1>(p, bf16, full, c, ws, grid, st);
+    return launched();
+}
+
+template <int FA, int FB>
+static void launch_wgrad(const MatArgs &p, bool bf16, bool full, Shape shape, dim3 grid, hipStream_t st) {
+    if (bf16)
+        launch_tile<true, FA, FB, uint16_t>(p, full, shape, grid, st);
+    else
+        launch_tile<true, FA, FB, uint32_t>(p, full, shape, grid, st);
+}
+
+static zc_status launch_wgrad(const MatArgs &p, uint32_t ta, uint32_t tb, bool bf16, bool full, hipStream_t st) {
+    const uint64_t t256 = ceil_div(p.m, 256) * ceil_div(p.n, 256) * p.groups;
+    const Shape shape = !full && t256 >= 192 ? kTile256 : kTile128;
+    const uint64_t tiles = shape == kTile256 ? t256 : ceil_div(p.m, 128) * ceil_div(p.n, 128) * p.groups;
+    if (tiles > 0xFFFF00u) return ZC_ERR_INVALID_ARG;
+    const dim3 grid((uint32_t)ceil_div(tiles, 256) * 256);
+    const int fa = ta == ZC_FP8_E5M2, fb = tb == ZC_FP8_E5M2;
+    if (!fa && !fb) launch_wgrad<0, 0>(p, bf16, full, shape, grid, st);
+    if (!fa && fb) launch_wgrad<0, 1>(p, bf16, full, shape, grid, st);
+    if (fa && !fb) launch_wgrad<1, 0>(p, bf16, full, shape, grid, st);
+    if (fa && fb) launch_wgrad<1, 1>(p, bf16, full, shape, grid, st);
     return launched();
 }
 
@@ -435,11 +687,13 @@ static bool types_ok(uint32_t ta, uint32_t tb, uint32_t to, uint32_t sum) {
 using namespace zc::moe;
 
 extern "C" uint64_t zc_fp8_matmul_workspace_bytes(uint64_t m, uint64_t n, uint64_t k, uint32_t groups) {
-    (void)m;
-    (void)n;
-    (void)k;
-    (void)groups;
-    return 0;
+    if (m > kMaxRows || n > kMaxCols || k > kMaxContraction || groups == 0 || groups > ZC_MAX_EXPERTS || !m || !n) return 0;
+    uint64_t most = 0;
+    for (int full = 0; full < 2; ++full) {
+        const Choice c = choose(m, n, k, groups, full != 0);
+        if (c.splits > 1 && m * n * 4 * c.splits > most) most = m * n * 4 * c.splits;
+    }
+    return most;
 }
 
 extern "C" zc_status zc_fp8_matmul(const void *d_a, const uint8_t *d_a_scales, uint32_t a_type, uint64_t m,
@@ -447,7 +701,6 @@ extern "C" zc_status zc_fp8_matmul(const void *d_a, const uint8_t *d_a_scales, u
                                    uint64_t k, uint32_t groups, const int32_t *d_offsets, void *d_out,
                                    uint32_t out_type, uint64_t out_stride, uint32_t sum_mode,
                                    void *d_workspace, uint64_t workspace_bytes, void *stream) {
-    (void)workspace_bytes;
     if (!types_ok(a_type, b_type, out_type, sum_mode) || m > kMaxRows || n > kMaxCols || k > kMaxContraction || groups == 0 ||
         groups > ZC_MAX_EXPERTS || (!d_offsets && groups != 1) || out_stride < n || out_stride > kMaxStride)
         return ZC_ERR_INVALID_ARG;
@@ -473,8 +726,11 @@ extern "C" zc_status zc_fp8_matmul(const void *d_a, const uint8_t *d_a_scales, u
     p.blocks = (uint32_t)ceil_div(k, kBlock);
     p.groups = groups;
     p.b_shift = 7;
-    return launch<false>(p, a_type, b_type, out_type == ZC_BF16, sum_mode == ZC_FP8_SUM_FULL,
-                         static_cast<hipStream_t>(stream));
+    const bool full = sum_mode == ZC_FP8_SUM_FULL;
+    const Choice c = choose(m, n, k, groups, full);
+    const bool room = d_workspace && workspace_bytes >= zc_fp8_matmul_workspace_bytes(m, n, k, groups);
+    return launch_forward(p, a_type, b_type, out_type == ZC_BF16, full, c,
+                          room ? static_cast<float *>(d_workspace) : nullptr, static_cast<hipStream_t>(stream));
 }
 
 extern "C" zc_status zc_fp8_matmul_wgrad(const void *d_a, const uint8_t *d_a_scales, uint32_t a_type, uint64_t n,
@@ -508,6 +764,6 @@ extern "C" zc_status zc_fp8_matmul_wgrad(const void *d_a, const uint8_t *d_a_sca
     p.rows = (uint32_t)rows;
     p.groups = groups;
     p.b_shift = 0;
-    return launch<true>(p, a_type, b_type, out_type == ZC_BF16, sum_mode == ZC_FP8_SUM_FULL,
-                         static_cast<hipStream_t>(stream));
+    return launch_wgrad(p, a_type, b_type, out_type == ZC_BF16, sum_mode == ZC_FP8_SUM_FULL,
+                        static_cast<hipStream_t>(stream));
 }
