@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import ctypes
 
-from .zc import _check, _lib, _ptr, _stream, ZcError  # noqa: F401  (raises when libzc.so is not built)
+from .zc import ZC_OK, _lib, ZcError  # noqa: F401  (raises when libzc.so is not built)
 
 ZC_F32, ZC_BF16, ZC_FP8_E4M3, ZC_FP8_E5M2 = range(4)
 ZC_SCORE_SOFTMAX, ZC_SCORE_SIGMOID = range(2)
@@ -27,6 +27,31 @@ class zc_route_config(ctypes.Structure):
     _fields_ = [("experts", ctypes.c_uint32), ("top_k", ctypes.c_uint32), ("score", ctypes.c_uint32),
                 ("groups", ctypes.c_uint32), ("group_top", ctypes.c_uint32), ("group_score", ctypes.c_uint32),
                 ("renormalise", ctypes.c_uint32), ("scale", ctypes.c_float)]
+
+
+# The calls of a serving step take a few microseconds: no object is made for the
+# current stream, and nothing is imported, once torch is loaded.
+_raw_stream = _device = None
+
+
+def _stream(s) -> int:
+    global _raw_stream, _device
+    if s is None:
+        if _raw_stream is None:
+            import torch
+            torch.cuda.current_stream()  # initialises the device
+            _raw_stream, _device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+        return _raw_stream(_device())
+    return s if isinstance(s, int) else int(s.cuda_stream)
+
+
+def _ptr(x):
+    return x if x is None or isinstance(x, int) else x.data_ptr()
+
+
+def _check(rc: int, where: str) -> None:
+    if rc != ZC_OK:
+        raise ZcError(rc, where)
 
 
 _P, _U32, _U64, _CFG = ctypes.c_void_p, ctypes.c_uint32, ctypes.c_uint64, ctypes.POINTER(zc_route_config)
