@@ -117,47 +117,48 @@ struct TransArgs {
     uint32_t rows, cols, groups, col_tiles;
 };
 
-constexpr uint32_t kTCols = 64;
+// Columns of a tile: 128 bytes of a source row.
+template <uint32_t SRC>
+constexpr uint32_t kTCols = SRC == ZC_BF16 ? 64 : 128;
 
-// A tile of one block of 128 tokens and 64 columns: read by rows into LDS as
-// BF16 (an 8-bit checkpoint's values fit BF16: 4 bits of mantissa, and the
-// exponents of BF16), quantised by columns (four threads a column, 32 tokens each), and
-// written as 128 consecutive bytes a column.  Rows past the group's end are
-// zeros.
+// A tile of one block of 128 tokens and 64 (8-bit source: 128) columns: read by
+// rows, whole lines, into LDS as BF16 (an 8-bit checkpoint's values fit BF16: few
+// digits, and the exponents of BF16), and quantised by columns: eight lanes a
+// column, 16 tokens each, which then write its 128 bytes as one line.  (Four
+// threads a column in four waves, 32 bytes each: 1.2 and 1.5 times as long.)
+// Rows past the group's end are zeros.
 template <uint32_t SRC, uint32_t TYPE, bool WIDE>
 __global__ __launch_bounds__(kQThreads) void quantize_t_kernel(TransArgs a) {
-    __shared__ uint16_t tile[kBlock][kTCols + 2];
-    __shared__ uint32_t part[4][kTCols];
+    constexpr uint32_t COLS = kTCols<SRC>;
+    __shared__ uint16_t tile[kBlock][COLS + 2];
     const uint32_t tid = threadIdx.x;
     const uint32_t ct = blockIdx.x % a.col_tiles, t = blockIdx.x / a.col_tiles;
     const Span sp = find_tile(a.offsets, a.groups, a.rows, kBlock, [&](uint32_t) { return t; });
     if (!sp.found) return;
-    const uint32_t row0 = sp.begin + sp.tile * kBlock, c0 = ct * kTCols;
+    const uint32_t row0 = sp.begin + sp.tile * kBlock, c0 = ct * COLS;
     const uint32_t rows = min(sp.end - row0, kBlock);
-    if (SRC == ZC_BF16) {
-        const uint16_t *x = static_cast<const uint16_t *>(a.x);
 #pragma unroll
-        for (uint32_t j = 0; j < kBlock / 32; ++j) {
-            const uint32_t r = j * 32 + tid / 8, c = (tid % 8) * 8;
+    for (uint32_t j = 0; j < kBlock / 32; ++j) {
+        const uint32_t r = j * 32 + tid / 8;
+        if (SRC == ZC_BF16) {
+            const uint16_t *x = static_cast<const uint16_t *>(a.x);
+            const uint32_t c = (tid % 8) * 8;
             u32v4 w = {0u, 0u, 0u, 0u};
             if (r < rows && c0 + c < a.cols) w = load8<WIDE>(x + (uint64_t)(row0 + r) * a.xs, c0 + c, a.cols);
 #pragma unroll
             for (uint32_t i = 0; i < 4; ++i) *reinterpret_cast<uint32_t *>(&tile[r][c + 2 * i]) = w[i];
-        }
-    } else {
-        const uint8_t *x = static_cast<const uint8_t *>(a.x);
-#pragma unroll
-        for (uint32_t j = 0; j < kBlock / 32; ++j) {
-            const uint32_t r = j * 32 + tid / 8, c = (tid % 8) * 8;
-            u32v2 w = {0u, 0u};
-            float s = 0.0f;
-            if (r < rows && c0 + c < a.xs) {  // xs: the row's bytes, a multiple of 128, zeros past cols
-                w = *reinterpret_cast<const u32v2 *>(x + (uint64_t)(row0 + r) * a.xs + c0 + c);
-                s = scale_value(a.xscales[(uint64_t)(row0 + r) * a.xss + (c0 + c) / kBlock]);
-            }
+        } else {
             typedef Fp8<SRC == ZC_BF16 ? ZC_FP8_E4M3 : SRC> F;
+            const uint8_t *x = static_cast<const uint8_t *>(a.x);
+            const uint32_t c = (tid % 8) * 16;
+            u32v4 w = {0u, 0u, 0u, 0u};
+            float s = 0.0f;
+            if (r < rows) {  // xs: the row's bytes, a multiple of 128, zeros past cols
+                w = __builtin_nontemporal_load(reinterpret_cast<const u32v4 *>(x + (uint64_t)(row0 + r) * a.xs + c0 + c));
+                s = scale_value(a.xscales[(uint64_t)(row0 + r) * a.xss + c0 / kBlock]);
+            }
 #pragma unroll
-            for (uint32_t i = 0; i < 2; ++i) {
+            for (uint32_t i = 0; i < 4; ++i) {
                 *reinterpret_cast<uint32_t *>(&tile[r][c + 4 * i]) =
                     bf_pack(F::template value<0>(w[i]) * s, F::template value<1>(w[i]) * s);
                 *reinterpret_cast<uint32_t *>(&tile[r][c + 4 * i + 2]) =
@@ -166,33 +167,28 @@ __global__ __launch_bounds__(kQThreads) void quantize_t_kernel(TransArgs a) {
         }
     }
     __syncthreads();
-    const uint32_t c = tid % kTCols, quarter = tid / kTCols;
-    uint32_t v[16];
-    uint32_t m = 0;
+    const uint32_t block = sp.blocks0 + sp.tile, piece = tid % 8;
 #pragma unroll
-    for (uint32_t i = 0; i < 16; ++i) {
-        v[i] = tile[quarter * 32 + 2 * i][c] | ((uint32_t)tile[quarter * 32 + 2 * i + 1][c] << 16);
-        m = finite_max(m, v[i]);
-    }
-    part[quarter][c] = m;
-    __syncthreads();
-    m = max(max(part[0][c], part[1][c]), max(part[2][c], part[3][c]));
-    const uint32_t byte = scale_byte(m, Fp8<TYPE>::kTop);
-    const float inv = scale_inverse(byte);
-    if (c0 + c < a.cols) {
-        const uint32_t block = sp.blocks0 + sp.tile;
-        uint8_t *q = a.q + (uint64_t)(c0 + c) * a.qs + (uint64_t)block * kBlock + quarter * 32;
+    for (uint32_t j = 0; j < COLS / 32; ++j) {
+        const uint32_t c = j * 32 + tid / 8;
+        uint32_t v[8], m = 0;
 #pragma unroll
-        for (uint32_t i = 0; i < 2; ++i) {
+        for (uint32_t i = 0; i < 8; ++i) {
+            v[i] = tile[16 * piece + 2 * i][c] | ((uint32_t)tile[16 * piece + 2 * i + 1][c] << 16);
+            m = finite_max(m, v[i]);
+        }
+        m = group_max<8>(m);
+        const uint32_t byte = scale_byte(m, Fp8<TYPE>::kTop);
+        const float inv = scale_inverse(byte);
+        if (c0 + c < a.cols) {
             u32v4 w;
 #pragma unroll
-            for (uint32_t j = 0; j < 4; ++j) {
-                const uint32_t p0 = v[8 * i + 2 * j], p1 = v[8 * i + 2 * j + 1];
-                w[j] = Fp8<TYPE>::pack4(bf_lo(p0) * inv, bf_hi(p0) * inv, bf_lo(p1) * inv, bf_hi(p1) * inv);
-            }
-            *reinterpret_cast<u32v4 *>(q + 16 * i) = w;
+            for (uint32_t i = 0; i < 4; ++i)
+                w[i] = Fp8<TYPE>::pack4(bf_lo(v[2 * i]) * inv, bf_hi(v[2 * i]) * inv, bf_lo(v[2 * i + 1]) * inv,
+                                        bf_hi(v[2 * i + 1]) * inv);
+            *reinterpret_cast<u32v4 *>(a.q + (uint64_t)(c0 + c) * a.qs + (uint64_t)block * kBlock + 16 * piece) = w;
+            if (piece == 0) a.scales[(uint64_t)(c0 + c) * a.ss + block] = (uint8_t)byte;
         }
-        if (quarter == 0) a.scales[(uint64_t)(c0 + c) * a.ss + block] = (uint8_t)byte;
     }
 }
 
@@ -317,7 +313,7 @@ extern "C" zc_status zc_fp8_quantize_t(const void *d_x, const uint8_t *d_x_scale
         return ZC_ERR_MISALIGNED;
     TransArgs a = {d_x, d_x_scales, d_offsets, static_cast<uint8_t *>(d_q), d_scales, x_stride, scale_stride(cols),
                    padded_rows, scale_stride(padded_rows), (uint32_t)rows, (uint32_t)cols, groups,
-                   (uint32_t)ceil_div(cols, kTCols)};
+                   (uint32_t)ceil_div(cols, x_type == ZC_BF16 ? kTCols<ZC_BF16> : kTCols<ZC_FP8_E4M3>)};
     const uint64_t grid = zc_fp8_padded_rows(rows, groups) / kBlock * a.col_tiles;
     if (grid > 0xFFFFFFu) return ZC_ERR_INVALID_ARG;  // 2^24 blocks of 256 threads: the launch limit
     const bool wide = aligned(d_x, 16) && x_stride % 8 == 0 && cols % 8 == 0;
