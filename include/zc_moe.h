@@ -35,7 +35,7 @@
  *     checked there: one out of range is treated as the description of the call
  *     says, and never read or written through.
  * Alignment: 2-byte elements need 2-byte, 4-byte elements 4-byte aligned
- * buffers; 8-bit arrays, weights' scales and workspaces 16-byte.  BF16 arrays
+ * buffers, as do scales; 8-bit arrays and workspaces 16-byte.  BF16 arrays
  * that start on 16 bytes with row lengths and strides that are multiples of 8
  * take the wide path.
  *

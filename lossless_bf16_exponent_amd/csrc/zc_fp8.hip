@@ -125,7 +125,7 @@ constexpr uint32_t kTCols = SRC == ZC_BF16 ? 64 : 128;
 // rows, whole lines, into LDS as BF16 (an 8-bit checkpoint's values fit BF16: few
 // digits, and the exponents of BF16), and quantised by columns: eight lanes a
 // column, 16 tokens each, which then write its 128 bytes as one line.  (Four
-// threads a column in four waves, 32 bytes each: 1.2 and 1.5 times as long.)
+// threads a column in four waves, 32 bytes each: 1.3 and 1.2 times as long.)
 // Rows past the group's end are zeros.
 template <uint32_t SRC, uint32_t TYPE, bool WIDE>
 __global__ __launch_bounds__(kQThreads) void quantize_t_kernel(TransArgs a) {
@@ -283,7 +283,7 @@ extern "C" zc_status zc_fp8_quantize(const void *d_x, uint64_t rows, uint64_t co
         return ZC_ERR_INVALID_ARG;
     if (!rows || !cols) return ZC_OK;
     if (!d_x || !d_q || !d_scales) return ZC_ERR_INVALID_ARG;
-    if (!aligned(d_x, 2) || !aligned(d_q, 16) || !aligned(d_scales, 16)) return ZC_ERR_MISALIGNED;
+    if (!aligned(d_x, 2) || !aligned(d_q, 16) || !aligned(d_scales, 4)) return ZC_ERR_MISALIGNED;
     const QuantArgs a = {static_cast<const uint16_t *>(d_x), static_cast<uint8_t *>(d_q), d_scales, x_stride,
                          stride8(cols), scale_stride(cols), (uint32_t)rows, (uint32_t)cols,
                          (uint32_t)ceil_div(cols, kBlock)};
@@ -308,7 +308,7 @@ extern "C" zc_status zc_fp8_quantize_t(const void *d_x, const uint8_t *d_x_scale
     if (padded_rows < zc_fp8_padded_rows(rows, groups)) return ZC_ERR_CAPACITY;
     if (!rows || !cols) return ZC_OK;
     if (!d_x || !d_q || !d_scales || (x_type != ZC_BF16 && !d_x_scales)) return ZC_ERR_INVALID_ARG;
-    if (!aligned(d_x, x_type == ZC_BF16 ? 2 : 16) || !aligned(d_q, 16) || !aligned(d_scales, 16) ||
+    if (!aligned(d_x, x_type == ZC_BF16 ? 2 : 16) || !aligned(d_x_scales, x_type == ZC_BF16 ? 1 : 4) || !aligned(d_q, 16) || !aligned(d_scales, 4) ||
         !aligned(d_offsets, 4))
         return ZC_ERR_MISALIGNED;
     TransArgs a = {d_x, d_x_scales, d_offsets, static_cast<uint8_t *>(d_q), d_scales, x_stride, scale_stride(cols),
@@ -332,7 +332,7 @@ extern "C" zc_status zc_fp8_transpose(const void *d_q, const uint8_t *d_scales, 
     if (rows > kMaxCols || cols > kMaxCols || batch > ZC_MAX_EXPERTS) return ZC_ERR_INVALID_ARG;
     if (!batch || !rows || !cols) return ZC_OK;
     if (!d_q || !d_scales || !d_qt || !d_scales_t) return ZC_ERR_INVALID_ARG;
-    if (!aligned(d_q, 16) || !aligned(d_scales, 16) || !aligned(d_qt, 16) || !aligned(d_scales_t, 16))
+    if (!aligned(d_q, 16) || !aligned(d_scales, 4) || !aligned(d_qt, 16) || !aligned(d_scales_t, 4))
         return ZC_ERR_MISALIGNED;
     const SquareArgs a = {static_cast<const uint8_t *>(d_q), d_scales, static_cast<uint8_t *>(d_qt), d_scales_t,
                           (uint32_t)rows, (uint32_t)cols, (uint32_t)ceil_div(rows, kBlock),

@@ -706,7 +706,7 @@ extern "C" zc_status zc_fp8_matmul(const void *d_a, const uint8_t *d_a_scales, u
         return ZC_ERR_INVALID_ARG;
     if (!m || !n) return ZC_OK;
     if (!d_out || (k && (!d_a || !d_a_scales || !d_b || !d_b_scales))) return ZC_ERR_INVALID_ARG;
-    if (!aligned(d_a, 16) || !aligned(d_a_scales, 16) || !aligned(d_b, 16) || !aligned(d_b_scales, 16) ||
+    if (!aligned(d_a, 16) || !aligned(d_a_scales, 4) || !aligned(d_b, 16) || !aligned(d_b_scales, 4) ||
         !aligned(d_offsets, 4) || !aligned(d_out, out_type == ZC_F32 ? 4 : 2) || !aligned(d_workspace, 16))
         return ZC_ERR_MISALIGNED;
     MatArgs p = {};
@@ -745,7 +745,7 @@ extern "C" zc_status zc_fp8_matmul_wgrad(const void *d_a, const uint8_t *d_a_sca
     if (padded_rows < zc_fp8_padded_rows(rows, groups)) return ZC_ERR_CAPACITY;
     if (!n || !k) return ZC_OK;
     if (!d_out || (rows && (!d_a || !d_a_scales || !d_b || !d_b_scales))) return ZC_ERR_INVALID_ARG;
-    if (!aligned(d_a, 16) || !aligned(d_a_scales, 16) || !aligned(d_b, 16) || !aligned(d_b_scales, 16) ||
+    if (!aligned(d_a, 16) || !aligned(d_a_scales, 4) || !aligned(d_b, 16) || !aligned(d_b_scales, 4) ||
         !aligned(d_offsets, 4) || !aligned(d_out, out_type == ZC_F32 ? 4 : 2))
         return ZC_ERR_MISALIGNED;
     MatArgs p = {};

@@ -175,8 +175,8 @@ extern "C" zc_status zc_swiglu(const void *d_gate_up, uint64_t rows, uint64_t co
         return ZC_ERR_INVALID_ARG;
     if (!rows || !cols || (!d_h && !d_hq && !d_kept)) return ZC_OK;
     if (!d_gate_up) return ZC_ERR_INVALID_ARG;
-    if (!aligned(d_gate_up, 2) || !aligned(d_h, 2) || !aligned(d_hq, 16) || !aligned(d_hq_scales, 16) ||
-        !aligned(d_kept, 16) || !aligned(d_kept_scales, 16))
+    if (!aligned(d_gate_up, 2) || !aligned(d_h, 2) || !aligned(d_hq, 16) || !aligned(d_hq_scales, 4) ||
+        !aligned(d_kept, 16) || !aligned(d_kept_scales, 4))
         return ZC_ERR_MISALIGNED;
     GateArgs a = {};
     a.gu = static_cast<const uint16_t *>(d_gate_up);
@@ -209,7 +209,7 @@ extern "C" zc_status zc_swiglu_backward(const void *d_kept, const uint8_t *d_kep
         return ZC_ERR_INVALID_ARG;
     if (!rows || !cols) return ZC_OK;
     if (!d_kept || !d_kept_scales || !d_dh || !d_dgate_up) return ZC_ERR_INVALID_ARG;
-    if (!aligned(d_kept, 16) || !aligned(d_kept_scales, 16) || !aligned(d_dh, 2) || !aligned(d_dgate_up, 2))
+    if (!aligned(d_kept, 16) || !aligned(d_kept_scales, 4) || !aligned(d_dh, 2) || !aligned(d_dgate_up, 2))
         return ZC_ERR_MISALIGNED;
     GateArgs a = {};
     a.kept = static_cast<uint8_t *>(const_cast<void *>(d_kept));

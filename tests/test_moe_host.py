@@ -111,17 +111,17 @@ def refusals(moe):
     yield "zc_fp8_quantize", [P, 4, 200, 200, e4, 1, P, P, None], [
         (0, None, INVALID), (0, P + 1, MISALIGNED), (1, 1 << 31, INVALID), (3, 199, INVALID), (4, bf, INVALID),
         (4, 4, INVALID), (5, 2, INVALID), (6, None, INVALID), (6, P + 8, MISALIGNED), (7, None, INVALID),
-        (7, P + 4, MISALIGNED)]
+        (7, P + 2, MISALIGNED)]
     yield "zc_fp8_quantize_t", [P, P, e4, 300, 200, 256, 2, P, e4, P, P, 512, None], [
         (0, None, INVALID), (0, P + 2, MISALIGNED), (1, None, INVALID), (2, 0, INVALID), (5, 200, INVALID),
         (6, 0, INVALID), (6, 1025, INVALID), (7, None, INVALID), (7, P + 1, MISALIGNED), (8, 1, INVALID),
-        (9, None, INVALID), (9, P + 8, MISALIGNED), (10, P + 8, MISALIGNED), (11, 384, CAPACITY), (11, 513, INVALID)]
+        (9, None, INVALID), (9, P + 8, MISALIGNED), (10, P + 2, MISALIGNED), (11, 384, CAPACITY), (11, 513, INVALID)]
     yield "zc_fp8_transpose", [P, P, 2, 200, 300, P, P, None], [
         (0, None, INVALID), (0, P + 8, MISALIGNED), (1, None, INVALID), (2, 1025, INVALID), (3, 1 << 29, INVALID),
         (5, None, INVALID), (6, P + 1, MISALIGNED)]
     yield "zc_fp8_matmul", [P, P, e4, 16, P, P, e4, 64, 128, 2, P, P, bf, 64, 0, None, 0, None], [
         (0, None, INVALID), (0, P + 8, MISALIGNED), (1, None, INVALID), (2, bf, INVALID), (3, 1 << 31, INVALID),
-        (4, None, INVALID), (5, P + 4, MISALIGNED), (6, 0, INVALID), (7, 1 << 29, INVALID), (8, 1 << 29, INVALID),
+        (4, None, INVALID), (5, P + 2, MISALIGNED), (6, 0, INVALID), (7, 1 << 29, INVALID), (8, 1 << 29, INVALID),
         (9, 0, INVALID), (10, None, INVALID), (10, P + 2, MISALIGNED), (11, None, INVALID), (11, P + 1, MISALIGNED),
         (12, e4, INVALID), (13, 63, INVALID), (14, 2, INVALID), (15, P + 8, MISALIGNED)]
     yield "zc_fp8_matmul_wgrad", [P, P, e4, 64, P, P, e4, 64, 512, 300, 2, P, P, 0, 1, None], [
@@ -132,7 +132,7 @@ def refusals(moe):
         (0, None, INVALID), (0, P + 1, MISALIGNED), (1, 1 << 31, INVALID), (3, 127, INVALID), (4, P + 1, MISALIGNED),
         (5, 63, INVALID), (6, None, INVALID), (7, None, INVALID), (8, P + 8, MISALIGNED), (9, None, INVALID)]
     yield "zc_swiglu_backward", [P, P, 4, 64, P, 64, P, 128, None], [
-        (0, None, INVALID), (1, None, INVALID), (1, P + 8, MISALIGNED), (4, None, INVALID), (5, 63, INVALID),
+        (0, None, INVALID), (1, None, INVALID), (1, P + 2, MISALIGNED), (4, None, INVALID), (5, 63, INVALID),
         (6, P + 1, MISALIGNED), (7, 127, INVALID)]
 
 
