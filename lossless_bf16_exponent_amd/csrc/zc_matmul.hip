@@ -65,7 +65,7 @@ __device__ __forceinline__ f32v16 mfma(const i32v8 &a, const i32v8 &b, const f32
 }
 
 // ---------------------------------------------------------------------------
-// tiles: four waves, direct-to-LDS loads four stages deep
+// tiles of four waves, loads straight into LDS
 // ---------------------------------------------------------------------------
 
 typedef __attribute__((address_space(3))) void lds_void;
@@ -94,15 +94,25 @@ __device__ __forceinline__ void wait_and_meet() {
 template <uint32_t BM, uint32_t BN, uint32_t STAGES>
 struct TileShared {
     uint8_t stage[STAGES][(BM + BN) * kBlock];
-    uint32_t scale[2][BM + BN];  // four blocks' scale bytes of every row
+    uint32_t scale[2][4][2][kLanes];  // four blocks' scale bytes of the rows that a wave loads, of A and of B
     uint32_t touched[4][kLanes];  // what the touches of later blocks bring, never read
 };
 
 // BM x BN tile of four waves (2 x 2).  The fragments of half a block are in
 // registers while the other half's come out of LDS.  In the middle of a block
 // every wave holds the rest of it, and one barrier then frees its buffer for the
-// block STAGES after it and hands over the next one.  T: uint16_t for BF16 results, uint32_t for
-// floats.
+// block STAGES after it and hands over the next one.  Between two matrix
+// instructions stand a read and a load, so that neither stops them for long.
+// T: uint16_t for BF16 results, uint32_t for floats.
+//
+// Bound by the matrix instructions and the clock that they leave: 65536 x 4096 x
+// 7168 in 32 equal groups takes 1450 us, 2650 TFLOP/s, 8192 x 8192 x 8192 392 us,
+// 2800; the instructions alone, from registers, reach 3700 at the same power,
+// and a 256 x 256 tile spends 1.1 us a block when few are at work (its
+// instructions 0.85 at 2.4 GHz) and 1.4 when all are.  About 10 us of a tile are
+// its start and its end.  256 x 256 since a row's bytes then serve 256 columns:
+// 128 x 128 moves twice the bytes from the L2, at 64 bytes a clock and CU, and
+// takes 1.5 times as long.
 template <uint32_t BM, uint32_t BN, uint32_t STAGES, bool WGRAD, int FA, int FB, bool FULL, typename T>
 __global__ __launch_bounds__(kMThreads, (sizeof(TileShared<BM, BN, STAGES>) > 80 * 1024 ? 1 : 2)) void tile_kernel(MatArgs p) {
     constexpr uint32_t MT = BM / 64, NT = BN / 64;         // 32 x 32 tiles of a wave
@@ -188,7 +198,8 @@ __global__ __launch_bounds__(kMThreads, (sizeof(TileShared<BM, BN, STAGES>) > 80
         const uint32_t ldsb = lds0 + BM * kBlock + wave * (BN / 4) * kBlock;
         constexpr uint32_t kStageStep = (BM + BN) * kBlock;
 
-        // scales: four blocks of a row are a dword; rows of the wave: BM / 4 of A, BN / 4 of B, one a lane
+        // scales: four blocks of a row are a dword; rows of the wave: BM / 4 of A, BN / 4 of B, one a lane (the
+        // lanes past them repeat the last, in places of their own: a condition would be a branch in the loop)
         const uint8_t *sa0 = p.as + (uint64_t)m0 * p.ldas;
         const uint8_t *sb0 = bs + (uint64_t)(n0 >> p.b_shift) * p.ldbs;
         const uint32_t sra = wave * (BM / 4) + min(lane, BM / 4 - 1), srb = wave * (BN / 4) + min(lane, BN / 4 - 1);
@@ -196,9 +207,9 @@ __global__ __launch_bounds__(kMThreads, (sizeof(TileShared<BM, BN, STAGES>) > 80
         const uint32_t soffb = ((min(n0 + srb, p.n - 1) >> p.b_shift) - (n0 >> p.b_shift)) * (uint32_t)p.ldbs;
         const uint32_t ldss = (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void *)&sh.scale[0][0]);
         const auto load_scales = [&](uint32_t c) {  // blocks 4c .. 4c + 3
-            const uint32_t at = ldss + (c & 1) * (BM + BN) * 4;
-            if (lane < BM / 4) lds_load4(sa0 + 4 * c, soffa, at + wave * BM);
-            if (lane < BN / 4) lds_load4(sb0 + 4 * c, soffb, at + 4 * BM + wave * BN);
+            const uint32_t at = ldss + ((c & 1) * 4 + wave) * 2 * kLanes * 4;
+            lds_load4(sa0 + 4 * c, soffa, at);
+            lds_load4(sb0 + 4 * c, soffb, at + kLanes * 4);
         };
         // A touch brings one line per row of a later block into the L2: a quarter of A's rows and an eighth of B's, since
         // the four and eight tiles beside this one that share them touch the others.  Three blocks ahead: 3 % of the
@@ -243,9 +254,15 @@ __global__ __launch_bounds__(kMThreads, (sizeof(TileShared<BM, BN, STAGES>) > 80
         uint32_t wa4[MT], wb4[NT];  // four blocks' scales of the lane's rows
         const auto read_scales = [&](uint32_t kb) {
 #pragma unroll
-            for (uint32_t i = 0; i < MT; ++i) wa4[i] = sh.scale[kb / 4 & 1][wm + 32 * i + fr];
+            for (uint32_t i = 0; i < MT; ++i) {
+                const uint32_t r = wm + 32 * i + fr;
+                wa4[i] = sh.scale[kb / 4 & 1][r / (BM / 4)][0][r % (BM / 4)];
+            }
 #pragma unroll
-            for (uint32_t j = 0; j < NT; ++j) wb4[j] = sh.scale[kb / 4 & 1][BM + wn + 32 * j + fr];
+            for (uint32_t j = 0; j < NT; ++j) {
+                const uint32_t r = wn + 32 * j + fr;
+                wb4[j] = sh.scale[kb / 4 & 1][r / (BN / 4)][1][r % (BN / 4)];
+            }
         };
         const auto take_scales = [&](uint32_t kb) {  // block kb's in the low byte
 #pragma unroll
@@ -307,22 +324,19 @@ __global__ __launch_bounds__(kMThreads, (sizeof(TileShared<BM, BN, STAGES>) > 80
                             // B in the place of the left matrix: a lane then holds four consecutive columns of one row
                             acc[i][j] = mfma<FB, FA>(join(fb[half][j]), join(fa[half][i]), acc[i][j], eb[j], ea[i]);
                         }
-                        // between the matrix instructions of the first part of a half: the reads of the other half, and
-                        // the loads of the block after the next
+                        // between the matrix instructions: the reads of the other half, and the loads of block t + STAGES
                         constexpr uint32_t kSlots = MT * NT;
                         const uint32_t slot = i * NT + j;
-                        if (slot < kSlots) {
-                            if (MORE && half == 1)
+                        if (MORE && half == 1)
 #pragma unroll
-                                for (uint32_t q = slot * LOADS / kSlots; q < (slot + 1) * LOADS / kSlots; ++q)
-                                    load_piece(t + STAGES, at0, q);
+                            for (uint32_t q = slot * LOADS / kSlots; q < (slot + 1) * LOADS / kSlots; ++q)
+                                load_piece(t + STAGES, at0, q);
 #pragma unroll
-                            for (uint32_t q = slot * kReads / kSlots; q < (slot + 1) * kReads / kSlots; ++q)
-                                read_piece(half ? at1 : at0, half ^ 1, q);
-                            if (half == 1 && slot + 1 == kSlots) {
-                                read_scales(kb + 1);
-                                touch(t + STAGES + 1);
-                            }
+                        for (uint32_t q = slot * kReads / kSlots; q < (slot + 1) * kReads / kSlots; ++q)
+                            read_piece(half ? at1 : at0, half ^ 1, q);
+                        if (half == 1 && slot + 1 == kSlots) {
+                            read_scales(kb + 1);
+                            touch(t + STAGES + 1);
                         }
                         __builtin_amdgcn_sched_barrier(0);
                     }
