@@ -138,65 +138,34 @@ __global__ void plan_empty_kernel(int32_t *offsets, uint32_t n) {
 }
 
 // ---------------------------------------------------------------------------
-// rows of BF16: V values an access (8: 16 bytes; 1 for rows that are not
-// aligned for that)
+// rows of BF16, eight values an access
 // ---------------------------------------------------------------------------
 
 constexpr uint32_t kRowThreads = 256;
+constexpr uint32_t kRowStep = kRowThreads * 8;
 constexpr uint32_t kCopies = 8;  // copies of a token whose rows are on their way at once
 
-// V values as they lie in memory.
-template <uint32_t V>
-struct Raw;
-template <>
-struct Raw<8> {
-    u32v4 w;
-    __device__ __forceinline__ float value(uint32_t i) const { return (i & 1) ? bf_hi(w[i / 2]) : bf_lo(w[i / 2]); }
-    __device__ __forceinline__ void set(uint32_t i, float lo, float hi) { w[i / 2] = bf_pack(lo, hi); }
-};
-template <>
-struct Raw<1> {
-    uint16_t w;
-    __device__ __forceinline__ float value(uint32_t) const { return bf_one(w); }
-};
+__device__ __forceinline__ float value_of(const u32v4 &w, uint32_t i) { return (i & 1) ? bf_hi(w[i / 2]) : bf_lo(w[i / 2]); }
 
-// Rows that are read or written once carry the non-temporal hint (the weighted
-// sum of 8192 x 8 rows of 7168: 246 -> 213 us).
-template <uint32_t V>
-__device__ __forceinline__ Raw<V> load_once(const uint16_t *p) {
-    Raw<V> r;
-    if constexpr (V == 8)
-        r.w = __builtin_nontemporal_load(reinterpret_cast<const u32v4 *>(p));
-    else
-        r.w = __builtin_nontemporal_load(p);
-    return r;
+// A row that is read several times (by several blocks, or again for further
+// copies) is not marked for single use, as load_values does.
+template <bool WIDE>
+__device__ __forceinline__ u32v4 load_again(const uint16_t *p, uint32_t n) {
+    if (n >= 8) return WIDE ? *reinterpret_cast<const u32v4 *>(p) : *reinterpret_cast<const u32v4a2 *>(p);
+    return load_values<WIDE>(p, n);
 }
-template <uint32_t V>
-__device__ __forceinline__ Raw<V> load_row(const uint16_t *p) {
-    Raw<V> r;
-    if constexpr (V == 8)
-        r.w = *reinterpret_cast<const u32v4 *>(p);
-    else
-        r.w = *p;
-    return r;
-}
-template <uint32_t V>
-__device__ __forceinline__ void store_raw(uint16_t *p, const Raw<V> &r) {
-    if constexpr (V == 8)
-        *reinterpret_cast<u32v4 *>(p) = r.w;
-    else
-        *p = r.w;
-}
-template <uint32_t V>
-__device__ __forceinline__ Raw<V> pack_vals(const float (&v)[V]) {
-    Raw<V> r;
-    if constexpr (V == 8) {
-#pragma unroll
-        for (uint32_t i = 0; i < V; i += 2) r.set(i, v[i], v[i + 1]);
+// The copies' rows are written without the mark (with it the gradients of 8192 x
+// 8 rows took 1.3 times as long).
+template <bool WIDE>
+__device__ __forceinline__ void store_row(uint16_t *p, const u32v4 &w, uint32_t n) {
+    if (WIDE) {
+        if (n >= 8) *reinterpret_cast<u32v4 *>(p) = w;
     } else {
-        r.w = bf_round(v[0]);
+        store_values<false>(p, w, n);
     }
-    return r;
+}
+__device__ __forceinline__ u32v4 pack_values(const float (&v)[8]) {
+    return u32v4{bf_pack(v[0], v[1]), bf_pack(v[2], v[3]), bf_pack(v[4], v[5]), bf_pack(v[6], v[7])};
 }
 
 struct RowArgs {
@@ -218,32 +187,35 @@ __device__ __forceinline__ int32_t row_of(const RowArgs &a, uint64_t t, uint32_t
 }
 
 // The row is read once and written to each of its places.  Block (t, y): the
-// y-th 256 V values of the row and every gridDim.y-th after it.
-template <uint32_t V>
+// y-th 2048 values of the row and every gridDim.y-th after it.  Bound by memory:
+// 8192 x 8 rows of 7168 take 205 us, 5.2 TB/s.
+template <bool WIDE>
 __global__ __launch_bounds__(kRowThreads) void dispatch_kernel(RowArgs a) {
     for (uint64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
         const uint16_t *src = a.x + t * a.xs;
-        for (uint32_t h = (blockIdx.y * kRowThreads + threadIdx.x) * V; h < a.hidden; h += gridDim.y * kRowThreads * V) {
-            const Raw<V> w = load_row<V>(src + h);
+        for (uint32_t h = blockIdx.y * kRowStep + threadIdx.x * 8; h < a.hidden; h += gridDim.y * kRowStep) {
+            const u32v4 w = load_again<WIDE>(src + h, a.hidden - h);
             for (uint32_t k = 0; k < a.top_k; ++k) {
                 const int32_t p = row_of(a, t, k);
-                if (p >= 0) store_raw<V>(a.out + (uint64_t)p * a.os + h, w);
+                if (p >= 0) store_row<WIDE>(a.out + (uint64_t)p * a.os + h, w, a.hidden - h);
             }
         }
     }
 }
 
 // The sums stay in 32 bits, k ascending; eight copies' rows are on their way at
-// once.  Blocks as in dispatch_kernel.
-template <uint32_t V>
+// once, each marked for single use (8192 x 8 rows of 7168: 246 -> 214 us, 4.9 TB/s).
+// Blocks as in dispatch_kernel.
+template <bool WIDE>
 __global__ __launch_bounds__(kRowThreads) void combine_kernel(RowArgs a) {
     for (uint64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
-        for (uint32_t h = (blockIdx.y * kRowThreads + threadIdx.x) * V; h < a.hidden; h += gridDim.y * kRowThreads * V) {
-            float sum[V];
+        for (uint32_t h = blockIdx.y * kRowStep + threadIdx.x * 8; h < a.hidden; h += gridDim.y * kRowStep) {
+            const uint32_t n = a.hidden - h;
+            float sum[8];
 #pragma unroll
-            for (uint32_t i = 0; i < V; ++i) sum[i] = 0.0f;
+            for (uint32_t i = 0; i < 8; ++i) sum[i] = 0.0f;
             for (uint32_t k0 = 0; k0 < a.top_k; k0 += kCopies) {
-                Raw<V> z[kCopies];
+                u32v4 z[kCopies];
                 int32_t p[kCopies];
                 float w[kCopies];
 #pragma unroll
@@ -251,22 +223,23 @@ __global__ __launch_bounds__(kRowThreads) void combine_kernel(RowArgs a) {
 #pragma unroll
                 for (uint32_t j = 0; j < kCopies; ++j) {
                     w[j] = p[j] >= 0 && a.weights ? a.weights[t * a.top_k + k0 + j] : 1.0f;
-                    if (p[j] >= 0) z[j] = load_once<V>(a.x + (uint64_t)p[j] * a.xs + h);
+                    if (p[j] >= 0) z[j] = load_values<WIDE>(a.x + (uint64_t)p[j] * a.xs + h, n);
                 }
 #pragma unroll
                 for (uint32_t j = 0; j < kCopies; ++j)
                     if (p[j] >= 0)
 #pragma unroll
-                        for (uint32_t i = 0; i < V; ++i) sum[i] = fmaf(w[j], z[j].value(i), sum[i]);
+                        for (uint32_t i = 0; i < 8; ++i) sum[i] = fmaf(w[j], value_of(z[j], i), sum[i]);
             }
-            store_raw<V>(a.out + t * a.os + h, pack_vals<V>(sum));
+            store_row<WIDE>(a.out + t * a.os + h, pack_values(sum), n);
         }
     }
 }
 
 // One block a token: dz = w dy and the products <dy, z>, each copy's summed over
-// the block in an order fixed by the sizes.
-template <uint32_t V>
+// the block in an order fixed by the sizes.  Bound by memory: 8192 x 8 rows of
+// 7168 take 414 us, 5.1 TB/s.
+template <bool WIDE>
 __global__ __launch_bounds__(kRowThreads) void combine_backward_kernel(RowArgs a) {
     __shared__ float part[kRowThreads / kLanes][kCopies];
     const uint32_t lane = lane_id(), wave = threadIdx.x / kLanes;
@@ -281,28 +254,29 @@ __global__ __launch_bounds__(kRowThreads) void combine_backward_kernel(RowArgs a
                 w[j] = p[j] >= 0 && a.weights && a.out ? a.weights[t * a.top_k + k0 + j] : 1.0f;
                 dot[j] = 0.0f;
             }
-            for (uint32_t h = threadIdx.x * V; h < a.hidden; h += kRowThreads * V) {
-                const Raw<V> dy = load_row<V>(a.dy + t * a.dys + h);
-                Raw<V> z[kCopies];
+            for (uint32_t h = threadIdx.x * 8; h < a.hidden; h += kRowStep) {
+                const uint32_t n = a.hidden - h;
+                const u32v4 dy = load_again<WIDE>(a.dy + t * a.dys + h, n);
+                u32v4 z[kCopies];
                 if (a.dweights)
 #pragma unroll
                     for (uint32_t j = 0; j < kCopies; ++j)
-                        if (p[j] >= 0) z[j] = load_once<V>(a.x + (uint64_t)p[j] * a.xs + h);
+                        if (p[j] >= 0) z[j] = load_values<WIDE>(a.x + (uint64_t)p[j] * a.xs + h, n);
                 if (a.out)
 #pragma unroll
                     for (uint32_t j = 0; j < kCopies; ++j)
                         if (p[j] >= 0) {
-                            float dz[V];
+                            float dz[8];
 #pragma unroll
-                            for (uint32_t i = 0; i < V; ++i) dz[i] = w[j] * dy.value(i);
-                            store_raw<V>(a.out + (uint64_t)p[j] * a.os + h, pack_vals<V>(dz));
+                            for (uint32_t i = 0; i < 8; ++i) dz[i] = w[j] * value_of(dy, i);
+                            store_row<WIDE>(a.out + (uint64_t)p[j] * a.os + h, pack_values(dz), n);
                         }
-                if (a.dweights)
+                if (a.dweights)  // values past the end are zeros on both sides
 #pragma unroll
                     for (uint32_t j = 0; j < kCopies; ++j)
                         if (p[j] >= 0)
 #pragma unroll
-                            for (uint32_t i = 0; i < V; ++i) dot[j] = fmaf(dy.value(i), z[j].value(i), dot[j]);
+                            for (uint32_t i = 0; i < 8; ++i) dot[j] = fmaf(value_of(dy, i), value_of(z[j], i), dot[j]);
             }
             if (!a.dweights) continue;
 #pragma unroll
@@ -327,10 +301,10 @@ static bool sizes_ok(uint64_t tokens, uint32_t top_k) {
 }
 static bool wide(const void *p, uint64_t stride) { return aligned(p, 16) && stride % 8 == 0; }
 static uint32_t token_blocks(uint32_t tokens) { return tokens < (1u << 20) ? tokens : (1u << 20); }
-// Blocks of a row of `hidden` values, V an access: one for each 256 V values, so
-// that a few tokens spread over the device too, at most 16.
-static dim3 row_grid(uint32_t tokens, uint32_t hidden, uint32_t v) {
-    const uint64_t pieces = ceil_div(hidden, (uint64_t)kRowThreads * v);
+// Blocks of a row of `hidden` values: one for each 2048, so that a few tokens
+// spread over the device too, at most 16.
+static dim3 row_grid(uint32_t tokens, uint32_t hidden) {
+    const uint64_t pieces = ceil_div(hidden, kRowStep);
     return dim3(token_blocks(tokens), (uint32_t)(pieces < 16 ? pieces : 16));
 }
 
@@ -391,9 +365,9 @@ extern "C" zc_status zc_dispatch(const void *d_x, uint64_t tokens, uint64_t hidd
     hipStream_t st = static_cast<hipStream_t>(stream);
     const dim3 block(kRowThreads);
     if (hidden % 8 == 0 && wide(d_x, x_stride) && wide(d_out, out_stride))
-        hipLaunchKernelGGL(dispatch_kernel<8>, row_grid(a.tokens, a.hidden, 8), block, 0, st, a);
+        hipLaunchKernelGGL(dispatch_kernel<true>, row_grid(a.tokens, a.hidden), block, 0, st, a);
     else
-        hipLaunchKernelGGL(dispatch_kernel<1>, row_grid(a.tokens, a.hidden, 1), block, 0, st, a);
+        hipLaunchKernelGGL(dispatch_kernel<false>, row_grid(a.tokens, a.hidden), block, 0, st, a);
     return launched();
 }
 
@@ -421,9 +395,9 @@ extern "C" zc_status zc_combine(const void *d_z, uint64_t rows, uint64_t hidden,
     hipStream_t st = static_cast<hipStream_t>(stream);
     const dim3 block(kRowThreads);
     if (hidden % 8 == 0 && wide(d_z, z_stride) && wide(d_y, y_stride))
-        hipLaunchKernelGGL(combine_kernel<8>, row_grid(a.tokens, a.hidden, 8), block, 0, st, a);
+        hipLaunchKernelGGL(combine_kernel<true>, row_grid(a.tokens, a.hidden), block, 0, st, a);
     else
-        hipLaunchKernelGGL(combine_kernel<1>, row_grid(a.tokens, a.hidden, 1), block, 0, st, a);
+        hipLaunchKernelGGL(combine_kernel<false>, row_grid(a.tokens, a.hidden), block, 0, st, a);
     return launched();
 }
 
@@ -458,8 +432,8 @@ extern "C" zc_status zc_combine_backward(const void *d_dy, uint64_t dy_stride, c
     const dim3 grid(token_blocks(a.tokens)), block(kRowThreads);
     if (hidden % 8 == 0 && wide(d_dy, dy_stride) && (!d_dweights || wide(d_z, z_stride)) &&
         (!d_dz || wide(d_dz, dz_stride)))
-        hipLaunchKernelGGL(combine_backward_kernel<8>, grid, block, 0, st, a);
+        hipLaunchKernelGGL(combine_backward_kernel<true>, grid, block, 0, st, a);
     else
-        hipLaunchKernelGGL(combine_backward_kernel<1>, grid, block, 0, st, a);
+        hipLaunchKernelGGL(combine_backward_kernel<false>, grid, block, 0, st, a);
     return launched();
 }

@@ -583,7 +583,8 @@ struct Choice {
 static Choice choose(uint64_t m, uint64_t n, uint64_t k, uint64_t groups, bool full) {
     Choice c = {0, kTile128, 1};
     const uint64_t used = m < groups ? m : groups, per_group = used ? ceil_div(m, used) : 0;
-    if (per_group <= 12 || (used == 1 && per_group <= 32)) {
+    const bool launchable = row_tiles(m, groups, 16) * ceil_div(n, 16) < (1u << 22);
+    if (launchable && (per_group <= 12 || (used == 1 && per_group <= 32))) {
         c.rows_mt = per_group <= 16 ? 1 : 2;
         return c;
     }

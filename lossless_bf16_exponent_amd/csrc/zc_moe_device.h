@@ -17,6 +17,7 @@ constexpr uint32_t kBlock = ZC_FP8_BLOCK;
 
 typedef uint32_t u32v4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32v2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32v4a2 __attribute__((ext_vector_type(4), aligned(2)));  // 16 bytes at any BF16 value
 
 // ---------------------------------------------------------------------------
 // host side
@@ -105,6 +106,38 @@ __device__ __forceinline__ uint32_t finite_max(uint32_t m, uint32_t pair) {
     const uint32_t a = pair & 0x7FFFu, b = (pair >> 16) & 0x7FFFu;
     m = max(m, a < 0x7F80u ? a : 0u);
     return max(m, b < 0x7F80u ? b : 0u);
+}
+
+// Eight BF16 values as four pairs, of which the first n exist (the others read
+// as zeros and are not written).  WIDE: the array starts on 16 bytes and n is 0 or
+// 8 or more.  Else a row may start at any value: the memory unit takes 16 bytes
+// at any address, and only a row's last values go one by one.
+template <bool WIDE>
+__device__ __forceinline__ u32v4 load_values(const uint16_t *p, uint32_t n) {
+    u32v4 w = {0u, 0u, 0u, 0u};
+    if (n >= 8) {
+        if (WIDE)
+            w = __builtin_nontemporal_load(reinterpret_cast<const u32v4 *>(p));
+        else
+            w = __builtin_nontemporal_load(reinterpret_cast<const u32v4a2 *>(p));
+    } else if (!WIDE && n) {
+#pragma unroll
+        for (uint32_t i = 0; i < 7; ++i) w[i / 2] |= (i < n ? (uint32_t)p[i] : 0u) << (16 * (i & 1));
+    }
+    return w;
+}
+template <bool WIDE>
+__device__ __forceinline__ void store_values(uint16_t *p, const u32v4 &w, uint32_t n) {
+    if (n >= 8) {
+        if (WIDE)
+            __builtin_nontemporal_store(w, reinterpret_cast<u32v4 *>(p));
+        else
+            *reinterpret_cast<u32v4a2 *>(p) = w;
+    } else if (!WIDE && n) {
+#pragma unroll
+        for (uint32_t i = 0; i < 7; ++i)
+            if (i < n) p[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+    }
 }
 
 // ---------------------------------------------------------------------------

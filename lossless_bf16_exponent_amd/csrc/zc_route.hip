@@ -260,15 +260,11 @@ struct RouteShared {
 constexpr float kOff = 0x1p-22f, kOffRel = 0x1p-23f;
 
 template <uint32_t R, bool BF16>
-__global__ __launch_bounds__(kRouteWaves * 64) void route_kernel(RouteArgs a) {
-    __shared__ RouteShared<R> shared[kRouteWaves];
-    const uint32_t lane = lane_id(), wave = threadIdx.x / 64, sub = lane % kRow, tok = lane / kRow;
-    RouteShared<R> &sh = shared[wave];
+__device__ __forceinline__ void route_tokens(const RouteArgs &a, uint64_t first, RouteShared<R> &sh) {
+    const uint32_t lane = lane_id(), sub = lane % kRow, tok = lane / kRow;
     const uint32_t E = a.cfg.experts, G = a.cfg.groups, K = a.cfg.top_k;
     const bool sigmoid = a.cfg.score == ZC_SCORE_SIGMOID;
     const float ninf = -__builtin_inff();
-    const uint64_t first = ((uint64_t)blockIdx.x * kRouteWaves + wave) * kRowTokens;
-    if (first >= a.tokens) return;  // whole waves: the kernel has no block barrier
     const bool live = first + tok < a.tokens;
     const uint64_t row = live ? first + tok : a.tokens - 1;
 
@@ -488,6 +484,18 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_kernel(RouteArgs a) {
     }
 }
 
+// Four tokens a wave and round; the waves do not wait for each other.
+template <uint32_t R, bool BF16>
+__global__ __launch_bounds__(kRouteWaves * 64) void route_kernel(RouteArgs a) {
+    __shared__ RouteShared<R> shared[kRouteWaves];
+    const uint32_t wave = threadIdx.x / 64;
+    for (uint64_t first = ((uint64_t)blockIdx.x * kRouteWaves + wave) * kRowTokens; first < a.tokens;
+         first += (uint64_t)gridDim.x * kRouteWaves * kRowTokens) {
+        route_tokens<R, BF16>(a, first, shared[wave]);
+        lanes_meet();
+    }
+}
+
 struct RouteBackArgs {
     RouteArgs f;  // ids holds the chosen experts; weights and bias unused
     const float *dweights;
@@ -606,7 +614,8 @@ static void launch_route(const RouteArgs &a, hipStream_t st) {
     const dim3 block(kRouteWaves * 64);
     if constexpr (R <= 8) {
         if (certifiable(a)) {
-            const dim3 grid((uint32_t)ceil_div(a.tokens, kRouteWaves * kRowTokens));
+            const uint64_t blocks = ceil_div(a.tokens, kRouteWaves * kRowTokens);
+            const dim3 grid((uint32_t)(blocks < (1u << 20) ? blocks : (1u << 20)));
             hipLaunchKernelGGL((route_kernel<4 * R, BF16>), grid, block, 0, st, a);
             return;
         }
