@@ -70,6 +70,7 @@ __device__ __forceinline__ f32v16 mfma(const i32v8 &a, const i32v8 &b, const f32
 
 typedef __attribute__((address_space(3))) void lds_void;
 typedef uint32_t u32v4a4 __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u32v2a2 __attribute__((ext_vector_type(2), aligned(2)));
 
 // A wave's loads straight into LDS (16 or 4 bytes a lane, the lanes' results one
 // after another from the wave-uniform address in M0), from a uniform base and a
@@ -360,7 +361,7 @@ __global__ __launch_bounds__(kMThreads, (sizeof(TileShared<BM, BN, STAGES>) > 80
     static_assert(sizeof(sh) >= 4 * rows * row_bytes, "room for a round of every wave");
     uint8_t *mine = room + wave * rows * row_bytes;
     T *out = static_cast<T *>(p.out) + out0;
-    const bool dwords = (p.ldo * es) % 4 == 0 && (reinterpret_cast<uintptr_t>(out) & 3) == 0;
+    typedef std::conditional_t<es == 2, u32v4a2, u32v4a4> Line;  // 16 bytes at any element
 #pragma unroll
     for (uint32_t round = 0; round < rounds; ++round) {
 #pragma unroll
@@ -385,13 +386,13 @@ __global__ __launch_bounds__(kMThreads, (sizeof(TileShared<BM, BN, STAGES>) > 80
         uint32_t r = m0 + wm + round * rows + lane / chunks;
         const uint8_t *from = mine + (lane / chunks) * row_bytes + cc * 16;
         T *o = out + (uint64_t)r * p.ldo + c;
-        const bool whole = dwords && c + per <= p.n;
+        const bool whole = c + per <= p.n;
 #pragma unroll 4
         for (uint32_t q = 0; q < rows / step; ++q, r += step, from += step * row_bytes, o += step * p.ldo) {
             const u32v4 v = *reinterpret_cast<const u32v4 *>(from);
             if (r < m1 && c < p.n) {
                 if (whole) {
-                    *reinterpret_cast<u32v4a4 *>(o) = v;
+                    *reinterpret_cast<Line *>(o) = v;
                 } else {
                     for (uint32_t k = 0; k < per && c + k < p.n; ++k)
                         o[k] = (T)(v[k * es / 4] >> (8 * es * k % 32));
@@ -399,6 +400,30 @@ __global__ __launch_bounds__(kMThreads, (sizeof(TileShared<BM, BN, STAGES>) > 80
             }
         }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    }
+}
+
+// Four results of a row, of which n exist.
+template <typename T>
+__device__ __forceinline__ void store4(T *o, float a, float b, float c, float d, uint32_t n) {
+    if constexpr (sizeof(T) == 2) {
+        const u32v2 w = {bf_pack(a, b), bf_pack(c, d)};
+        if (n >= 4) {
+            *reinterpret_cast<u32v2a2 *>(o) = w;
+        } else {
+#pragma unroll
+            for (uint32_t j = 0; j < 3; ++j)
+                if (j < n) o[j] = (uint16_t)(w[j / 2] >> (16 * (j & 1)));
+        }
+    } else {
+        const u32v4 w = {__float_as_uint(a), __float_as_uint(b), __float_as_uint(c), __float_as_uint(d)};
+        if (n >= 4) {
+            *reinterpret_cast<u32v4a4 *>(o) = w;
+        } else {
+#pragma unroll
+            for (uint32_t j = 0; j < 3; ++j)
+                if (j < n) o[j] = w[j];
+        }
     }
 }
 
@@ -433,13 +458,7 @@ __global__ __launch_bounds__(256) void add_parts_kernel(const float *parts, uint
             for (uint32_t s = 0; s < splits; ++s)
                 for (uint32_t j = 0; j < k; ++j) v[j] += src[s * stride + j];
         }
-        T *o = out + r * ldo + c;
-        for (uint32_t j = 0; j < k; ++j) {
-            if constexpr (sizeof(T) == 2)
-                o[j] = bf_round(v[j]);
-            else
-                o[j] = __float_as_uint(v[j]);
-        }
+        store4(out + r * ldo + c, v[0], v[1], v[2], v[3], k);
     }
 }
 
@@ -517,15 +536,7 @@ __global__ __launch_bounds__(WAVES * 64) void rows_kernel(MatArgs p) {
         // a lane holds four consecutive columns of one row
         const uint32_t r = m0 + 16 * i + fr, c = n0 + 4 * (lane / 16);
         if (r < m1) {
-            T *o = static_cast<T *>(p.out) + (uint64_t)r * p.ldo + c;
-#pragma unroll
-            for (uint32_t j = 0; j < 4; ++j)
-                if (c + j < p.n) {
-                    if constexpr (sizeof(T) == 2)
-                        o[j] = bf_round(v[j]);
-                    else
-                        o[j] = __float_as_uint(v[j]);
-                }
+            store4(static_cast<T *>(p.out) + (uint64_t)r * p.ldo + c, v[0], v[1], v[2], v[3], c < p.n ? p.n - c : 0u);
         }
     }
 }
