@@ -371,3 +371,91 @@ def test_product_gradients_against_differences(zc):
         diff = (d[:, i] * xt[:, j]).sum()
         size = (np.abs(d[:, i]) * np.abs(xt[:, j])).sum()
         assert abs(got_dw[i, j] - diff) <= 2 * (m + 8) * ref.F32_HALF_STEP * size + 1e-12
+
+
+# ---------------------------------------------------------------------------
+# more tiles than the device holds at once
+# ---------------------------------------------------------------------------
+
+def close_on_device(got, a, b, f32, what):
+    """got against a b^T in 64 bits on the device, within fast_tolerance's bound with the largest product of 64 taken as
+    the product of the largest factors."""
+    a, b = a.double(), b.double()
+    want = a @ b.T
+    k = ref.up(a.shape[1], 64)
+
+    def largest(v):
+        return torch.nn.functional.pad(v.abs(), (0, k - v.shape[1])).view(v.shape[0], -1, 64).amax(dim=2)
+
+    tol = (0 if f32 else ref.BF16_HALF_STEP) * want.abs() + (a.shape[1] + 8) * 2 * ref.F32_HALF_STEP * (a.abs() @ b.abs().T)
+    tol += 2.0 ** -10 * (largest(a) @ largest(b).T) + 2.0 ** -126
+    over = (got.double() - want).abs() > tol
+    assert not bool(over.any()), "%s: %d of %d off" % (what, int(over.sum()), over.numel())
+
+
+def stood_for(q, s, cols, block_rows=1):
+    """What e4m3 blocks on the device stand for, in 64 bits."""
+    t = torch.tensor(ref.VALUES[ref.E4M3], device="cuda")[q.long()]
+    e = torch.exp2(s.double() - 127).round(decimals=60)[:, :t.shape[1] // 128].repeat_interleave(128, dim=1)
+    return (t * e.repeat_interleave(block_rows, dim=0)[:t.shape[0]])[:, :cols]
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("m,n,k,groups", [(4400, 4500, 128, 1), (4352, 4352, 256, 1), (4400, 4353, 300, 1), (4500, 4609, 640, 1),
+                                          (9000, 2100, 1100, 5), (4800, 8200, 384, 9)])
+def test_matmul_many_tiles(zc, m, n, k, groups, f32):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(m + n + k)
+    x = (torch.randn(m, k, generator=g, device="cuda") * torch.exp2(torch.randint(-6, 7, (m, 1), generator=g, device="cuda"))).bfloat16()
+    w = (torch.randn(groups, n, k, generator=g, device="cuda") * 0.1).bfloat16()
+    xq, xs = Out((m, zc.zc_fp8_stride(k)), torch.uint8), Out((m, zc.zc_fp8_scale_stride(k)), torch.uint8)
+    zc.zc_fp8_quantize(x, m, k, k, ref.E4M3, 1, xq, xs)
+    wq = Out((groups, n, zc.zc_fp8_stride(k)), torch.uint8)
+    ws = Out((groups, ref.up(n, 128) // 128, zc.zc_fp8_scale_stride(k)), torch.uint8)
+    for i in range(groups):
+        zc.zc_fp8_quantize(w[i], n, k, k, ref.E4M3, 128, wq.t[i], ws.t[i])
+    cuts = np.sort(np.random.default_rng(m).integers(0, m + 1, groups - 1))
+    offsets = np.concatenate([[0], cuts, [m]])
+    out = Out((m, n + 3), torch.float32 if f32 else torch.bfloat16)
+    for _ in range(2):  # the second time over the first one's results
+        zc.zc_fp8_matmul(xq, xs, ref.E4M3, m, wq, ws, ref.E4M3, n, k, groups, device(offsets.astype(np.int32)), out,
+                         zc.ZC_F32 if f32 else zc.ZC_BF16, n + 3)
+    out.numpy()
+    a = stood_for(xq.t, xs.t, k)
+    for i, (r0, r1) in enumerate(zip(offsets, offsets[1:])):
+        if r0 < r1:
+            close_on_device(out.t[r0:r1, :n], a[r0:r1], stood_for(wq.t[i], ws.t[i], k, 128), f32, "group %d" % i)
+
+
+@pytest.mark.parametrize("f32", [False, True])
+def test_wgrad_many_tiles(zc, f32):
+    """Groups of no, one, two and more blocks of tokens, next to each other."""
+    n, k = 1100, 1300
+    counts = [300, 0, 1, 700, 128, 129, 0, 256, 5, 1000, 385, 64]
+    rows, groups = sum(counts), len(counts)
+    offsets = np.concatenate([[0], np.cumsum(counts)])
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    dy, x = torch.randn(rows, n, generator=g, device="cuda").bfloat16(), torch.randn(rows, k, generator=g, device="cuda").bfloat16()
+    padded = zc.zc_fp8_padded_rows(rows, groups)
+    od = device(offsets.astype(np.int32))
+    ops = []
+    for v, cols in ((dy, n), (x, k)):
+        q = torch.full((cols, padded), 0x7F, dtype=torch.uint8, device="cuda")
+        s = torch.full((cols, zc.zc_fp8_scale_stride(padded)), 0xFF, dtype=torch.uint8, device="cuda")
+        zc.zc_fp8_quantize_t(v, None, zc.ZC_BF16, rows, cols, cols, groups, od, ref.E4M3, q, s, padded)
+        ops.append((q, s))
+    out = Out((groups, n, k), torch.float32 if f32 else torch.bfloat16)
+    for _ in range(2):
+        zc.zc_fp8_matmul_wgrad(*ops[0], ref.E4M3, n, *ops[1], ref.E4M3, k, padded, rows, groups, od, out,
+                               zc.ZC_F32 if f32 else zc.ZC_BF16)
+    out.numpy()
+    at = 0
+    for i, c in enumerate(counts):
+        if not c:
+            assert not bool(out.t[i].any())
+            continue
+        b0, b1 = at // 128, at // 128 + ref.up(c, 128) // 128
+        pair = [stood_for(q[:, 128 * b0:128 * b1], s[:, b0:b1], c) for q, s in ops]
+        close_on_device(out.t[i], *pair, f32, "group %d" % i)
+        at = 128 * b1
