@@ -29,6 +29,7 @@ struct RouteArgs {
     uint64_t stride;
     uint32_t tokens;
     zc_route_config cfg;
+    uint32_t first = 0;  // first token of the launch
 };
 
 template <bool BF16>
@@ -484,16 +485,14 @@ __device__ __forceinline__ void route_tokens(const RouteArgs &a, uint64_t first,
     }
 }
 
-// Four tokens a wave and round; the waves do not wait for each other.
+// Four tokens a wave; the waves do not wait for each other. No loop over tokens:
+// around this body it costs a tenth of a call of one token (7.4 -> 8.3 us).
 template <uint32_t R, bool BF16>
 __global__ __launch_bounds__(kRouteWaves * 64) void route_kernel(RouteArgs a) {
     __shared__ RouteShared<R> shared[kRouteWaves];
     const uint32_t wave = threadIdx.x / 64;
-    for (uint64_t first = ((uint64_t)blockIdx.x * kRouteWaves + wave) * kRowTokens; first < a.tokens;
-         first += (uint64_t)gridDim.x * kRouteWaves * kRowTokens) {
-        route_tokens<R, BF16>(a, first, shared[wave]);
-        lanes_meet();
-    }
+    const uint64_t first = a.first + ((uint64_t)blockIdx.x * kRouteWaves + wave) * kRowTokens;
+    if (first < a.tokens) route_tokens<R, BF16>(a, first, shared[wave]);
 }
 
 struct RouteBackArgs {
@@ -614,9 +613,15 @@ static void launch_route(const RouteArgs &a, hipStream_t st) {
     const dim3 block(kRouteWaves * 64);
     if constexpr (R <= 8) {
         if (certifiable(a)) {
-            const uint64_t blocks = ceil_div(a.tokens, kRouteWaves * kRowTokens);
-            const dim3 grid((uint32_t)(blocks < (1u << 20) ? blocks : (1u << 20)));
-            hipLaunchKernelGGL((route_kernel<4 * R, BF16>), grid, block, 0, st, a);
+            // A grid holds less than 2^32 threads.
+            constexpr uint64_t most = 1u << 20;
+            RouteArgs part = a;
+            for (uint64_t first = 0; first < a.tokens; first += most * kRouteWaves * kRowTokens) {
+                const uint64_t blocks = ceil_div(a.tokens - first, kRouteWaves * kRowTokens);
+                part.first = (uint32_t)first;
+                hipLaunchKernelGGL((route_kernel<4 * R, BF16>), dim3((uint32_t)(blocks < most ? blocks : most)), block,
+                                   0, st, part);
+            }
             return;
         }
     }

@@ -233,3 +233,19 @@ def test_route_on_another_stream(zc):
     zc.zc_route(logits, zc.ZC_F32, 4096, 128, None, cfg, ids, w, stream=st)
     st.synchronize()
     assert np.array_equal(ids.numpy(), ref.route(x, None, cfg)[0])
+
+
+def test_route_more_tokens_than_a_launch_takes(zc):
+    t, period = 16 * 2 ** 20 + 21, 1009
+    x = np.random.default_rng(3).standard_normal((period, 4)).astype(np.float32)
+    cfg = zc.route_config(4, 1, score="sigmoid", renormalise=False)
+    logits = torch.from_numpy(x).cuda().repeat(t // period + 1, 1)[:t].contiguous()
+    ids, w = Out((t, 1), torch.int32), Out((t, 1), torch.float32)
+    zc.zc_route(logits, zc.ZC_F32, t, 4, None, cfg, ids, w)
+    ids.numpy(), w.numpy()
+    best = x.argmax(axis=1)
+    value = 1 / (1 + np.exp(-x.astype(np.float64).max(axis=1)))
+    at = torch.arange(t, device="cuda") % period
+    assert torch.equal(ids.t[:, 0].long(), torch.from_numpy(best).cuda()[at])
+    want = torch.from_numpy(value).cuda()[at]
+    assert bool(((w.t[:, 0].double() - want).abs() <= torch.from_numpy(weight_tolerance(value, 1)).cuda()[at]).all())
