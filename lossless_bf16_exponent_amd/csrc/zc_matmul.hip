@@ -589,8 +589,9 @@ struct Choice {
 // 256 CUs takes, for each block of the contraction, 1.2 us with tiles of 256 x 256,
 // 0.85 with 256 x 128, 0.55 with 128 x 128 alone on a CU, and 1.1 with two of those
 // on it (512 x 4096 x 7168: 67, 45, 29, 40 us; 4096 x 4096 x 7168: 92, 117, 137,
-// 122), and 4 to 9 us for its start and end.  With few tiles of 128 x 128 the contraction is split, at the cost of
-// writing and adding the parts (4 us and their bytes).  Groups are taken to have equally many rows.
+// 122), and 4 to 9 us for its start and end.  With few tiles of 128 x 128 the
+// contraction is split, at the cost of writing and adding the parts (4 us and
+// their bytes).  Groups are taken to have equally many rows.
 static Choice choose(uint64_t m, uint64_t n, uint64_t k, uint64_t groups, bool full) {
     Choice c = {0, kTile128, 1};
     const uint64_t used = m < groups ? m : groups, per_group = used ? ceil_div(m, used) : 0;

@@ -485,8 +485,11 @@ __device__ __forceinline__ void route_tokens(const RouteArgs &a, uint64_t first,
     }
 }
 
-// Four tokens a wave; the waves do not wait for each other. No loop over tokens:
-// around this body it costs a tenth of a call of one token (7.4 -> 8.3 us).
+// Four tokens a wave; the waves do not wait for each other.  Bound by the latency
+// of a wave's steps, one after another: 1 token of 256 experts in 8 groups takes
+// 7.1 us, 8192 tokens (two waves a SIMD) 10 to 13, where their bytes need 1.7; one
+// wave a token with every score in 64 bits took 28.  No loop over tokens: around
+// this body it costs a tenth of a call of one token (7.4 -> 8.3 us).
 template <uint32_t R, bool BF16>
 __global__ __launch_bounds__(kRouteWaves * 64) void route_kernel(RouteArgs a) {
     __shared__ RouteShared<R> shared[kRouteWaves];
@@ -506,6 +509,7 @@ struct RouteBackArgs {
 //   renormalised: d = scale * (dw - sum(dw p) / S) / S,  else d = scale * dw;
 // sigmoid: dl = d s (1 - s) at the chosen, 0 elsewhere;
 // softmax: dl_i = s_i (d_i - sum d s), d_i = 0 for experts not chosen.
+// Bound by latency as the forward is: 8191 tokens of 128 experts take 7.0 us.
 template <uint32_t R, bool BF16>
 __global__ __launch_bounds__(kRouteWaves * 64) void route_backward_kernel(RouteBackArgs a) {
     __shared__ float ds[kRouteWaves][R * 64];
