@@ -119,8 +119,7 @@ constexpr uint32_t kTCols = SRC == ZC_BF16 ? 64 : 128;
 // column, 16 tokens each, which then write its 128 bytes as one line.  (Four
 // threads a column in four waves, 32 bytes each: 1.3 and 1.2 times as long.)
 // 8192 tokens in 8 groups take 26 us from 4096 columns of BF16 (3.9 TB/s, of 5.2
-// that a copy reaches) and 42 from 7168 of 8 bits (2.8 TB/s: the values are taken
-// apart and quantised anew, twice as many to a byte).
+// that a copy reaches) and 42 from 7168 of 8 bits (2.8 TB/s), which are also unpacked.
 // Rows past the group's end are zeros.
 template <uint32_t SRC, uint32_t TYPE, bool WIDE>
 __global__ __launch_bounds__(kQThreads) void quantize_t_kernel(TransArgs a) {
