@@ -352,7 +352,9 @@ __device__ __forceinline__ void route_tokens(const RouteArgs &a, uint64_t first,
             }
             score = two ? b1 + b2 : b1;
         }
-        // a group stays when fewer than group_top come before it: one other group a rotation of the row
+        // a group stays when fewer than group_top come before it: one other group a rotation of the row.  Every lane takes
+        // part, those past the last group with their -inf: a rotation brings 0 from a lane that is switched off, and a 0
+        // would come before a group whose score is negative
         const auto places = [&](auto mine_score, auto rotate) -> uint32_t {
             uint32_t before = 0;
             const auto meet = [&](auto o, uint32_t other) {
@@ -376,9 +378,10 @@ __device__ __forceinline__ void route_tokens(const RouteArgs &a, uint64_t first,
             return before;
         };
         const auto row_any = [&](bool b) { return ((__ballot(b) >> (kRow * tok)) & 0xFFFFu) != 0; };
-        bool keep = sub < G && places(score, [&](auto n) {
-                        return __uint_as_float(rotated<decltype(n)::value>(__float_as_uint(score)));
-                    }) < a.cfg.group_top;
+        const uint32_t place = places(score, [&](auto n) {
+            return __uint_as_float(rotated<decltype(n)::value>(__float_as_uint(score)));
+        });
+        bool keep = sub < G && place < a.cfg.group_top;
         if (a.cfg.group_top < G) {
             const float last = -row_max(keep ? -score : ninf), next = row_max(sub < G && !keep ? score : ninf);
             // (a NaN score: infinities of both signs in a group)
@@ -411,12 +414,12 @@ __device__ __forceinline__ void route_tokens(const RouteArgs &a, uint64_t first,
                 double score64 = -__builtin_inf();
                 if (sub < G) score64 = exact(i1) + (two ? exact(i2) : 0.0);
                 const uint64_t bits = __builtin_bit_cast(uint64_t, score64);
-                const bool keep64 = sub < G && places(score64, [&](auto n) {
-                                        const uint64_t hi = rotated<decltype(n)::value>((uint32_t)(bits >> 32));
-                                        return __builtin_bit_cast(double, hi << 32 | rotated<decltype(n)::value>((uint32_t)bits));
-                                    }) < a.cfg.group_top;
+                const uint32_t place64 = places(score64, [&](auto n) {
+                    const uint64_t hi = rotated<decltype(n)::value>((uint32_t)(bits >> 32));
+                    return __builtin_bit_cast(double, hi << 32 | rotated<decltype(n)::value>((uint32_t)bits));
+                });
                 if (unsure) {
-                    keep = keep64;
+                    keep = sub < G && place64 < a.cfg.group_top;
                     slow |= row_any(!sure || score64 != score64);
                 }
             }
