@@ -253,11 +253,16 @@ struct RouteShared {
 // reciprocal 3 h, of values of at most 1; adding the bias rounds by h |a|.
 //   candidates  if t is the K-th largest a, K experts have c >= t - d(t), so
 //               every expert among the K best has a >= t - 2 d(t) or so
-//   groups      a group's score, a sum of two, is off by at most 2^-21 + 2^-22 of its
-//               size: the kept groups are certain when the last kept and
-//               the first left are further apart than both may be off.  Else the
-//               two experts of every group are scored in 64 bits, if they
-//               are certain themselves
+//   groups      a group's score, the sum b1 + b2 of its two largest a, is off by at
+//               most d(b1) + d(b2) and the sum's rounding, h (|b1| + |b2|): the sizes of
+//               the addends, which may cancel, not that of the sum.  (a + d(a) and
+//               a - d(a) grow with a, so this holds whichever two the c put first.)
+//               The kept groups are certain when the lowest that one of them may be
+//               lies above the highest that another may be.  The comparison takes
+//               3 h (|b1| + |b2|) in place of 2 (for one score 2 h |b1| in place of 1),
+//               for the roundings of its own sums, and a sixteenth more, for those of
+//               the bounds.  Else the two experts of every group are scored in 64
+//               bits, if they are certain themselves
 constexpr float kOff = 0x1p-22f, kOffRel = 0x1p-23f;
 
 template <uint32_t R, bool BF16>
@@ -340,7 +345,7 @@ __device__ __forceinline__ void route_tokens(const RouteArgs &a, uint64_t first,
         lanes_meet();
         const bool two = a.cfg.group_score == 2 && per > 1;
         const float *group = mine;
-        float score = ninf;
+        float score = ninf, off = 0.0f;
         if (sub < G) {
             float b1 = ninf, b2 = ninf;
 #pragma unroll 8
@@ -351,6 +356,7 @@ __device__ __forceinline__ void route_tokens(const RouteArgs &a, uint64_t first,
                 b1 = fmaxf(b1, x);
             }
             score = two ? b1 + b2 : b1;
+            off = 1.0625f * (two ? 2.0f * kOff + 1.5f * kOffRel * (fabsf(b1) + fabsf(b2)) : kOff + kOffRel * fabsf(b1));
         }
         // a group stays when fewer than group_top come before it: one other group a rotation of the row.  Every lane takes
         // part, those past the last group with their -inf: a rotation brings 0 from a lane that is switched off, and a 0
@@ -383,10 +389,9 @@ __device__ __forceinline__ void route_tokens(const RouteArgs &a, uint64_t first,
         });
         bool keep = sub < G && place < a.cfg.group_top;
         if (a.cfg.group_top < G) {
-            const float last = -row_max(keep ? -score : ninf), next = row_max(sub < G && !keep ? score : ninf);
-            // (a NaN score: infinities of both signs in a group)
-            const bool unsure = row_any(score != score) ||
-                                !(last - next > 2.0f * (2.0f * kOff + kOffRel * (fabsf(last) + fabsf(next))));
+            const float low = -row_max(keep ? off - score : ninf), high = row_max(sub < G && !keep ? score + off : ninf);
+            // (infinities have no distance from each other, and a group that holds those of both signs has no score)
+            const bool unsure = row_any(sub < G && !(fabsf(score) < 3.0e38f)) || !(low > high);
             if (__ballot(unsure)) {
                 float b1 = ninf, b2 = ninf, b3 = ninf;
                 uint32_t i1 = 0, i2 = 0;

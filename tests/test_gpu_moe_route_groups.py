@@ -1,5 +1,5 @@
-"""Routing by groups of experts whose scores are negative or of both signs: balance
-biases of any sign, and numbers of groups from 2 to 16.  Ids are
+"""Routing by groups of experts whose scores are negative, of both signs, or cancel:
+balance biases of any sign and size, and numbers of groups from 2 to 16.  Ids are
 those of the 64-bit scores, exactly."""
 import numpy as np
 import pytest
@@ -50,6 +50,40 @@ def test_negative_bias_bf16_logits(zc, bf16):
     x = ref.bf16(x) if bf16 else x
     cfg = zc.route_config(256, 8, "sigmoid", groups=8, group_top=4, group_score=2)
     check(zc, x, f32(-0.95 + 0.05 * g.standard_normal(256)), cfg, bf16)
+
+
+# One expert of a group is lifted and the others are pushed down by as much: a group's two best scores cancel, and what is left
+# has the roundings of the large ones.
+@pytest.mark.parametrize("size", [1.0, 16.0, 64.0, 1e3, 1e4, 1e5, 1e6])
+@pytest.mark.parametrize("groups,group_top,per", [(2, 1, 4), (8, 3, 4), (16, 5, 2), (16, 8, 16)])
+def test_scores_that_cancel(zc, groups, group_top, per, size):
+    g = np.random.default_rng([groups, per, int(size)])
+    bias = np.full((groups, per), -size)
+    bias[np.arange(groups), g.integers(0, per, groups)] = size
+    cfg = zc.route_config(groups * per, min(3, group_top * per), "sigmoid", groups=groups, group_top=group_top,
+                          group_score=2)
+    check(zc, f32(g.standard_normal((6000, groups * per))), f32(bias.reshape(-1)), cfg)
+
+
+def test_two_groups_that_cancel(zc):
+    """64-bit group scores 1.02975 and 1.02953; 32-bit sums come out the other way round."""
+    x = f32([[0.24, -0.73, -0.12, -0.62, 0.31, -1.11, -0.24, -0.19]])
+    bias = f32([1e4, -1e4, -1e4, -1e4] * 2)
+    check(zc, x, bias, zc.route_config(8, 2, "sigmoid", groups=2, group_top=1, group_score=2))
+
+
+@pytest.mark.parametrize("groups,group_top", [(4, 2), (8, 3), (16, 4)])
+def test_masks_that_leave_one_expert(zc, groups, group_top):
+    """A mask of -1e9 leaves one expert in some groups, none in others: their scores stand far below those of the rest, and
+    still in the order of the 64-bit sums."""
+    g = np.random.default_rng(groups)
+    per = 8
+    bias = np.zeros((groups, per))
+    bias[0, 1:] = bias[1, :] = -1e9
+    bias[2, :5] = -1e9
+    bias = bias + 0.01 * g.standard_normal((groups, per))
+    cfg = zc.route_config(groups * per, 6, "sigmoid", groups=groups, group_top=group_top, group_score=2)
+    check(zc, f32(g.standard_normal((300, groups * per))), f32(bias.reshape(-1)), cfg)
 
 
 def test_near_tied_groups_of_negative_scores(zc):
