@@ -20,22 +20,30 @@ struct GateArgs {
     uint32_t rows, cols, blocks;
 };
 
-// sigmoid(g) and 1 - sigmoid(g) from t = e^-|g| <= 1: neither overflows, nor
-// loses digits to a subtraction.  The hardware exponential and reciprocal (1 ulp
-// of 32 bits) are far finer than the BF16 results.  The hardware exponential
-// flushes results below 2^-126, which g e^g with |g| near 88 still multiplies into
-// a normal number: there it is taken 2^64 higher.  NaN stays NaN.
+// sigmoid(g) = s * unit and 1 - sigmoid(g) from t = e^-|g| <= 1: neither overflows,
+// nor loses digits to a subtraction.  The hardware exponential and reciprocal (1
+// ulp of 32 bits) are far finer than the BF16 results.  Below e^-87 t has few
+// digits in 32 bits or none, and g t times a large value is a normal number
+// again: past |g| = 80 it is taken 2^64 higher, and a sigmoid that is t keeps that
+// factor until the products are made (unit; 1 else).  There 1 + t is 1, and g t is
+// nothing beside 1.  NaN stays NaN.
 struct Sigmoid {
-    float s, rest;
+    float s, rest, unit;
 };
 __device__ __forceinline__ Sigmoid sigmoid(float g) {
-    const float a = fabsf(g), shift = a > 80.0f ? 64.0f : 0.0f;
-    const float t = __builtin_amdgcn_exp2f(fmaf(a, -1.44269504f, shift)) * (a > 80.0f ? 0x1p-64f : 1.0f);
-    const float r = __builtin_amdgcn_rcpf(1.0f + t), tr = t * r;
+    const float a = fabsf(g);
+    const bool far = a > 80.0f;
+    const float t = __builtin_amdgcn_exp2f(fmaf(a, -1.44269504f, far ? 64.0f : 0.0f));
+    const float r = __builtin_amdgcn_rcpf(1.0f + (far ? 0.0f : t)), tr = t * r;
     Sigmoid o;
     o.s = g >= 0.0f ? r : tr;
-    o.rest = g >= 0.0f ? tr : r;
+    o.rest = g >= 0.0f ? (far ? 0.0f : tr) : r;
+    o.unit = far && g < 0.0f ? 0x1p-64f : 1.0f;
     return o;
+}
+__device__ __forceinline__ float gated(float g, float u) {
+    const Sigmoid o = sigmoid(g);
+    return g * o.s * u * o.unit;
 }
 
 // The 8 values' 8-bit form under the block's scale (16 lanes a block); lane 0
@@ -77,10 +85,8 @@ __global__ __launch_bounds__(kGThreads) void swiglu_kernel(GateArgs a) {
         if (!a.h && !a.hq) continue;
         u32v4 h;
 #pragma unroll
-        for (uint32_t i = 0; i < 4; ++i) {
-            const float g0 = bf_lo(g[i]), g1 = bf_hi(g[i]);
-            h[i] = bf_pack(g0 * sigmoid(g0).s * bf_lo(u[i]), g1 * sigmoid(g1).s * bf_hi(u[i]));
-        }
+        for (uint32_t i = 0; i < 4; ++i)
+            h[i] = bf_pack(gated(bf_lo(g[i]), bf_lo(u[i])), gated(bf_hi(g[i]), bf_hi(u[i])));
         if (a.h) store_values<WIDE>(a.h + (uint64_t)row * a.h_stride + c, h, n);
         if (a.hq) {
             uint8_t *s = a.hs + (uint64_t)row * a.hss;
@@ -120,8 +126,8 @@ __global__ __launch_bounds__(kGThreads) void swiglu_backward_kernel(GateArgs a) 
         for (uint32_t i = 0; i < 8; ++i) {
             const float gv = g[i] * gs, uv = u[i] * us, d = (i & 1) ? bf_hi(dh[i / 2]) : bf_lo(dh[i / 2]);
             const Sigmoid sg = sigmoid(gv);
-            dg[i] = d * uv * (sg.s * fmaf(gv, sg.rest, 1.0f));
-            du[i] = d * (gv * sg.s);
+            dg[i] = d * uv * (sg.s * fmaf(gv, sg.rest, 1.0f)) * sg.unit;
+            du[i] = d * (gv * sg.s) * sg.unit;
         }
         u32v4 wg, wu;
 #pragma unroll

@@ -124,3 +124,23 @@ def test_extreme_gates(zc):
     dh = np.ones((1, 16))
     zc.zc_swiglu_backward(o["kq"], o["ks"], 1, 16, bf16_device(dh), 16, out, 32)
     assert np.isfinite(out.numpy()[0, :10]).all()
+
+
+def test_gates_whose_sigmoid_is_below_the_normal_numbers(zc):
+    """sigmoid(-88) to sigmoid(-104) have few or no digits in 32 bits; their products with large values have all of theirs."""
+    m, f = 6, 128
+    r = np.random.default_rng(104)
+    g = ref.bf16(-r.uniform(88.0, 104.0, (m, f)))
+    u = ref.bf16(r.standard_normal((m, f)) * 2.0 ** np.array([20, 40, 50, 70, 90, 110])[:, None])
+    gu = np.concatenate([g, u], axis=1)
+    o = forward(zc, gu, f, 0)
+    want = ref.swiglu(g, u)
+    close(o["h"].numpy(), want, tolerance(want, np.abs(want), g), "h")
+    dh = ref.bf16(r.standard_normal((m, f)) * 2.0 ** np.array([60, 50, 30, 20, 10, 5])[:, None])
+    out = Out((m, 2 * f), torch.bfloat16)
+    zc.zc_swiglu_backward(o["kq"], o["ks"], m, f, bf16_device(dh), f, out, 2 * f)
+    got, kq, ks = out.numpy(), o["kq"].numpy(), o["ks"].numpy()
+    g, u = ref.values(kq[:, :f], ks[:, :1], ref.E4M3, f), ref.values(kq[:, f:], ks[:, 1:2], ref.E4M3, f)
+    dg, du, size = ref.swiglu_backward(g, u, dh)
+    close(got[:, :f], dg, tolerance(dg, size, g), "dgate")
+    close(got[:, f:], du, tolerance(du, np.abs(du), g), "dup")
