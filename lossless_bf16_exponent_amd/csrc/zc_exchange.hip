@@ -330,7 +330,7 @@ extern "C" zc_status zc_dispatch_plan(const int32_t *d_ids, uint64_t tokens, uin
         !aligned(d_workspace, 16))
         return ZC_ERR_MISALIGNED;
     if (tokens && workspace_bytes < zc_dispatch_workspace_bytes(tokens, top_k, experts)) return ZC_ERR_CAPACITY;
-    hipStream_t st = static_cast<hipStream_t>(stream);
+    hipStream_t st = stream_of(stream);
     if (!tokens) {
         hipLaunchKernelGGL(plan_empty_kernel, dim3(1), dim3(256), 0, st, d_offsets, experts + 1);
         return launched();
@@ -362,7 +362,7 @@ extern "C" zc_status zc_dispatch(const void *d_x, uint64_t tokens, uint64_t hidd
     a.top_k = top_k;
     a.rows = (uint32_t)rows;
     a.hidden = (uint32_t)hidden;
-    hipStream_t st = static_cast<hipStream_t>(stream);
+    hipStream_t st = stream_of(stream);
     const dim3 block(kRowThreads);
     if (hidden % 8 == 0 && wide(d_x, x_stride) && wide(d_out, out_stride))
         hipLaunchKernelGGL(dispatch_kernel<true>, row_grid(a.tokens, a.hidden), block, 0, st, a);
@@ -392,7 +392,7 @@ extern "C" zc_status zc_combine(const void *d_z, uint64_t rows, uint64_t hidden,
     a.top_k = top_k;
     a.rows = (uint32_t)rows;
     a.hidden = (uint32_t)hidden;
-    hipStream_t st = static_cast<hipStream_t>(stream);
+    hipStream_t st = stream_of(stream);
     const dim3 block(kRowThreads);
     if (hidden % 8 == 0 && wide(d_z, z_stride) && wide(d_y, y_stride))
         hipLaunchKernelGGL(combine_kernel<true>, row_grid(a.tokens, a.hidden), block, 0, st, a);
@@ -428,7 +428,7 @@ extern "C" zc_status zc_combine_backward(const void *d_dy, uint64_t dy_stride, c
     a.top_k = top_k;
     a.rows = (uint32_t)rows;
     a.hidden = (uint32_t)hidden;
-    hipStream_t st = static_cast<hipStream_t>(stream);
+    hipStream_t st = stream_of(stream);
     const dim3 grid(token_blocks(a.tokens)), block(kRowThreads);
     if (hidden % 8 == 0 && wide(d_dy, dy_stride) && (!d_dweights || wide(d_z, z_stride)) &&
         (!d_dz || wide(d_dz, dz_stride)))

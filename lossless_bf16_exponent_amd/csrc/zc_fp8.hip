@@ -289,7 +289,7 @@ extern "C" zc_status zc_fp8_quantize(const void *d_x, uint64_t rows, uint64_t co
                          stride8(cols), scale_stride(cols), (uint32_t)rows, (uint32_t)cols,
                          (uint32_t)ceil_div(cols, kBlock)};
     const bool wide = aligned(d_x, 16) && x_stride % 8 == 0 && cols % 8 == 0;
-    hipStream_t st = static_cast<hipStream_t>(stream);
+    hipStream_t st = stream_of(stream);
     if (type == ZC_FP8_E4M3)
         launch_quantize<ZC_FP8_E4M3>(a, block_rows != 1, wide, st);
     else
@@ -318,7 +318,7 @@ extern "C" zc_status zc_fp8_quantize_t(const void *d_x, const uint8_t *d_x_scale
     a.units = zc_fp8_padded_rows(rows, groups) / kBlock * a.col_tiles;
     const uint32_t grid = grid_of(a.units);
     const bool wide = aligned(d_x, 16) && x_stride % 8 == 0 && cols % 8 == 0;
-    hipStream_t st = static_cast<hipStream_t>(stream);
+    hipStream_t st = stream_of(stream);
     if (x_type == ZC_BF16)
         launch_quantize_t<ZC_BF16>(type, a, wide, grid, st);
     else if (x_type == ZC_FP8_E4M3)
@@ -338,7 +338,7 @@ extern "C" zc_status zc_fp8_transpose(const void *d_q, const uint8_t *d_scales, 
     const SquareArgs a = {static_cast<const uint8_t *>(d_q), d_scales, static_cast<uint8_t *>(d_qt), d_scales_t,
                           (uint32_t)rows, (uint32_t)cols, (uint32_t)ceil_div(rows, kBlock),
                           (uint32_t)ceil_div(cols, kBlock), batch};
-    hipLaunchKernelGGL(transpose_kernel, dim3(grid_of(batch * a.row_blocks * a.col_blocks)), dim3(kQThreads), 0, static_cast<hipStream_t>(stream),
+    hipLaunchKernelGGL(transpose_kernel, dim3(grid_of(batch * a.row_blocks * a.col_blocks)), dim3(kQThreads), 0, stream_of(stream),
                        a);
     return launched();
 }

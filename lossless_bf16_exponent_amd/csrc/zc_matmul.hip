@@ -757,7 +757,7 @@ extern "C" zc_status zc_fp8_matmul(const void *d_a, const uint8_t *d_a_scales, u
     const Choice c = choose(m, n, k, groups, full);
     const bool room = d_workspace && workspace_bytes >= zc_fp8_matmul_workspace_bytes(m, n, k, groups);
     return launch_forward(p, a_type, b_type, out_type == ZC_BF16, full, c,
-                          room ? static_cast<float *>(d_workspace) : nullptr, static_cast<hipStream_t>(stream));
+                          room ? static_cast<float *>(d_workspace) : nullptr, stream_of(stream));
 }
 
 extern "C" zc_status zc_fp8_matmul_wgrad(const void *d_a, const uint8_t *d_a_scales, uint32_t a_type, uint64_t n,
@@ -792,5 +792,5 @@ extern "C" zc_status zc_fp8_matmul_wgrad(const void *d_a, const uint8_t *d_a_sca
     p.groups = groups;
     p.b_shift = 0;
     return launch_wgrad(p, a_type, b_type, out_type == ZC_BF16, sum_mode == ZC_FP8_SUM_FULL,
-                        static_cast<hipStream_t>(stream));
+                        stream_of(stream));
 }

@@ -35,6 +35,13 @@ constexpr uint64_t kMaxRows = 0x7FFFFFFFull - ZC_MOE_ROW_SLACK;
 constexpr uint64_t kMaxCols = 1ull << 28;
 constexpr uint64_t kMaxStride = 1ull << 40;
 
+// A call's stream, asked for once its arguments are accepted.  What another call
+// left pending in the HIP runtime is dropped: launched() then tells of this one's
+// launches only.
+inline hipStream_t stream_of(void *stream) {
+    (void)hipGetLastError();
+    return static_cast<hipStream_t>(stream);
+}
 inline zc_status launched() { return hipGetLastError() == hipSuccess ? ZC_OK : ZC_ERR_HIP; }
 
 // ---------------------------------------------------------------------------

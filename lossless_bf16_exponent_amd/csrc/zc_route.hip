@@ -672,7 +672,7 @@ extern "C" zc_status zc_route(const void *d_logits, uint32_t logits_type, uint64
     if (!tokens) return ZC_OK;
     const RouteArgs a = {d_logits, d_bias, d_ids, d_weights, logits_stride, (uint32_t)tokens, *cfg};
     const bool bf16 = logits_type == ZC_BF16;
-    hipStream_t st = static_cast<hipStream_t>(stream);
+    hipStream_t st = stream_of(stream);
     if (cfg->experts <= 64)
         launch_route<1>(a, bf16, st);
     else if (cfg->experts <= 128)
@@ -702,7 +702,7 @@ extern "C" zc_status zc_route_backward(const void *d_logits, uint32_t logits_typ
                          *cfg};
     const RouteBackArgs a = {f, d_dweights, d_dlogits, dlogits_stride};
     const bool bf16 = logits_type == ZC_BF16;
-    hipStream_t st = static_cast<hipStream_t>(stream);
+    hipStream_t st = stream_of(stream);
     if (cfg->experts <= 64)
         launch_route_backward<1>(a, bf16, st);
     else if (cfg->experts <= 128)
