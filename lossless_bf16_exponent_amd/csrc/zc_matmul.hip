@@ -75,14 +75,13 @@ typedef uint32_t u32v2a2 __attribute__((ext_vector_type(2), aligned(2)));
 // A wave's loads straight into LDS (16 or 4 bytes a lane, the lanes' results one
 // after another from the wave-uniform address in M0), from a uniform base and a
 // 32-bit offset a lane.  Inline assembly, so that the compiler adds no waits of
-// its own: the kernel counts them.
+// its own: the kernel counts them.  M0 is an operand, which the compiler sets, so
+// that it knows of every change of it.
 __device__ __forceinline__ void lds_load16(const uint8_t *base, uint32_t offset, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(offset), "s"(base)
-                 : "memory");
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(offset), "s"(base), "{m0}"(lds) : "memory");
 }
 __device__ __forceinline__ void lds_load4(const uint8_t *base, uint32_t offset, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(offset), "s"(base)
-                 : "memory");
+    asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(offset), "s"(base), "{m0}"(lds) : "memory");
 }
 template <int VM>
 __device__ __forceinline__ void wait_and_meet() {
