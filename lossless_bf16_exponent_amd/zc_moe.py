@@ -3,8 +3,9 @@
 Every function has the name of the C entry point it calls and its arguments in
 the same order; pointer and stream arguments are those of ``zc`` (an integer
 device address or anything with ``data_ptr()``; None is NULL).  A nonzero status
-raises ``zc.ZcError``.  All work runs in the HIP kernels of libzc.so: there is
-no fallback path.
+raises ``zc.ZcError``.  A product is summed in full (ZC_FP8_SUM_FULL) unless the
+caller asks for the faster sums.  All work runs in the HIP kernels of libzc.so:
+there is no fallback path.
 """
 from __future__ import annotations
 
@@ -166,14 +167,14 @@ def zc_fp8_matmul_workspace_bytes(m, n, k, groups) -> int:
 
 
 def zc_fp8_matmul(d_a, d_a_scales, a_type, m, d_b, d_b_scales, b_type, n, k, groups, d_offsets, d_out, out_type,
-                  out_stride, sum_mode=ZC_FP8_SUM_FAST, d_workspace=None, workspace_bytes=0, stream=None) -> None:
+                  out_stride, sum_mode=ZC_FP8_SUM_FULL, d_workspace=None, workspace_bytes=0, stream=None) -> None:
     _check(_lib.zc_fp8_matmul(_ptr(d_a), _ptr(d_a_scales), a_type, m, _ptr(d_b), _ptr(d_b_scales), b_type, n, k, groups,
                               _ptr(d_offsets), _ptr(d_out), out_type, out_stride, sum_mode, _ptr(d_workspace),
                               workspace_bytes, _stream(stream)), "zc_fp8_matmul")
 
 
 def zc_fp8_matmul_wgrad(d_a, d_a_scales, a_type, n, d_b, d_b_scales, b_type, k, padded_rows, rows, groups, d_offsets,
-                        d_out, out_type, sum_mode=ZC_FP8_SUM_FAST, stream=None) -> None:
+                        d_out, out_type, sum_mode=ZC_FP8_SUM_FULL, stream=None) -> None:
     _check(_lib.zc_fp8_matmul_wgrad(_ptr(d_a), _ptr(d_a_scales), a_type, n, _ptr(d_b), _ptr(d_b_scales), b_type, k,
                                     padded_rows, rows, groups, _ptr(d_offsets), _ptr(d_out), out_type,
                                     sum_mode, _stream(stream)), "zc_fp8_matmul_wgrad")

@@ -174,3 +174,10 @@ def test_nothing_to_do_is_ok(zc, moe):
                      ("zc_swiglu", [None, 0, 64, 128, None, 64, None, None, None, None, None]),
                      ("zc_swiglu_backward", [None, None, 0, 64, None, 64, None, 128, None])):
         assert call(zc, moe, fn, args) == 0, fn
+
+
+def test_products_are_summed_in_full_unless_told_otherwise(moe):
+    """A caller who does not say how a product is summed gets the sums that lose nothing."""
+    import inspect
+    for f in (moe.zc_fp8_matmul, moe.zc_fp8_matmul_wgrad):
+        assert inspect.signature(f).parameters["sum_mode"].default == moe.ZC_FP8_SUM_FULL
