@@ -6,8 +6,8 @@ import pytest
 import torch
 
 import moe_ref as ref
-from moe_gpu import Out, device, moe
-from test_gpu_moe_fp8 import close_on_device
+from moe_gpu import Out, close, device, moe
+from test_gpu_moe_fp8 import close_on_device, fast_tolerance, product_tolerance
 
 pytestmark = pytest.mark.gpu
 TYPES = [(ref.E4M3, ref.E4M3), (ref.E5M2, ref.E4M3), (ref.E4M3, ref.E5M2), (ref.E5M2, ref.E5M2)]
@@ -113,3 +113,42 @@ def test_weight_gradients_of_256_by_256(zc, counts, ta, tb, f32):
         pair = [stood_for(q[:, 128 * b0:128 * b1], s[:, b0:b1], kind, c) for q, s, kind in ops]
         close_on_device(out.t[i], *pair, f32, "group %d" % i)
         at = 128 * b1
+
+
+@pytest.mark.parametrize("fast", [False, True])
+@pytest.mark.parametrize("m", [3, 70])
+@pytest.mark.parametrize("ta,tb", TYPES)
+def test_smallest_and_largest_scales(zc, ta, tb, m, fast):
+    """Blocks next to the smallest numbers (scale bytes 0 to 3) times blocks next to the largest, and the other way round."""
+    n, k = 66, 256
+    r = np.random.default_rng([m, ta, tb])
+    for low, high in ((-126, 100), (-117, 110), (-130, 115)):
+        small, large = [ref.bf16(r.uniform(-2, 2, (rows, k)) * 2.0 ** e) for rows, e in ((m, low), (n, high))]
+        for swap in (False, True):
+            x, w = (ref.bf16(large[:1] * r.uniform(0.5, 1.0, (m, 1))), ref.bf16(small[:1] * r.uniform(0.5, 1.0, (n, 1)))) if swap else (small, large)
+            aq, as_ = ref.quantize(x, ta)
+            bq, bs = ref.quantize(w, tb, 128)
+            a, b = ref.values(aq, as_, ta, k), ref.values(bq, bs, tb, k, 128)
+            out = Out((m, n), torch.float32)
+            ops = [device(v) for v in (aq, as_, bq, bs)]
+            zc.zc_fp8_matmul(ops[0], ops[1], ta, m, ops[2], ops[3], tb, n, k, 1, None, out, zc.ZC_F32, n,
+                             zc.ZC_FP8_SUM_FAST if fast else zc.ZC_FP8_SUM_FULL)
+            want = a @ b.T
+            tol = fast_tolerance(a, b, want, True) if fast else product_tolerance(want, np.abs(a) @ np.abs(b).T, k, True)
+            close(out.numpy(), want, tol, "scales %s" % ((low, high, swap),))
+
+
+@pytest.mark.parametrize("kind", [ref.E4M3, ref.E5M2])
+@pytest.mark.parametrize("exponent", [-133, -130, -126, -118, 100, 120])
+def test_reblocking_keeps_the_smallest_values(zc, kind, exponent):
+    """The transposed form of an 8-bit checkpoint whose values are next to the smallest or the largest numbers."""
+    rows, cols = 150, 200
+    r = np.random.default_rng([kind, exponent + 200])
+    x = ref.bf16(r.uniform(-4, 4, (rows, cols)) * 2.0 ** exponent)
+    q, s = ref.quantize(x, kind)
+    padded = zc.zc_fp8_padded_rows(rows, 1)
+    qt, st = Out((cols, padded), torch.uint8), Out((cols, zc.zc_fp8_scale_stride(padded)), torch.uint8)
+    zc.zc_fp8_quantize_t(device(q), device(s), kind, rows, cols, zc.zc_fp8_stride(cols), 1, None, ref.E4M3, qt, st, padded)
+    want_q, want_s, n = ref.quantize_t(ref.values(q, s, kind, cols), ref.E4M3, 1, None, padded)
+    assert n == padded and np.array_equal(qt.numpy(), want_q)
+    assert np.array_equal(st.numpy()[:, :padded // 128], want_s[:, :padded // 128])
