@@ -24,16 +24,18 @@ struct GateArgs {
 // nor loses digits to a subtraction.  The hardware exponential and reciprocal (1
 // ulp of 32 bits) are far finer than the BF16 results.  Below e^-87 t has few
 // digits in 32 bits or none, and g t times a large value is a normal number
-// again: past |g| = 80 it is taken 2^64 higher, and a sigmoid that is t keeps that
-// factor until the products are made (unit; 1 else).  There 1 + t is 1, and g t is
-// nothing beside 1.  NaN stays NaN.
+// again.  A wave that holds a gate past 80 (FAR) therefore takes t 2^64 higher
+// there, and a sigmoid that is t keeps that factor until the products are made
+// (unit; 1 else); 1 + t is then 1, and g t nothing beside 1.  NaN stays NaN.
+constexpr float kFar = 80.0f;
 struct Sigmoid {
     float s, rest, unit;
 };
+template <bool FAR>
 __device__ __forceinline__ Sigmoid sigmoid(float g) {
     const float a = fabsf(g);
-    const bool far = a > 80.0f;
-    const float t = __builtin_amdgcn_exp2f(fmaf(a, -1.44269504f, far ? 64.0f : 0.0f));
+    const bool far = FAR && a > kFar;
+    const float t = __builtin_amdgcn_exp2f(FAR ? fmaf(a, -1.44269504f, far ? 64.0f : 0.0f) : a * -1.44269504f);
     const float r = __builtin_amdgcn_rcpf(1.0f + (far ? 0.0f : t)), tr = t * r;
     Sigmoid o;
     o.s = g >= 0.0f ? r : tr;
@@ -41,9 +43,33 @@ __device__ __forceinline__ Sigmoid sigmoid(float g) {
     o.unit = far && g < 0.0f ? 0x1p-64f : 1.0f;
     return o;
 }
-__device__ __forceinline__ float gated(float g, float u) {
-    const Sigmoid o = sigmoid(g);
-    return g * o.s * u * o.unit;
+// Whether a lane of the wave holds a gate past kFar.
+__device__ __forceinline__ bool any_far(const float (&g)[8]) {
+    float m = 0.0f;
+#pragma unroll
+    for (uint32_t i = 0; i < 8; ++i) m = fmaxf(m, fabsf(g[i]));
+    return __ballot(m > kFar) != 0;
+}
+template <bool FAR>
+__device__ __forceinline__ u32v4 gated8(const float (&g)[8], const u32v4 &u) {
+    u32v4 h;
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i) {
+        const Sigmoid a = sigmoid<FAR>(g[2 * i]), b = sigmoid<FAR>(g[2 * i + 1]);
+        h[i] = bf_pack(g[2 * i] * a.s * bf_lo(u[i]) * a.unit, g[2 * i + 1] * b.s * bf_hi(u[i]) * b.unit);
+    }
+    return h;
+}
+template <bool FAR>
+__device__ __forceinline__ void gradients8(const float (&g)[8], const float (&u)[8], const u32v4 &dh, float (&dg)[8],
+                                           float (&du)[8]) {
+#pragma unroll
+    for (uint32_t i = 0; i < 8; ++i) {
+        const float d = (i & 1) ? bf_hi(dh[i / 2]) : bf_lo(dh[i / 2]);
+        const Sigmoid o = sigmoid<FAR>(g[i]);
+        dg[i] = d * u[i] * (o.s * fmaf(g[i], o.rest, 1.0f)) * o.unit;
+        du[i] = d * (g[i] * o.s) * o.unit;
+    }
 }
 
 // The 8 values' 8-bit form under the block's scale (16 lanes a block); lane 0
@@ -83,10 +109,10 @@ __global__ __launch_bounds__(kGThreads) void swiglu_kernel(GateArgs a) {
             if (kb + 1 == a.blocks && 2 * a.blocks + sub < a.kss) s[2 * a.blocks + sub] = 0;
         }
         if (!a.h && !a.hq) continue;
-        u32v4 h;
+        float gf[8];
 #pragma unroll
-        for (uint32_t i = 0; i < 4; ++i)
-            h[i] = bf_pack(gated(bf_lo(g[i]), bf_lo(u[i])), gated(bf_hi(g[i]), bf_hi(u[i])));
+        for (uint32_t i = 0; i < 8; ++i) gf[i] = (i & 1) ? bf_hi(g[i / 2]) : bf_lo(g[i / 2]);
+        const u32v4 h = any_far(gf) ? gated8<true>(gf, u) : gated8<false>(gf, u);
         if (a.h) store_values<WIDE>(a.h + (uint64_t)row * a.h_stride + c, h, n);
         if (a.hq) {
             uint8_t *s = a.hs + (uint64_t)row * a.hss;
@@ -124,11 +150,13 @@ __global__ __launch_bounds__(kGThreads) void swiglu_backward_kernel(GateArgs a) 
         }
 #pragma unroll
         for (uint32_t i = 0; i < 8; ++i) {
-            const float gv = g[i] * gs, uv = u[i] * us, d = (i & 1) ? bf_hi(dh[i / 2]) : bf_lo(dh[i / 2]);
-            const Sigmoid sg = sigmoid(gv);
-            dg[i] = d * uv * (sg.s * fmaf(gv, sg.rest, 1.0f)) * sg.unit;
-            du[i] = d * (gv * sg.s) * sg.unit;
+            g[i] *= gs;
+            u[i] *= us;
         }
+        if (any_far(g))
+            gradients8<true>(g, u, dh, dg, du);
+        else
+            gradients8<false>(g, u, dh, dg, du);
         u32v4 wg, wu;
 #pragma unroll
         for (uint32_t i = 0; i < 4; ++i) {
