@@ -46,8 +46,11 @@
  * zeros).  A value is stored as v / scale rounded to the type, to nearest with
  * ties to even; since the scale is a power of two this is its only rounding.
  * NaN and infinities keep their kind (e4m3 has no infinity: NaN), and do not
- * enter the scale.  Power-of-two scales are what the scaled matrix
- * instructions of gfx950 apply by themselves.
+ * enter the scale.  A magnitude from 1.9375 * 2^127 (e4m3) or 1.875 * 2^127 (e5m2)
+ * up rounds to 2^128, which BF16 and floats cannot hold: full sums,
+ * zc_fp8_quantize_t from 8 bits and zc_swiglu_backward take it as an infinity.
+ * Power-of-two scales are what the scaled matrix instructions of gfx950 apply by
+ * themselves.
  *   values  rows of zc_fp8_stride(cols) bytes: cols rounded up to 128, the
  *           bytes past cols are zero
  *   scales  rows of zc_fp8_scale_stride(cols) bytes: ceil(cols / 128) of them

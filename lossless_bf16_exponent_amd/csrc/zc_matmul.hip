@@ -587,10 +587,19 @@ struct Choice {
 // Else the shape with the least time by this model: a round of workgroups over the
 // 256 CUs takes, for each block of the contraction, 1.2 us with tiles of 256 x 256,
 // 0.85 with 256 x 128, 0.55 with 128 x 128 alone on a CU, and 1.1 with two of those
-// on it (512 x 4096 x 7168: 67, 45, 29, 40 us; 4096 x 4096 x 7168: 92, 117, 137,
-// 122), and 4 to 9 us for its start and end.  With few tiles of 128 x 128 the
+// on it, and 4 to 9 us for its start and end.  With few tiles of 128 x 128 the
 // contraction is split, at the cost of writing and adding the parts (4 us and
 // their bytes).  Groups are taken to have equally many rows.
+//
+// The model orders the shapes; its times are rough (512 x 4096 x 7168: 67, 45, 29
+// and 40 us measured, 76, 54, 35 and 66 by the model; 4096 x 4096 x 7168: 92, 117,
+// 137 and 122, and 76, 107, 139 and 131).  Every shape was timed at 17 to 2048 rows (powers
+// of two, and 17 and 33), n = 512, 2048, 4096, 8192 and k = 512, 2048, 7168, 16384,
+// one group, weights from memory, calls back to back: of those 128 products the
+// choice is within 5 % of the fastest shape in 97 and within 20 % in 114.  The
+// others, up to 1.7 times the fastest: 33 to 128 rows with k = 2048 or n = 512,
+// where rows_kernel takes 7 to 9 us and a split 11 to 13 (its second launch), and
+// 17 rows with k = 16384, where a split takes 15 to 17 and rows_kernel 20 to 21.
 static Choice choose(uint64_t m, uint64_t n, uint64_t k, uint64_t groups, bool full) {
     Choice c = {0, kTile128, 1};
     const uint64_t used = m < groups ? m : groups, per_group = used ? ceil_div(m, used) : 0;

@@ -12,6 +12,9 @@
 //                 and only those are scored and ranked in 64 bits.  A token whose
 //                 groups the bound cannot tell apart, or with more than 16
 //                 candidates, goes through the first one's code in place.
+// Softmax weights that are not renormalised, and softmax with a bias, have no such
+// bound and take the first: 8192 tokens of 256 experts in 8 groups 31.5 us there,
+// 10 to 13 in the second.
 #include <type_traits>
 
 #include "zc_moe_device.h"

@@ -90,8 +90,8 @@ __device__ __forceinline__ void keep8(const u32v4 &w, uint8_t *q, uint8_t *s, ui
 }
 
 // Everything is read once and written once: non-temporal accesses (65536 x 2048
-// forward 198 -> 181 us, backward 197 -> 178 us; 5.9 and 6.0 TB/s, past what a large
-// copy reaches).  16 lanes of eight values a block of 128.
+// forward 198 -> 181 us, backward 197 -> 178 us).  Now 181 and 171 us, 5.9 and 6.3
+// TB/s, past what a large copy reaches.  16 lanes of eight values a block of 128.
 template <bool WIDE>
 __global__ __launch_bounds__(kGThreads) void swiglu_kernel(GateArgs a) {
     const uint32_t sub = threadIdx.x % kGLanes;
