@@ -331,17 +331,17 @@ extern "C" zc_status zc_dispatch_plan(const int32_t *d_ids, uint64_t tokens, uin
         !aligned(d_workspace, 16))
         return ZC_ERR_MISALIGNED;
     if (tokens && workspace_bytes < zc_dispatch_workspace_bytes(tokens, top_k, experts)) return ZC_ERR_CAPACITY;
-    hipStream_t st = stream_of(stream);
+    Launches on(stream);
     if (!tokens) {
-        hipLaunchKernelGGL(plan_empty_kernel, dim3(1), dim3(256), 0, st, d_offsets, experts + 1);
-        return launched();
+        on.launch(plan_empty_kernel, dim3(1), dim3(256), d_offsets, experts + 1);
+        return on.status();
     }
     PlanArgs a = {d_ids, static_cast<uint32_t *>(d_workspace), d_offsets, d_position, d_source,
                   (uint32_t)(tokens * top_k), experts, 0, per_chunk_of(tokens * top_k)};
     a.chunks = (uint32_t)ceil_div(a.copies, a.per_chunk);
-    if (a.chunks > 1) hipLaunchKernelGGL(plan_count_kernel, dim3(a.chunks), dim3(kPlanThreads), 0, st, a);
-    hipLaunchKernelGGL(plan_place_kernel, dim3(a.chunks), dim3(kPlanThreads), 0, st, a);
-    return launched();
+    if (a.chunks > 1) on.launch(plan_count_kernel, dim3(a.chunks), dim3(kPlanThreads), a);
+    on.launch(plan_place_kernel, dim3(a.chunks), dim3(kPlanThreads), a);
+    return on.status();
 }
 
 extern "C" zc_status zc_dispatch(const void *d_x, uint64_t tokens, uint64_t hidden, uint64_t x_stride,
@@ -363,13 +363,13 @@ extern "C" zc_status zc_dispatch(const void *d_x, uint64_t tokens, uint64_t hidd
     a.top_k = top_k;
     a.rows = (uint32_t)rows;
     a.hidden = (uint32_t)hidden;
-    hipStream_t st = stream_of(stream);
+    Launches on(stream);
     const dim3 block(kRowThreads);
     if (hidden % 8 == 0 && wide(d_x, x_stride) && wide(d_out, out_stride))
-        hipLaunchKernelGGL(dispatch_kernel<true>, row_grid(a.tokens, a.hidden), block, 0, st, a);
+        on.launch(dispatch_kernel<true>, row_grid(a.tokens, a.hidden), block, a);
     else
-        hipLaunchKernelGGL(dispatch_kernel<false>, row_grid(a.tokens, a.hidden), block, 0, st, a);
-    return launched();
+        on.launch(dispatch_kernel<false>, row_grid(a.tokens, a.hidden), block, a);
+    return on.status();
 }
 
 extern "C" zc_status zc_combine(const void *d_z, uint64_t rows, uint64_t hidden, uint64_t z_stride,
@@ -393,13 +393,13 @@ extern "C" zc_status zc_combine(const void *d_z, uint64_t rows, uint64_t hidden,
     a.top_k = top_k;
     a.rows = (uint32_t)rows;
     a.hidden = (uint32_t)hidden;
-    hipStream_t st = stream_of(stream);
+    Launches on(stream);
     const dim3 block(kRowThreads);
     if (hidden % 8 == 0 && wide(d_z, z_stride) && wide(d_y, y_stride))
-        hipLaunchKernelGGL(combine_kernel<true>, row_grid(a.tokens, a.hidden), block, 0, st, a);
+        on.launch(combine_kernel<true>, row_grid(a.tokens, a.hidden), block, a);
     else
-        hipLaunchKernelGGL(combine_kernel<false>, row_grid(a.tokens, a.hidden), block, 0, st, a);
-    return launched();
+        on.launch(combine_kernel<false>, row_grid(a.tokens, a.hidden), block, a);
+    return on.status();
 }
 
 extern "C" zc_status zc_combine_backward(const void *d_dy, uint64_t dy_stride, const void *d_z, uint64_t rows,
@@ -429,12 +429,12 @@ extern "C" zc_status zc_combine_backward(const void *d_dy, uint64_t dy_stride, c
     a.top_k = top_k;
     a.rows = (uint32_t)rows;
     a.hidden = (uint32_t)hidden;
-    hipStream_t st = stream_of(stream);
+    Launches on(stream);
     const dim3 grid(token_blocks(a.tokens)), block(kRowThreads);
     if (hidden % 8 == 0 && wide(d_dy, dy_stride) && (!d_dweights || wide(d_z, z_stride)) &&
         (!d_dz || wide(d_dz, dz_stride)))
-        hipLaunchKernelGGL(combine_backward_kernel<true>, grid, block, 0, st, a);
+        on.launch(combine_backward_kernel<true>, grid, block, a);
     else
-        hipLaunchKernelGGL(combine_backward_kernel<false>, grid, block, 0, st, a);
-    return launched();
+        on.launch(combine_backward_kernel<false>, grid, block, a);
+    return on.status();
 }

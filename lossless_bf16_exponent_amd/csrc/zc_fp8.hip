@@ -232,37 +232,37 @@ __global__ __launch_bounds__(kQThreads) void transpose_kernel(SquareArgs a) {
 static uint32_t grid_of(uint64_t units) { return (uint32_t)(units < (1u << 20) ? units : (1u << 20)); }
 
 template <uint32_t TYPE>
-static void launch_quantize(const QuantArgs &a, bool square, bool wide, hipStream_t st) {
+static void launch_quantize(const QuantArgs &a, bool square, bool wide, Launches &on) {
     const dim3 block(kQThreads);
     if (square) {
         const dim3 grid(grid_of(ceil_div(a.rows, kBlock) * a.blocks));
         if (wide)
-            hipLaunchKernelGGL((quantize_square_kernel<TYPE, true>), grid, block, 0, st, a);
+            on.launch((quantize_square_kernel<TYPE, true>), grid, block, a);
         else
-            hipLaunchKernelGGL((quantize_square_kernel<TYPE, false>), grid, block, 0, st, a);
+            on.launch((quantize_square_kernel<TYPE, false>), grid, block, a);
     } else {
         const dim3 grid(grid_of(ceil_div((uint64_t)a.rows * a.blocks, kQBlocks)));
         if (wide)
-            hipLaunchKernelGGL((quantize_kernel<TYPE, true>), grid, block, 0, st, a);
+            on.launch((quantize_kernel<TYPE, true>), grid, block, a);
         else
-            hipLaunchKernelGGL((quantize_kernel<TYPE, false>), grid, block, 0, st, a);
+            on.launch((quantize_kernel<TYPE, false>), grid, block, a);
     }
 }
 
 template <uint32_t SRC, uint32_t TYPE>
-static void launch_quantize_t(const TransArgs &a, bool wide, uint32_t grid, hipStream_t st) {
+static void launch_quantize_t(const TransArgs &a, bool wide, uint32_t grid, Launches &on) {
     if (wide)
-        hipLaunchKernelGGL((quantize_t_kernel<SRC, TYPE, true>), dim3(grid), dim3(kQThreads), 0, st, a);
+        on.launch((quantize_t_kernel<SRC, TYPE, true>), dim3(grid), dim3(kQThreads), a);
     else
-        hipLaunchKernelGGL((quantize_t_kernel<SRC, TYPE, false>), dim3(grid), dim3(kQThreads), 0, st, a);
+        on.launch((quantize_t_kernel<SRC, TYPE, false>), dim3(grid), dim3(kQThreads), a);
 }
 
 template <uint32_t SRC>
-static void launch_quantize_t(uint32_t type, const TransArgs &a, bool wide, uint32_t grid, hipStream_t st) {
+static void launch_quantize_t(uint32_t type, const TransArgs &a, bool wide, uint32_t grid, Launches &on) {
     if (type == ZC_FP8_E4M3)
-        launch_quantize_t<SRC, ZC_FP8_E4M3>(a, wide, grid, st);
+        launch_quantize_t<SRC, ZC_FP8_E4M3>(a, wide, grid, on);
     else
-        launch_quantize_t<SRC, ZC_FP8_E5M2>(a, wide, grid, st);
+        launch_quantize_t<SRC, ZC_FP8_E5M2>(a, wide, grid, on);
 }
 
 }  // namespace moe
@@ -292,12 +292,12 @@ extern "C" zc_status zc_fp8_quantize(const void *d_x, uint64_t rows, uint64_t co
                          stride8(cols), scale_stride(cols), (uint32_t)rows, (uint32_t)cols,
                          (uint32_t)ceil_div(cols, kBlock)};
     const bool wide = aligned(d_x, 16) && x_stride % 8 == 0 && cols % 8 == 0;
-    hipStream_t st = stream_of(stream);
+    Launches on(stream);
     if (type == ZC_FP8_E4M3)
-        launch_quantize<ZC_FP8_E4M3>(a, block_rows != 1, wide, st);
+        launch_quantize<ZC_FP8_E4M3>(a, block_rows != 1, wide, on);
     else
-        launch_quantize<ZC_FP8_E5M2>(a, block_rows != 1, wide, st);
-    return launched();
+        launch_quantize<ZC_FP8_E5M2>(a, block_rows != 1, wide, on);
+    return on.status();
 }
 
 extern "C" zc_status zc_fp8_quantize_t(const void *d_x, const uint8_t *d_x_scales, uint32_t x_type, uint64_t rows,
@@ -321,14 +321,14 @@ extern "C" zc_status zc_fp8_quantize_t(const void *d_x, const uint8_t *d_x_scale
     a.units = zc_fp8_padded_rows(rows, groups) / kBlock * a.col_tiles;
     const uint32_t grid = grid_of(a.units);
     const bool wide = aligned(d_x, 16) && x_stride % 8 == 0 && cols % 8 == 0;
-    hipStream_t st = stream_of(stream);
+    Launches on(stream);
     if (x_type == ZC_BF16)
-        launch_quantize_t<ZC_BF16>(type, a, wide, grid, st);
+        launch_quantize_t<ZC_BF16>(type, a, wide, grid, on);
     else if (x_type == ZC_FP8_E4M3)
-        launch_quantize_t<ZC_FP8_E4M3>(type, a, true, grid, st);
+        launch_quantize_t<ZC_FP8_E4M3>(type, a, true, grid, on);
     else
-        launch_quantize_t<ZC_FP8_E5M2>(type, a, true, grid, st);
-    return launched();
+        launch_quantize_t<ZC_FP8_E5M2>(type, a, true, grid, on);
+    return on.status();
 }
 
 extern "C" zc_status zc_fp8_transpose(const void *d_q, const uint8_t *d_scales, uint64_t batch, uint64_t rows,
@@ -341,7 +341,7 @@ extern "C" zc_status zc_fp8_transpose(const void *d_q, const uint8_t *d_scales, 
     const SquareArgs a = {static_cast<const uint8_t *>(d_q), d_scales, static_cast<uint8_t *>(d_qt), d_scales_t,
                           (uint32_t)rows, (uint32_t)cols, (uint32_t)ceil_div(rows, kBlock),
                           (uint32_t)ceil_div(cols, kBlock), batch};
-    hipLaunchKernelGGL(transpose_kernel, dim3(grid_of(batch * a.row_blocks * a.col_blocks)), dim3(kQThreads), 0, stream_of(stream),
-                       a);
-    return launched();
+    Launches on(stream);
+    on.launch(transpose_kernel, dim3(grid_of(batch * a.row_blocks * a.col_blocks)), dim3(kQThreads), a);
+    return on.status();
 }

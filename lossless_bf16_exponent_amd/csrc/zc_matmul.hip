@@ -548,26 +548,26 @@ __global__ __launch_bounds__(WAVES * 64) void rows_kernel(MatArgs p) {
 enum Shape { kTile128, kTile128Deep, kTile256x128, kTile256 };
 
 template <bool WGRAD, int FA, int FB, typename T>
-static void launch_tile(const MatArgs &p, bool full, Shape shape, dim3 grid, hipStream_t st) {
+static void launch_tile(const MatArgs &p, bool full, Shape shape, dim3 grid, Launches &on) {
     const dim3 block(kMThreads);
     if (full)
-        hipLaunchKernelGGL((tile_kernel<128, 128, 2, WGRAD, FA, FB, true, T>), grid, block, 0, st, p);
+        on.launch((tile_kernel<128, 128, 2, WGRAD, FA, FB, true, T>), grid, block, p);
     else if (shape == kTile256)
-        hipLaunchKernelGGL((tile_kernel<256, 256, 2, WGRAD, FA, FB, false, T>), grid, block, 0, st, p);
+        on.launch((tile_kernel<256, 256, 2, WGRAD, FA, FB, false, T>), grid, block, p);
     else if (!WGRAD && shape == kTile256x128)
-        hipLaunchKernelGGL((tile_kernel<256, 128, 3, WGRAD, FA, FB, false, T>), grid, block, 0, st, p);
+        on.launch((tile_kernel<256, 128, 3, WGRAD, FA, FB, false, T>), grid, block, p);
     else if (!WGRAD && shape == kTile128Deep)
-        hipLaunchKernelGGL((tile_kernel<128, 128, 3, WGRAD, FA, FB, false, T>), grid, block, 0, st, p);
+        on.launch((tile_kernel<128, 128, 3, WGRAD, FA, FB, false, T>), grid, block, p);
     else
-        hipLaunchKernelGGL((tile_kernel<128, 128, 2, WGRAD, FA, FB, false, T>), grid, block, 0, st, p);
+        on.launch((tile_kernel<128, 128, 2, WGRAD, FA, FB, false, T>), grid, block, p);
 }
 
 template <int FA, int FB, typename T>
-static void launch_rows(const MatArgs &p, uint32_t mt, dim3 grid, hipStream_t st) {
+static void launch_rows(const MatArgs &p, uint32_t mt, dim3 grid, Launches &on) {
     if (mt == 1)
-        hipLaunchKernelGGL((rows_kernel<1, 8, 4, FA, FB, T>), grid, dim3(512), 0, st, p);
+        on.launch((rows_kernel<1, 8, 4, FA, FB, T>), grid, dim3(512), p);
     else
-        hipLaunchKernelGGL((rows_kernel<2, 8, 4, FA, FB, T>), grid, dim3(512), 0, st, p);
+        on.launch((rows_kernel<2, 8, 4, FA, FB, T>), grid, dim3(512), p);
 }
 
 // Upper bound of the tiles of `tile` rows over all groups.
@@ -638,19 +638,19 @@ static Choice choose(uint64_t m, uint64_t n, uint64_t k, uint64_t groups, bool f
 }
 
 template <int FA, int FB>
-static void launch_forward(MatArgs p, bool bf16, bool full, const Choice &c, float *ws, dim3 grid, hipStream_t st) {
+static void launch_forward(MatArgs p, bool bf16, bool full, const Choice &c, float *ws, dim3 grid, Launches &on) {
     if (c.rows_mt) {
         if (bf16)
-            launch_rows<FA, FB, uint16_t>(p, c.rows_mt, grid, st);
+            launch_rows<FA, FB, uint16_t>(p, c.rows_mt, grid, on);
         else
-            launch_rows<FA, FB, uint32_t>(p, c.rows_mt, grid, st);
+            launch_rows<FA, FB, uint32_t>(p, c.rows_mt, grid, on);
         return;
     }
     if (c.splits == 1) {
         if (bf16)
-            launch_tile<false, FA, FB, uint16_t>(p, full, c.shape, grid, st);
+            launch_tile<false, FA, FB, uint16_t>(p, full, c.shape, grid, on);
         else
-            launch_tile<false, FA, FB, uint32_t>(p, full, c.shape, grid, st);
+            launch_tile<false, FA, FB, uint32_t>(p, full, c.shape, grid, on);
         return;
     }
     void *out = p.out;
@@ -659,19 +659,19 @@ static void launch_forward(MatArgs p, bool bf16, bool full, const Choice &c, flo
     p.ldo = p.n;
     p.split_stride = (uint64_t)p.rows * p.n;
     grid.y = c.splits;
-    launch_tile<false, FA, FB, uint32_t>(p, full, c.shape, grid, st);
+    launch_tile<false, FA, FB, uint32_t>(p, full, c.shape, grid, on);
     const uint64_t units = ceil_div((uint64_t)p.rows * ceil_div(p.n, 4), 256);
     const dim3 add((uint32_t)(units < 4096 ? units : 4096));
     if (bf16)
-        hipLaunchKernelGGL(add_parts_kernel<uint16_t>, add, dim3(256), 0, st, ws, c.splits, p.split_stride,
-                           static_cast<uint16_t *>(out), p.rows, p.n, ldo, p.offsets, p.groups);
+        on.launch(add_parts_kernel<uint16_t>, add, dim3(256), ws, c.splits, p.split_stride, static_cast<uint16_t *>(out),
+                  p.rows, p.n, ldo, p.offsets, p.groups);
     else
-        hipLaunchKernelGGL(add_parts_kernel<uint32_t>, add, dim3(256), 0, st, ws, c.splits, p.split_stride,
-                           static_cast<uint32_t *>(out), p.rows, p.n, ldo, p.offsets, p.groups);
+        on.launch(add_parts_kernel<uint32_t>, add, dim3(256), ws, c.splits, p.split_stride, static_cast<uint32_t *>(out),
+                  p.rows, p.n, ldo, p.offsets, p.groups);
 }
 
 static zc_status launch_forward(const MatArgs &p, uint32_t ta, uint32_t tb, bool bf16, bool full, Choice c, float *ws,
-                                hipStream_t st) {
+                                Launches &on) {
     if (!ws) c.splits = 1;
     const uint64_t tm = c.rows_mt ? 16 * c.rows_mt : c.shape == kTile128 || c.shape == kTile128Deep ? 128 : 256;
     const uint64_t tn = c.rows_mt ? 16 : c.shape == kTile256 ? 256 : 128;
@@ -680,33 +680,33 @@ static zc_status launch_forward(const MatArgs &p, uint32_t ta, uint32_t tb, bool
     if (tiles > 0xFFFFFFFFull / threads - 256) return ZC_ERR_INVALID_ARG;
     const dim3 grid((uint32_t)(c.rows_mt ? tiles : ceil_div(tiles, 8) * 8));
     const int fa = ta == ZC_FP8_E5M2, fb = tb == ZC_FP8_E5M2;
-    if (!fa && !fb) launch_forward<0, 0>(p, bf16, full, c, ws, grid, st);
-    if (!fa && fb) launch_forward<0, 1>(p, bf16, full, c, ws, grid, st);
-    if (fa && !fb) launch_forward<1, 0>(p, bf16, full, c, ws, grid, st);
-    if (fa && fb) launch_forward<1, 1>(p, bf16, full, c, ws, grid, st);
-    return launched();
+    if (!fa && !fb) launch_forward<0, 0>(p, bf16, full, c, ws, grid, on);
+    if (!fa && fb) launch_forward<0, 1>(p, bf16, full, c, ws, grid, on);
+    if (fa && !fb) launch_forward<1, 0>(p, bf16, full, c, ws, grid, on);
+    if (fa && fb) launch_forward<1, 1>(p, bf16, full, c, ws, grid, on);
+    return on.status();
 }
 
 template <int FA, int FB>
-static void launch_wgrad(const MatArgs &p, bool bf16, bool full, Shape shape, dim3 grid, hipStream_t st) {
+static void launch_wgrad(const MatArgs &p, bool bf16, bool full, Shape shape, dim3 grid, Launches &on) {
     if (bf16)
-        launch_tile<true, FA, FB, uint16_t>(p, full, shape, grid, st);
+        launch_tile<true, FA, FB, uint16_t>(p, full, shape, grid, on);
     else
-        launch_tile<true, FA, FB, uint32_t>(p, full, shape, grid, st);
+        launch_tile<true, FA, FB, uint32_t>(p, full, shape, grid, on);
 }
 
-static zc_status launch_wgrad(const MatArgs &p, uint32_t ta, uint32_t tb, bool bf16, bool full, hipStream_t st) {
+static zc_status launch_wgrad(const MatArgs &p, uint32_t ta, uint32_t tb, bool bf16, bool full, Launches &on) {
     const uint64_t t256 = ceil_div(p.m, 256) * ceil_div(p.n, 256) * p.groups;
     const Shape shape = !full && t256 >= 192 ? kTile256 : kTile128;
     const uint64_t tiles = shape == kTile256 ? t256 : ceil_div(p.m, 128) * ceil_div(p.n, 128) * p.groups;
     if (tiles > 0xFFFF00u) return ZC_ERR_INVALID_ARG;
     const dim3 grid((uint32_t)ceil_div(tiles, 256) * 256);
     const int fa = ta == ZC_FP8_E5M2, fb = tb == ZC_FP8_E5M2;
-    if (!fa && !fb) launch_wgrad<0, 0>(p, bf16, full, shape, grid, st);
-    if (!fa && fb) launch_wgrad<0, 1>(p, bf16, full, shape, grid, st);
-    if (fa && !fb) launch_wgrad<1, 0>(p, bf16, full, shape, grid, st);
-    if (fa && fb) launch_wgrad<1, 1>(p, bf16, full, shape, grid, st);
-    return launched();
+    if (!fa && !fb) launch_wgrad<0, 0>(p, bf16, full, shape, grid, on);
+    if (!fa && fb) launch_wgrad<0, 1>(p, bf16, full, shape, grid, on);
+    if (fa && !fb) launch_wgrad<1, 0>(p, bf16, full, shape, grid, on);
+    if (fa && fb) launch_wgrad<1, 1>(p, bf16, full, shape, grid, on);
+    return on.status();
 }
 
 // A tile's rows are reached by 32-bit offsets from its first: 256 rows of at most 2^24 bytes.
@@ -764,8 +764,9 @@ extern "C" zc_status zc_fp8_matmul(const void *d_a, const uint8_t *d_a_scales, u
     const bool full = sum_mode == ZC_FP8_SUM_FULL;
     const Choice c = choose(m, n, k, groups, full);
     const bool room = d_workspace && workspace_bytes >= zc_fp8_matmul_workspace_bytes(m, n, k, groups);
+    Launches on(stream);
     return launch_forward(p, a_type, b_type, out_type == ZC_BF16, full, c,
-                          room ? static_cast<float *>(d_workspace) : nullptr, stream_of(stream));
+                          room ? static_cast<float *>(d_workspace) : nullptr, on);
 }
 
 extern "C" zc_status zc_fp8_matmul_wgrad(const void *d_a, const uint8_t *d_a_scales, uint32_t a_type, uint64_t n,
@@ -799,6 +800,6 @@ extern "C" zc_status zc_fp8_matmul_wgrad(const void *d_a, const uint8_t *d_a_sca
     p.rows = (uint32_t)rows;
     p.groups = groups;
     p.b_shift = 0;
-    return launch_wgrad(p, a_type, b_type, out_type == ZC_BF16, sum_mode == ZC_FP8_SUM_FULL,
-                        stream_of(stream));
+    Launches on(stream);
+    return launch_wgrad(p, a_type, b_type, out_type == ZC_BF16, sum_mode == ZC_FP8_SUM_FULL, on);
 }

@@ -624,7 +624,7 @@ static bool certifiable(const RouteArgs &a) {
 }
 
 template <uint32_t R, bool BF16>
-static void launch_route(const RouteArgs &a, hipStream_t st) {
+static void launch_route(const RouteArgs &a, Launches &on) {
     const dim3 block(kRouteWaves * 64);
     if constexpr (R <= 8) {
         if (certifiable(a)) {
@@ -634,30 +634,29 @@ static void launch_route(const RouteArgs &a, hipStream_t st) {
             for (uint64_t first = 0; first < a.tokens; first += most * kRouteWaves * kRowTokens) {
                 const uint64_t blocks = ceil_div(a.tokens - first, kRouteWaves * kRowTokens);
                 part.first = (uint32_t)first;
-                hipLaunchKernelGGL((route_kernel<4 * R, BF16>), dim3((uint32_t)(blocks < most ? blocks : most)), block,
-                                   0, st, part);
+                on.launch((route_kernel<4 * R, BF16>), dim3((uint32_t)(blocks < most ? blocks : most)), block, part);
             }
             return;
         }
     }
-    hipLaunchKernelGGL((rank_kernel<R, BF16>), dim3(route_blocks(a.tokens)), block, 0, st, a);
+    on.launch((rank_kernel<R, BF16>), dim3(route_blocks(a.tokens)), block, a);
 }
 
 template <uint32_t R>
-static void launch_route(const RouteArgs &a, bool bf16, hipStream_t st) {
+static void launch_route(const RouteArgs &a, bool bf16, Launches &on) {
     if (bf16)
-        launch_route<R, true>(a, st);
+        launch_route<R, true>(a, on);
     else
-        launch_route<R, false>(a, st);
+        launch_route<R, false>(a, on);
 }
 
 template <uint32_t R>
-static void launch_route_backward(const RouteBackArgs &a, bool bf16, hipStream_t st) {
+static void launch_route_backward(const RouteBackArgs &a, bool bf16, Launches &on) {
     const dim3 grid(route_blocks(a.f.tokens)), block(kRouteWaves * 64);
     if (bf16)
-        hipLaunchKernelGGL((route_backward_kernel<R, true>), grid, block, 0, st, a);
+        on.launch((route_backward_kernel<R, true>), grid, block, a);
     else
-        hipLaunchKernelGGL((route_backward_kernel<R, false>), grid, block, 0, st, a);
+        on.launch((route_backward_kernel<R, false>), grid, block, a);
 }
 
 }  // namespace moe
@@ -675,18 +674,18 @@ extern "C" zc_status zc_route(const void *d_logits, uint32_t logits_type, uint64
     if (!tokens) return ZC_OK;
     const RouteArgs a = {d_logits, d_bias, d_ids, d_weights, logits_stride, (uint32_t)tokens, *cfg};
     const bool bf16 = logits_type == ZC_BF16;
-    hipStream_t st = stream_of(stream);
+    Launches on(stream);
     if (cfg->experts <= 64)
-        launch_route<1>(a, bf16, st);
+        launch_route<1>(a, bf16, on);
     else if (cfg->experts <= 128)
-        launch_route<2>(a, bf16, st);
+        launch_route<2>(a, bf16, on);
     else if (cfg->experts <= 256)
-        launch_route<4>(a, bf16, st);
+        launch_route<4>(a, bf16, on);
     else if (cfg->experts <= 512)
-        launch_route<8>(a, bf16, st);
+        launch_route<8>(a, bf16, on);
     else
-        launch_route<16>(a, bf16, st);
-    return launched();
+        launch_route<16>(a, bf16, on);
+    return on.status();
 }
 
 extern "C" zc_status zc_route_backward(const void *d_logits, uint32_t logits_type, uint64_t tokens,
@@ -705,16 +704,16 @@ extern "C" zc_status zc_route_backward(const void *d_logits, uint32_t logits_typ
                          *cfg};
     const RouteBackArgs a = {f, d_dweights, d_dlogits, dlogits_stride};
     const bool bf16 = logits_type == ZC_BF16;
-    hipStream_t st = stream_of(stream);
+    Launches on(stream);
     if (cfg->experts <= 64)
-        launch_route_backward<1>(a, bf16, st);
+        launch_route_backward<1>(a, bf16, on);
     else if (cfg->experts <= 128)
-        launch_route_backward<2>(a, bf16, st);
+        launch_route_backward<2>(a, bf16, on);
     else if (cfg->experts <= 256)
-        launch_route_backward<4>(a, bf16, st);
+        launch_route_backward<4>(a, bf16, on);
     else if (cfg->experts <= 512)
-        launch_route_backward<8>(a, bf16, st);
+        launch_route_backward<8>(a, bf16, on);
     else
-        launch_route_backward<16>(a, bf16, st);
-    return launched();
+        launch_route_backward<16>(a, bf16, on);
+    return on.status();
 }

@@ -206,12 +206,12 @@ extern "C" zc_status zc_swiglu(const void *d_gate_up, uint64_t rows, uint64_t co
     a.rows = (uint32_t)rows;
     a.cols = (uint32_t)cols;
     a.blocks = (uint32_t)ceil_div(cols, kBlock);
-    hipStream_t st = stream_of(stream);
+    Launches on(stream);
     if (cols % 8 == 0 && wide8(d_gate_up, stride) && (!d_h || wide8(d_h, h_stride)))
-        hipLaunchKernelGGL(swiglu_kernel<true>, dim3(gate_grid(a)), dim3(kGThreads), 0, st, a);
+        on.launch(swiglu_kernel<true>, dim3(gate_grid(a)), dim3(kGThreads), a);
     else
-        hipLaunchKernelGGL(swiglu_kernel<false>, dim3(gate_grid(a)), dim3(kGThreads), 0, st, a);
-    return launched();
+        on.launch(swiglu_kernel<false>, dim3(gate_grid(a)), dim3(kGThreads), a);
+    return on.status();
 }
 
 extern "C" zc_status zc_swiglu_backward(const void *d_kept, const uint8_t *d_kept_scales, uint64_t rows,
@@ -236,10 +236,10 @@ extern "C" zc_status zc_swiglu_backward(const void *d_kept, const uint8_t *d_kep
     a.rows = (uint32_t)rows;
     a.cols = (uint32_t)cols;
     a.blocks = (uint32_t)ceil_div(cols, kBlock);
-    hipStream_t st = stream_of(stream);
+    Launches on(stream);
     if (cols % 8 == 0 && wide8(d_dh, dh_stride) && wide8(d_dgate_up, stride))
-        hipLaunchKernelGGL(swiglu_backward_kernel<true>, dim3(gate_grid(a)), dim3(kGThreads), 0, st, a);
+        on.launch(swiglu_backward_kernel<true>, dim3(gate_grid(a)), dim3(kGThreads), a);
     else
-        hipLaunchKernelGGL(swiglu_backward_kernel<false>, dim3(gate_grid(a)), dim3(kGThreads), 0, st, a);
-    return launched();
+        on.launch(swiglu_backward_kernel<false>, dim3(gate_grid(a)), dim3(kGThreads), a);
+    return on.status();
 }
