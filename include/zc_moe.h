@@ -17,6 +17,15 @@
  *              8-bit input is the checkpoint that the weight gradient reads
  *   activation zc_swiglu, zc_swiglu_backward: the gated activation between two
  *              products, its input kept in 8 bits for the backward pass
+ * and what stands between them in a whole block, from residual to residual:
+ *   norm       zc_norm, zc_norm_backward: the norm of a block's output, its gate
+ *              and scale, the residual sum, and the norm before the next block
+ *   product    zc_matmul, zc_activation_backward, zc_matmul_dgrad,
+ *              zc_matmul_wgrad: BF16 products with bias, activation and residual
+ *              in their epilogue (the router's logits, a shared expert, dense
+ *              projections)
+ *   balance    zc_balance, zc_balance_backward: copies of every expert, the
+ *              balance loss and the z loss of every sequence
  *
  * Conventions: those of zc.h (caller-owned buffers, no allocation, no
  * synchronization, no state between calls, device work is kernel launches
@@ -87,6 +96,23 @@ extern "C" {
 
 #define ZC_SCORE_SOFTMAX 0u
 #define ZC_SCORE_SIGMOID 1u
+
+#define ZC_NORM_NONE 0u
+#define ZC_NORM_RMS 1u
+#define ZC_NORM_LAYER 2u
+
+#define ZC_ACT_NONE 0u
+#define ZC_ACT_RELU 1u
+#define ZC_ACT_SILU 2u
+#define ZC_ACT_GELU 3u
+#define ZC_ACT_GELU_TANH 4u
+#define ZC_ACT_SIGMOID 5u
+
+#define ZC_NORM_MAX_COLS 16384u
+#define ZC_MAX_SEQUENCES 1024u
+/* neither zc_matmul_workspace_bytes nor zc_balance_workspace_bytes is ever more than this */
+#define ZC_MATMUL_WORKSPACE_MAX (64ull << 20)
+#define ZC_BALANCE_WORKSPACE_MAX (64ull << 20)
 
 #define ZC_MAX_EXPERTS 1024u
 #define ZC_MAX_TOP_K 32u
@@ -280,6 +306,162 @@ zc_status zc_swiglu(const void *d_gate_up, uint64_t rows, uint64_t cols, uint64_
 zc_status zc_swiglu_backward(const void *d_kept, const uint8_t *d_kept_scales, uint64_t rows, uint64_t cols,
                              const void *d_dh, uint64_t dh_stride, void *d_dgate_up, uint64_t gu_stride,
                              void *stream);
+
+/* One norm: kind NONE (N(v) = v; nothing else of it is read), RMS: N(v)[c] =
+ * w[c] * v[c] / sqrt(mean(v^2) + eps) + b[c], or LAYER: the same of v - mean(v).
+ * eps is a finite normal number above 0. */
+typedef struct zc_norm_params {
+    const void *d_weight; /* cols values of `type`, or NULL: all 1 */
+    const void *d_bias;   /* cols values of `type`, or NULL: all 0 */
+    uint32_t kind;        /* ZC_NORM_ */
+    uint32_t type;        /* ZC_F32 or ZC_BF16 */
+    float eps;
+} zc_norm_params;
+
+/* What stands between two blocks of a residual stream:
+ *   h = after(z);  r[t, c] = x[t, c] + scale * row_gate[t] * gate[c] * h[t, c];  y = before(r) */
+typedef struct zc_norm_config {
+    zc_norm_params after;  /* the norm of the block's output z */
+    zc_norm_params before; /* the norm of the sum r, before the next block */
+    const void *d_gate;    /* cols values of gate_type, or NULL: all 1 */
+    const float *d_row_gate; /* rows floats, or NULL: all 1 */
+    uint32_t gate_type;    /* ZC_F32 or ZC_BF16 */
+    float scale;           /* finite */
+} zc_norm_config;
+
+/* Norms, gate and residual sum in one pass over the rows; statistics and sums
+ * in 32 bits, each result rounded once (y comes from r before r is rounded).
+ *   d_x     the residual stream, stream_type ZC_BF16 or ZC_F32
+ *   d_z     BF16, or NULL: no block output, r = x (cfg->after, the gates and the
+ *           scale are not read)
+ *   d_r     stream_type, or NULL; may be d_x with the same stride
+ *   d_y     BF16, or NULL
+ *   d_yq, d_yq_scales  the 8-bit e4m3 blocks that zc_fp8_quantize makes of y: the
+ *           input of the next product; or NULL
+ * cols is at most ZC_NORM_MAX_COLS.  A finite row has finite statistics also
+ * where its squares leave the range of a float.  A row that holds NaN or an infinity:
+ * what the formula gives, NaN where it has no value. */
+zc_status zc_norm(const void *d_x, uint32_t stream_type, uint64_t rows, uint64_t cols, uint64_t x_stride,
+                  const void *d_z, uint64_t z_stride, const zc_norm_config *cfg, void *d_r, uint64_t r_stride,
+                  void *d_y, uint64_t y_stride, void *d_yq, uint8_t *d_yq_scales, void *stream);
+
+/* Gradients of the parameters, sums over the rows in 32 bits; any may be NULL.
+ * Those of a norm of kind NONE, or without d_z those of the whole first half, are zeros. */
+typedef struct zc_norm_grads {
+    float *d_weight_after, *d_bias_after, *d_gate; /* cols floats each */
+    float *d_weight_before, *d_bias_before;        /* cols floats each */
+    float *d_row_gate;                             /* rows floats */
+} zc_norm_grads;
+
+/* Workspace of zc_norm_backward: the parts of the sums over the rows (a
+ * multiple of 256; 0 for invalid sizes). */
+uint64_t zc_norm_backward_workspace_bytes(uint64_t rows, uint64_t cols);
+
+/* Gradients of zc_norm, evaluated at the stored sum d_r (stream_type).
+ *   d_dr   gradient that arrives at r beside y's, stream_type, or NULL: 0
+ *   d_dy   BF16, or NULL: 0
+ *   d_dx   stream_type, or NULL: the whole gradient of r, which is that of x; may
+ *          be d_dr with the same stride
+ *   d_dz   BF16, or NULL
+ * d_workspace is needed where a parameter's gradient over the rows is asked for. */
+zc_status zc_norm_backward(const void *d_r, uint32_t stream_type, uint64_t rows, uint64_t cols, uint64_t r_stride,
+                           const void *d_z, uint64_t z_stride, const zc_norm_config *cfg, const void *d_dr,
+                           uint64_t dr_stride, const void *d_dy, uint64_t dy_stride, void *d_dx, uint64_t dx_stride,
+                           void *d_dz, uint64_t dz_stride, const zc_norm_grads *grads, void *d_workspace,
+                           uint64_t workspace_bytes, void *stream);
+
+/* What zc_matmul does with a sum v before it leaves:
+ *   pre = v + bias;  out = residual + scale * activation(pre)
+ * activation: NONE, RELU, SILU v * sigmoid(v), GELU v * Phi(v) (the normal
+ * distribution), GELU_TANH v * (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2,
+ * SIGMOID. */
+typedef struct zc_epilogue {
+    const void *d_bias;       /* cols values of bias_type, or NULL: 0 */
+    const void *d_residual;   /* rows of residual_type, or NULL: 0; may be the output, with its type and stride */
+    void *d_pre;              /* BF16, or NULL: pre, kept for zc_activation_backward */
+    uint64_t residual_stride;
+    uint64_t pre_stride;
+    uint32_t bias_type;       /* ZC_F32 or ZC_BF16 */
+    uint32_t residual_type;   /* ZC_F32 or ZC_BF16 */
+    uint32_t activation;      /* ZC_ACT_ */
+    float scale;              /* finite */
+} zc_epilogue;
+
+/* Workspace with which a product of rows x cols results over `contraction`
+ * values may be split (0: it is not; at most ZC_MATMUL_WORKSPACE_MAX): (m, n, k) for zc_matmul, (m,
+ * k, n) for zc_matmul_dgrad, (n, k, m) for zc_matmul_wgrad. */
+uint64_t zc_matmul_workspace_bytes(uint64_t rows, uint64_t cols, uint64_t contraction);
+
+/* d_out[r, c] = epilogue(sum over k of A[r, k] * W[c, k]), A (m x k) and W (n x
+ * k) BF16; products are exact, sums in 32 bits, d_out (out_type ZC_BF16 or
+ * ZC_F32) and pre rounded once.  epilogue NULL: the sum itself.  k = 0: a sum of nothing
+ * is 0, and the epilogue is applied.  A workspace smaller than
+ * zc_matmul_workspace_bytes is not used; NULL: no split.  n and k are at most 2^28. */
+zc_status zc_matmul(const void *d_a, uint64_t m, uint64_t a_stride, const void *d_w, uint64_t n, uint64_t k,
+                    uint64_t w_stride, const zc_epilogue *epilogue, void *d_out, uint32_t out_type,
+                    uint64_t out_stride, void *d_workspace, uint64_t workspace_bytes, void *stream);
+
+/* Workspace of zc_activation_backward for d_dbias (a multiple of 256; 0 for invalid sizes). */
+uint64_t zc_activation_backward_workspace_bytes(uint64_t rows, uint64_t cols);
+
+/* From the gradient of zc_matmul's output (dout_type ZC_BF16 or ZC_F32) to that
+ * of its pre-activation: dpre = scale * dout * activation'(pre) at the kept pre
+ * (BF16; not read for NONE), rounded to BF16; d_dbias[c] = sum over the rows of
+ * dpre before that rounding, in 32 bits.  The slope of RELU at 0 is 0.  Either
+ * result may be NULL; d_dpre may be d_dout where that is BF16, or d_pre, with the
+ * same stride.  d_workspace is needed for d_dbias. */
+zc_status zc_activation_backward(const void *d_dout, uint32_t dout_type, uint64_t rows, uint64_t cols,
+                                 uint64_t dout_stride, const void *d_pre, uint64_t pre_stride, uint32_t activation,
+                                 float scale, void *d_dpre, uint64_t dpre_stride, float *d_dbias, void *d_workspace,
+                                 uint64_t workspace_bytes, void *stream);
+
+/* Gradient of zc_matmul's A: d_dx[r, j] = add[r, j] + sum over c of dpre[r, c] *
+ * W[c, j] (m x k; dpre m x n BF16).  d_add: add_type, NULL: 0; may be d_dx with
+ * its type and stride.  Sums, results and workspace as in zc_matmul. */
+zc_status zc_matmul_dgrad(const void *d_dpre, uint64_t m, uint64_t n, uint64_t dpre_stride, const void *d_w,
+                          uint64_t k, uint64_t w_stride, const void *d_add, uint32_t add_type, uint64_t add_stride,
+                          void *d_dx, uint32_t dx_type, uint64_t dx_stride, void *d_workspace,
+                          uint64_t workspace_bytes, void *stream);
+
+/* Gradient of zc_matmul's W: d_dw[c, j] = add[c, j] + sum over r of dpre[r, c] *
+ * A[r, j] (n x k).  d_add, for gradients that add up over calls, as above. */
+zc_status zc_matmul_wgrad(const void *d_dpre, uint64_t m, uint64_t n, uint64_t dpre_stride, const void *d_a,
+                          uint64_t k, uint64_t a_stride, const void *d_add, uint32_t add_type, uint64_t add_stride,
+                          void *d_dw, uint32_t dw_type, uint64_t dw_stride, void *d_workspace,
+                          uint64_t workspace_bytes, void *stream);
+
+/* Workspace of zc_balance (a multiple of 256; 0 for invalid sizes). */
+uint64_t zc_balance_workspace_bytes(uint64_t tokens, uint32_t experts, uint32_t sequences);
+
+/* Copies of every expert, balance loss and z loss of every sequence.  Of cfg,
+ * only experts, top_k and score are read.  Sequence s: the tokens [d_offsets[s],
+ * d_offsets[s + 1]) (sequences + 1 int32, ascending; values are clamped to
+ * 0..tokens and to ascending order; NULL with sequences 1: all tokens) whose
+ * d_mask is not 0 (tokens bytes; NULL: all).  With p = the softmax of a token's
+ * logits, or sigmoid / (sum of its sigmoids + 1e-20):
+ *   d_used[s]       its tokens, n
+ *   d_counts[s, e]  its copies with d_ids = e (tokens x top_k int32; an id outside
+ *                   0..experts-1 counts nowhere)
+ *   d_loss[s]       experts / (top_k n^2) * sum over e of counts[s, e] * sum over its tokens of p[t, e]
+ *   d_zloss[s]      1 / n * sum over its tokens of (log of the sum over e of exp(logits[t, e]))^2
+ * Without tokens the losses are 0.  The losses may be NULL, and then d_logits
+ * too.  A token whose logits are all -inf has p = 0 and no part in the z loss.
+ * sequences is at most ZC_MAX_SEQUENCES; with tokens = 0 everything is written (zeros). */
+zc_status zc_balance(const void *d_logits, uint32_t logits_type, uint64_t tokens, uint64_t logits_stride,
+                     const zc_route_config *cfg, const int32_t *d_ids, const uint8_t *d_mask, uint32_t sequences,
+                     const int32_t *d_offsets, void *d_workspace, uint64_t workspace_bytes, int32_t *d_counts,
+                     int32_t *d_used, float *d_loss, float *d_zloss, void *stream);
+
+/* Gradient of the logits from the gradients of the losses (sequences floats
+ * each; NULL: 0), for the counts and used that zc_balance wrote (the counts have no
+ * gradient): d_dlogits[t, :] = add[t, :] + that of token t's sequence; a token of no sequence, or
+ * masked, has add alone.  d_add: logits_type, NULL: 0 (the gradient of
+ * zc_route_backward); may be d_dlogits with the same stride. */
+zc_status zc_balance_backward(const void *d_logits, uint32_t logits_type, uint64_t tokens, uint64_t logits_stride,
+                              const zc_route_config *cfg, const uint8_t *d_mask, uint32_t sequences,
+                              const int32_t *d_offsets, const int32_t *d_counts, const int32_t *d_used,
+                              const float *d_dloss, const float *d_dzloss, const void *d_add, uint64_t add_stride,
+                              void *d_dlogits, uint64_t dlogits_stride, void *stream);
 
 #ifdef __cplusplus
 }

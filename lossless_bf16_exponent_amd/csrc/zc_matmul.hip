@@ -6,6 +6,7 @@
 // every lane's 32 values, in the 32-bit sum, at no cost of their own.
 #include <type_traits>
 
+#include "zc_lds.h"
 #include "zc_moe_device.h"
 
 namespace zc {
@@ -68,25 +69,7 @@ __device__ __forceinline__ f32v16 mfma(const i32v8 &a, const i32v8 &b, const f32
 // tiles of four waves, loads straight into LDS
 // ---------------------------------------------------------------------------
 
-typedef __attribute__((address_space(3))) void lds_void;
-typedef uint32_t u32v4a4 __attribute__((ext_vector_type(4), aligned(4)));
 typedef uint32_t u32v2a2 __attribute__((ext_vector_type(2), aligned(2)));
-
-// A wave's loads straight into LDS (16 or 4 bytes a lane, the lanes' results one
-// after another from the wave-uniform address in M0), from a uniform base and a
-// 32-bit offset a lane.  Inline assembly, so that the compiler adds no waits of
-// its own: the kernel counts them.  M0 is an operand, which the compiler sets, so
-// that it knows of every change of it.
-__device__ __forceinline__ void lds_load16(const uint8_t *base, uint32_t offset, uint32_t lds) {
-    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(offset), "s"(base), "{m0}"(lds) : "memory");
-}
-__device__ __forceinline__ void lds_load4(const uint8_t *base, uint32_t offset, uint32_t lds) {
-    asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(offset), "s"(base), "{m0}"(lds) : "memory");
-}
-template <int VM>
-__device__ __forceinline__ void wait_and_meet() {
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(VM) : "memory");
-}
 
 // A stage is one block of 128 along the contraction: 128 bytes of every row, a
 // whole cache line each.  (Stages of 64 bytes, four deep, asked the L2 for twice

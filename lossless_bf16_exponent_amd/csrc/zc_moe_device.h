@@ -20,6 +20,7 @@ constexpr uint32_t kBlock = ZC_FP8_BLOCK;
 typedef uint32_t u32v4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32v2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32v4a2 __attribute__((ext_vector_type(4), aligned(2)));  // 16 bytes at any BF16 value
+typedef uint32_t u32v4a4 __attribute__((ext_vector_type(4), aligned(4)));  // 16 bytes at any float
 
 // ---------------------------------------------------------------------------
 // host side
@@ -165,6 +166,74 @@ __device__ __forceinline__ void store_values(uint16_t *p, const u32v4 &w, uint32
 }
 
 // ---------------------------------------------------------------------------
+// eight values of a row
+// ---------------------------------------------------------------------------
+
+// As they are stored: four registers of BF16 pairs, or eight floats.  Rows start at any
+// value; of the last lane's values n exist, and the others read as 0.
+template <bool F32>
+struct Eight {
+    u32v4 w[F32 ? 2 : 1];
+    __device__ __forceinline__ float operator[](uint32_t i) const {
+        if (F32) return __uint_as_float(w[i / 4 % (F32 ? 2 : 1)][i & 3]);
+        return (i & 1) ? bf_hi(w[0][i / 2]) : bf_lo(w[0][i / 2]);
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (uint32_t i = 0; i < (F32 ? 2 : 1); ++i) w[i] = u32v4{0u, 0u, 0u, 0u};
+    }
+    // once: nothing reads it again
+    __device__ __forceinline__ void load(const void *base, uint64_t at, uint32_t n, bool once) {
+        if (F32) {
+            const float *p = static_cast<const float *>(base) + at;
+            if (n >= 8) {
+                const u32v4a4 *q = reinterpret_cast<const u32v4a4 *>(p);
+                w[0] = once ? __builtin_nontemporal_load(q) : *q;
+                w[F32 ? 1 : 0] = once ? __builtin_nontemporal_load(q + 1) : q[1];
+            } else {
+                clear();
+#pragma unroll
+                for (uint32_t i = 0; i < 7; ++i)
+                    if (i < n) w[i / 4 % (F32 ? 2 : 1)][i & 3] = __float_as_uint(p[i]);
+            }
+        } else {
+            const uint16_t *p = static_cast<const uint16_t *>(base) + at;
+            if (n >= 8) {
+                const u32v4a2 *q = reinterpret_cast<const u32v4a2 *>(p);
+                w[0] = once ? __builtin_nontemporal_load(q) : *q;
+            } else {
+                clear();
+#pragma unroll
+                for (uint32_t i = 0; i < 7; ++i)
+                    if (i < n) w[0][i / 2] |= (uint32_t)p[i] << (16 * (i & 1));
+            }
+        }
+    }
+};
+
+__device__ __forceinline__ u32v4 pack8(const float (&v)[8]) {
+    u32v4 w;
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i) w[i] = bf_pack(v[2 * i], v[2 * i + 1]);
+    return w;
+}
+__device__ __forceinline__ void store_floats(float *p, uint32_t n, const float (&v)[8]) {
+    if (n >= 8) {
+        u32v4 a, b;
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i) {
+            a[i] = __float_as_uint(v[i]);
+            b[i] = __float_as_uint(v[4 + i]);
+        }
+        *reinterpret_cast<u32v4a4 *>(p) = a;
+        *reinterpret_cast<u32v4a4 *>(p + 4) = b;
+    } else {
+#pragma unroll
+        for (uint32_t i = 0; i < 7; ++i)
+            if (i < n) p[i] = v[i];
+    }
+}
+// ---------------------------------------------------------------------------
 // waves
 // ---------------------------------------------------------------------------
 
@@ -182,6 +251,25 @@ __device__ __forceinline__ float group_sum(float v) {
 #pragma unroll
     for (int s = 1; s < WIDTH; s <<= 1) v += __shfl_xor(v, s);
     return v;
+}
+
+constexpr uint32_t kKeepLanes = 16;
+
+// The 8 values' 8-bit form under the block's scale (16 lanes a block); lane 0
+// writes the scale.
+__device__ __forceinline__ void keep8(const u32v4 &w, uint8_t *q, uint8_t *s, uint32_t sub) {
+    uint32_t m = 0;
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i) m = finite_max(m, w[i]);
+    m = group_max<kKeepLanes>(m);
+    typedef Fp8<ZC_FP8_E4M3> F;
+    const uint32_t byte = scale_byte(m, F::kTop);
+    const float inv = scale_inverse(byte);
+    uint2 r;
+    r.x = F::pack4(bf_lo(w[0]) * inv, bf_hi(w[0]) * inv, bf_lo(w[1]) * inv, bf_hi(w[1]) * inv);
+    r.y = F::pack4(bf_lo(w[2]) * inv, bf_hi(w[2]) * inv, bf_lo(w[3]) * inv, bf_hi(w[3]) * inv);
+    *reinterpret_cast<uint2 *>(q) = r;
+    if (sub == 0) *s = (uint8_t)byte;
 }
 
 // Sum over the wave, in an order of its own that does not change.

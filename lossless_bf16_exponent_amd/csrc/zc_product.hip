@@ -1,0 +1,843 @@
+// BF16 products with an epilogue, and the gradients of their operands, MI355X / gfx950:
+//   forward  out[r, c] = sum_k A[r, k] W[c, k]      both operands along the contraction
+//   dgrad    dx[r, j]  = sum_c dpre[r, c] W[c, j]   the right operand across it
+//   wgrad    dw[c, j]  = sum_r dpre[r, c] A[r, j]   both across it
+// An operand that lies across the contraction comes out of LDS through the
+// transposing reads of gfx950, so that nothing is transposed in memory.
+#include <math.h>
+
+#include <type_traits>
+
+#include "zc_lds.h"
+#include "zc_moe_device.h"
+
+namespace zc {
+namespace moe {
+
+typedef float f32v16 __attribute__((ext_vector_type(16)));
+typedef float f32v4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16v8 __attribute__((ext_vector_type(8)));
+typedef short s16v4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16v4 lds_s16v4;
+
+struct Epilogue {
+    const void *bias, *res;
+    uint16_t *pre;
+    void *out;
+    uint64_t res_stride, pre_stride, out_stride;
+    uint32_t bias_f32, res_f32, out_f32, act;
+    float scale;
+};
+
+struct ProductArgs {
+    const uint16_t *a, *b;
+    uint64_t lda, ldb;  // elements
+    uint32_t m, n, k;   // results' rows and columns, contraction
+    uint32_t blocks;    // blocks of 64 along the contraction
+    uint32_t direct;    // of which the first so many may be loaded whole
+    float *parts;       // a split contraction's sums, gridDim.y of them; or NULL
+    Epilogue e;
+};
+
+// ---------------------------------------------------------------------------
+// activations
+// ---------------------------------------------------------------------------
+
+// sigmoid(v) = s * t.  From -20 down it is e^v to 32 bits, taken as the square of
+// e^(v / 2): a product with a large value then keeps its digits where e^v has none left.
+struct Parts {
+    float s, t;
+};
+__device__ __forceinline__ Parts sigmoid_parts(float v) {
+    if (v < -20.0f) {
+        const float h = expf(0.5f * v);
+        return {h, h};
+    }
+    return {1.0f / (1.0f + expf(-v)), 1.0f};
+}
+constexpr float kRootHalf = 0.70710678f, kRootPi = 0.79788456f, kCubic = 0.044715f;  // sqrt(1 / 2), sqrt(2 / pi)
+
+__device__ __forceinline__ float activation(float v, uint32_t act) {
+    switch (act) {
+        case ZC_ACT_RELU: return v > 0.0f ? v : v != v ? v : 0.0f;
+        case ZC_ACT_SILU: {
+            const Parts p = sigmoid_parts(v);
+            return v * p.s * p.t;
+        }
+        case ZC_ACT_GELU: {
+            // the tail from erfc, which keeps its digits
+            const float x = v * kRootHalf;
+            return v * (0.5f * erfcf(-x));
+        }
+        case ZC_ACT_GELU_TANH: {
+            // (1 + tanh(u)) / 2 = sigmoid(2 u)
+            const Parts p = sigmoid_parts(2.0f * kRootPi * (v + kCubic * v * v * v));
+            return v * p.s * p.t;
+        }
+        case ZC_ACT_SIGMOID: {
+            const Parts p = sigmoid_parts(v);
+            return p.s * p.t;
+        }
+        default: return v;
+    }
+}
+
+// d times the slope at v.
+__device__ __forceinline__ float sloped(float d, float v, uint32_t act) {
+    switch (act) {
+        case ZC_ACT_RELU: return v > 0.0f ? d : v != v ? v : 0.0f;
+        case ZC_ACT_SILU: {
+            const Parts p = sigmoid_parts(v);
+            const float rest = v < -20.0f ? 1.0f : expf(-v) * p.s;
+            return d * (1.0f + v * rest) * p.s * p.t;
+        }
+        case ZC_ACT_GELU: {
+            // Phi(v) + v phi(v), the density as a square for the same reason as above
+            const float half = expf(-0.25f * v * v);
+            return d * (0.5f * erfcf(-v * kRootHalf)) + (d * v * 0.39894228f * half) * half;
+        }
+        case ZC_ACT_GELU_TANH: {
+            // from 30 on the slope is 1 or 0 in 32 bits
+            const float x = v != v ? v : fminf(fmaxf(v, -30.0f), 30.0f), w = 2.0f * kRootPi * (x + kCubic * x * x * x);
+            const Parts p = sigmoid_parts(w);
+            const float rest = w < -20.0f ? 1.0f : expf(-w) * p.s;
+            return d * (1.0f + x * rest * (2.0f * kRootPi * (1.0f + 3.0f * kCubic * x * x))) * p.s * p.t;
+        }
+        case ZC_ACT_SIGMOID: {
+            const float x = v != v ? v : -fabsf(v);
+            const Parts p = sigmoid_parts(x);
+            return d * p.s * p.t * (1.0f / (1.0f + expf(x)));
+        }
+        default: return d;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// epilogue
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ void load8(const void *p, uint32_t f32, uint64_t at, uint32_t n, float (&v)[8]) {
+    if (f32) {
+        Eight<true> w;
+        w.load(p, at, n, false);
+#pragma unroll
+        for (uint32_t i = 0; i < 8; ++i) v[i] = w[i];
+    } else {
+        Eight<false> w;
+        w.load(p, at, n, false);
+#pragma unroll
+        for (uint32_t i = 0; i < 8; ++i) v[i] = w[i];
+    }
+}
+// The sums of columns c .. c + n - 1 of row r become results.
+__device__ __forceinline__ void finish8(const Epilogue &e, uint64_t r, uint32_t c, uint32_t n, float (&v)[8]) {
+    float w[8];
+    if (e.bias) {
+        load8(e.bias, e.bias_f32, c, n, w);
+#pragma unroll
+        for (uint32_t i = 0; i < 8; ++i) v[i] += w[i];
+    }
+    if (e.pre) store_values<false>(e.pre + r * e.pre_stride + c, pack8(v), n);
+    if (e.act != ZC_ACT_NONE)
+#pragma unroll
+        for (uint32_t i = 0; i < 8; ++i) v[i] = activation(v[i], e.act);
+    if (e.res) {
+        load8(e.res, e.res_f32, r * e.res_stride + c, n, w);
+#pragma unroll
+        for (uint32_t i = 0; i < 8; ++i) v[i] = fmaf(e.scale, v[i], w[i]);
+    } else {
+#pragma unroll
+        for (uint32_t i = 0; i < 8; ++i) v[i] *= e.scale;
+    }
+    if (e.out_f32)
+        store_floats(static_cast<float *>(e.out) + r * e.out_stride + c, n, v);
+    else
+        store_values<false>(static_cast<uint16_t *>(e.out) + r * e.out_stride + c, pack8(v), n);
+}
+
+// ---------------------------------------------------------------------------
+// tiles
+// ---------------------------------------------------------------------------
+
+constexpr uint32_t kPThreads = 256;
+constexpr uint32_t kPBlock = 64;       // contraction of a stage
+constexpr uint32_t kPBytes = 2 * kPBlock;  // of a row or column in a stage
+
+// One operand of a tile of B rows (or columns) of the results.  A stage holds B x
+// 64 values in places of 16 bytes, a wave's pieces of 64 places one after another:
+//   along   row r of the tile is 128 bytes; chunk c (8 values of the contraction)
+//           sits at place c ^ (r / 2 mod 8), so that sixteen lanes that read the
+//           same chunk of sixteen rows meet sixteen different columns of banks
+//   across  value k of the contraction is 2 B bytes; chunk c (8 results) sits at
+//           place c ^ 4 (k mod 4): a transposing read takes 64 bytes of each of
+//           four k, which then lie in four different quarters of the banks
+template <uint32_t B, bool ACROSS>
+struct Operand {
+    static constexpr uint32_t kLoads = B / 32;         // pieces of a wave
+    static constexpr uint32_t kTiles = B / 64;         // 32 x 32 tiles of a wave
+    static constexpr uint32_t kReads = ACROSS ? 4 : 2;  // of a tile and half stage
+    static constexpr uint32_t kRow = B / 8;            // across: chunks of a k
+
+    const uint16_t *p;
+    uint64_t ld;
+    uint32_t first, last, k;  // the tile's first row, the last one there is; contraction
+    uint32_t at[ACROSS ? kTiles : 1];
+
+    // place `lane` of the wave's piece i: row (or k) and chunk
+    __device__ __forceinline__ static uint32_t line(uint32_t wave, uint32_t i) {
+        return ACROSS ? (wave * kLoads + i) * (kLanes / kRow) + lane_id() / kRow : wave * (B / 4) + 8 * i + lane_id() / 8;
+    }
+    __device__ __forceinline__ static uint32_t chunk(uint32_t line) {
+        return ACROSS ? (lane_id() % kRow) ^ (4 * (line & 3)) : (lane_id() & 7) ^ (line / 2 & 7);
+    }
+
+    // byte offset of a lane's 16 bytes of a whole block from the block's start, rows past the last repeating it
+    __device__ __forceinline__ uint32_t offset(uint32_t wave, uint32_t i) const {
+        const uint32_t l = line(wave, i), c = chunk(l), room = last - first;
+        return ACROSS ? l * (uint32_t)ld * 2 + min(16 * c, room / 8 * 16) : min(l, room) * (uint32_t)ld * 2 + 16 * c;
+    }
+    __device__ __forceinline__ const uint8_t *block(uint32_t kb) const {
+        const uint64_t e = ACROSS ? (uint64_t)kb * kPBlock * ld + first : (uint64_t)first * ld + (uint64_t)kb * kPBlock;
+        return reinterpret_cast<const uint8_t *>(p + e);
+    }
+    __device__ __forceinline__ uint64_t step() const { return ACROSS ? (uint64_t)kPBlock * ld * 2 : kPBytes; }
+
+    // any block, any alignment: what lies past the contraction reads as 0
+    __device__ __forceinline__ u32v4 load(uint32_t kb, uint32_t wave, uint32_t i) const {
+        const uint32_t l = line(wave, i), c = chunk(l);
+        const uint32_t kk = kb * kPBlock + (ACROSS ? l : 8 * c), r = first + (ACROSS ? 8 * c : l);
+        Eight<false> w;
+        w.clear();
+        if (kk < k && r <= last) w.load(p, ACROSS ? kk * ld + r : r * ld + kk, ACROSS ? last + 1 - r : k - kk, false);
+        return w.w[0];
+    }
+
+    // fragments: lane l holds row l mod 32 of a 32 x 32 tile and the contraction's 8 values 8 (l / 32) .. of 16
+    __device__ __forceinline__ void place(uint32_t base, uint32_t within) {
+        const uint32_t lane = lane_id();
+        if (ACROSS) {
+            const uint32_t j = lane % 16, k0 = 8 * (lane / 32) + j / 4;
+#pragma unroll
+            for (uint32_t i = 0; i < kTiles; ++i) {
+                const uint32_t c = (within + 32 * i) / 8 + 2 * (lane / 16 & 1) + j % 4 / 2;
+                at[ACROSS ? i : 0] = base + k0 * (2 * B) + 16 * (c ^ (4 * (k0 & 3))) + 8 * (j & 1);
+            }
+        } else {
+            at[0] = base + (within + lane % 32) * kPBytes;
+        }
+    }
+    // read q of the tile i's fragment: along, the 16 values q of the half; across, 4 values of the contraction
+    __device__ __forceinline__ void read(const uint8_t *stage, uint32_t half, uint32_t i, uint32_t q, bf16v8 (&f)[2]) const {
+        if constexpr (ACROSS) {
+            const uint32_t k = 32 * half + 16 * (q / 2) + 4 * (q & 1);
+            const s16v4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16v4 *)(stage + at[i] + k * (2 * B)));
+            const auto bits = __builtin_bit_cast(uint2, v);
+            u32v4 w = __builtin_bit_cast(u32v4, f[q / 2]);
+            w[2 * (q & 1)] = bits.x;
+            w[2 * (q & 1) + 1] = bits.y;
+            f[q / 2] = __builtin_bit_cast(bf16v8, w);
+        } else {
+            const uint32_t c = (4 * half + 2 * q + lane_id() / 32) ^ (lane_id() % 32 / 2 & 7u);
+            f[q] = *reinterpret_cast<const bf16v8 *>(stage + at[0] + 32 * i * kPBytes + 16 * c);
+        }
+    }
+};
+
+// BM x BN tile of four waves (2 x 2).  DIRECT: whole blocks go from memory straight
+// into LDS, STAGES of them under way, in the order of the 8-bit products' tiles: the
+// fragments of half a block are in registers while the other half's come out
+// of LDS, and one barrier in the middle of a block frees its place and hands over
+// the next.  The contraction's ragged end, and all of it without DIRECT (operands at
+// any element, rows far apart), goes through registers.
+template <uint32_t BM, uint32_t BN, uint32_t STAGES, bool XA, bool XB, bool DIRECT>
+__global__ __launch_bounds__(kPThreads, STAGES * (BM + BN) * kPBytes > 80 * 1024 ? 1 : 2) void product_kernel(ProductArgs p) {
+    typedef Operand<BM, XA> OA;
+    typedef Operand<BN, XB> OB;
+    constexpr uint32_t MT = OA::kTiles, NT = OB::kTiles, LA = OA::kLoads, LB = OB::kLoads, LOADS = LA + LB;
+    constexpr uint32_t kStage = (BM + BN) * kPBytes;
+    constexpr uint32_t kRowBytes = BN / 2 * 4 + 16;  // of a wave's results on their way out
+    constexpr uint32_t kRoom = STAGES * kStage > 4 * 32 * kRowBytes ? STAGES * kStage : 4 * 32 * kRowBytes;
+    __shared__ alignas(1024) uint8_t sh[kRoom];
+    const uint32_t lane = lane_id(), wave = (uint32_t)__builtin_amdgcn_readfirstlane(threadIdx.x / kLanes);
+
+    // Consecutive workgroups go to the eight XCDs in turn: an XCD gets one run of
+    // tiles, in bands of eight rows of tiles, column by column, so that its CUs
+    // share rows of both operands in its L2.
+    const uint32_t mtiles = (p.m + BM - 1) / BM, ntiles = (p.n + BN - 1) / BN, total = mtiles * ntiles;
+    const uint32_t xcd = blockIdx.x % 8, local = blockIdx.x / 8, per = total / 8, rest = total % 8;
+    if (local >= per + (xcd < rest)) return;
+    const uint32_t id = xcd * per + min(xcd, rest) + local;
+    const uint32_t band = id / (8 * ntiles), in_band = id % (8 * ntiles), band_rows = min(8u, mtiles - 8 * band);
+    const uint32_t m0 = (8 * band + in_band % band_rows) * BM, n0 = in_band / band_rows * BN;
+    const uint32_t kb0 = (uint32_t)((uint64_t)p.blocks * blockIdx.y / gridDim.y);
+    const uint32_t kb1 = (uint32_t)((uint64_t)p.blocks * (blockIdx.y + 1) / gridDim.y);
+
+    OA oa = {p.a, p.lda, m0, p.m - 1, p.k};
+    OB ob = {p.b, p.ldb, n0, p.n - 1, p.k};
+    const uint32_t wm = (wave & 1) * (BM / 2), wn = (wave >> 1) * (BN / 2);
+    oa.place(0, wm);
+    ob.place(BM * kPBytes, wn);
+
+    f32v16 acc[MT][NT];
+#pragma unroll
+    for (uint32_t i = 0; i < MT; ++i)
+#pragma unroll
+        for (uint32_t j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+
+    bf16v8 fa[2][MT][2], fb[2][NT][2];  // [half of the block]
+    // the q-th of a half's reads
+    constexpr uint32_t kReads = MT * OA::kReads + NT * OB::kReads;
+    const auto read_piece = [&](uint32_t at, uint32_t half, uint32_t q) {
+        if (q < MT * OA::kReads)
+            oa.read(sh + at, half, q / OA::kReads, q % OA::kReads, fa[half][q / OA::kReads % MT]);
+        else
+            ob.read(sh + at, half, (q - MT * OA::kReads) / OB::kReads % NT, (q - MT * OA::kReads) % OB::kReads,
+                    fb[half][(q - MT * OA::kReads) / OB::kReads % NT]);
+    };
+    // B in the place of the left matrix: a lane then holds four consecutive columns of one row
+    const auto multiply = [&](uint32_t half, uint32_t i, uint32_t j) {
+#pragma unroll
+        for (uint32_t h = 0; h < 2; ++h)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[half][j][h], fa[half][i][h], acc[i][j], 0, 0, 0);
+    };
+
+    const uint32_t whole = DIRECT ? min(kb1, p.direct) : kb0;
+    if constexpr (DIRECT) if (kb0 < whole) {
+        const uint32_t blocks = whole - kb0;
+        const uint8_t *ga = oa.block(kb0), *gb = ob.block(kb0);
+        uint32_t offa[LA], offb[LB];
+#pragma unroll
+        for (uint32_t i = 0; i < LA; ++i) offa[i] = oa.offset(wave, i);
+#pragma unroll
+        for (uint32_t i = 0; i < LB; ++i) offb[i] = ob.offset(wave, i);
+        const uint32_t lds0 = (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void *)&sh[0]);
+        const uint32_t ldsa = lds0 + wave * LA * 1024, ldsb = lds0 + BM * kPBytes + wave * LB * 1024;
+        const auto load_piece = [&](uint32_t t, uint32_t at, uint32_t i) {  // the wave's i-th load of block kb0 + t
+            if (i < LA)
+                lds_load16(ga + t * oa.step(), offa[i % LA], ldsa + at + i * 1024);
+            else
+                lds_load16(gb + t * ob.step(), offb[(i - LA) % LB], ldsb + at + (i - LA) * 1024);
+        };
+#pragma unroll
+        for (uint32_t t = 0; t < STAGES; ++t)
+            if (t < blocks)
+#pragma unroll
+                for (uint32_t i = 0; i < LOADS; ++i) load_piece(t, t * kStage, i);
+        if (blocks >= STAGES)
+            wait_and_meet<(int)((STAGES - 1) * LOADS)>();
+        else
+            wait_and_meet<0>();
+#pragma unroll
+        for (uint32_t q = 0; q < kReads; ++q) read_piece(0, 0, q);
+
+        uint32_t at0 = 0, at1 = STAGES > 1 ? kStage : 0;  // where blocks t and t + 1 are
+        const auto step = [&](uint32_t t, auto more) {
+            constexpr bool MORE = decltype(more)::value;  // there is a block to load into this one's place
+#pragma unroll
+            for (uint32_t half = 0; half < 2; ++half) {
+                // block t + 1 has landed, and every wave holds the rest of block t
+                if (half == 1) wait_and_meet<MORE ? (int)((STAGES - 2) * LOADS) : 0>();
+#pragma unroll
+                for (uint32_t i = 0; i < MT; ++i)
+#pragma unroll
+                    for (uint32_t j = 0; j < NT; ++j) {
+                        multiply(half, i, j);
+                        constexpr uint32_t kSlots = MT * NT;
+                        const uint32_t slot = i * NT + j;
+                        if (MORE && half == 1)
+#pragma unroll
+                            for (uint32_t q = slot * LOADS / kSlots; q < (slot + 1) * LOADS / kSlots; ++q)
+                                load_piece(t + STAGES, at0, q);
+#pragma unroll
+                        for (uint32_t q = slot * kReads / kSlots; q < (slot + 1) * kReads / kSlots; ++q)
+                            read_piece(half ? at1 : at0, half ^ 1, q);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+            }
+            at0 = at1;
+            at1 = at1 == (STAGES - 1) * kStage ? 0 : at1 + kStage;
+        };
+        uint32_t t = 0;
+        for (; t + STAGES < blocks; ++t) step(t, std::true_type{});
+        for (; t < blocks; ++t) step(t, std::false_type{});
+        wait_and_meet<0>();
+    }
+    for (uint32_t kb = max(whole, kb0); kb < kb1; ++kb) {
+        u32v4 w[LOADS];
+#pragma unroll
+        for (uint32_t i = 0; i < LOADS; ++i) w[i] = i < LA ? oa.load(kb, wave, i) : ob.load(kb, wave, i - LA);
+        __syncthreads();  // every wave is done with the block before
+#pragma unroll
+        for (uint32_t i = 0; i < LOADS; ++i) {
+            const uint32_t at = i < LA ? (wave * LA + i) * 1024 : BM * kPBytes + (wave * LB + i - LA) * 1024;
+            *reinterpret_cast<u32v4 *>(sh + at + 16 * lane) = w[i];
+        }
+        __syncthreads();
+#pragma unroll
+        for (uint32_t half = 0; half < 2; ++half) {
+#pragma unroll
+            for (uint32_t q = 0; q < kReads; ++q) read_piece(0, half, q);
+#pragma unroll
+            for (uint32_t i = 0; i < MT; ++i)
+#pragma unroll
+                for (uint32_t j = 0; j < NT; ++j) multiply(half, i, j);
+        }
+    }
+
+    // Results through LDS, 32 rows of a wave at a time, so that a row's BN / 2 columns
+    // leave as whole lines, eight a lane.
+    __syncthreads();
+    Epilogue e = p.e;
+    if (p.parts) {
+        e = {};
+        e.out = p.parts + (uint64_t)blockIdx.y * p.m * p.n;
+        e.out_stride = p.n;
+        e.out_f32 = 1;
+        e.scale = 1.0f;
+    }
+    uint8_t *mine = sh + wave * 32 * kRowBytes;
+#pragma unroll
+    for (uint32_t i = 0; i < MT; ++i) {
+#pragma unroll
+        for (uint32_t j = 0; j < NT; ++j)
+#pragma unroll
+            for (uint32_t q = 0; q < 16; q += 4)
+                *reinterpret_cast<f32v4 *>(mine + lane % 32 * kRowBytes + (32 * j + 2 * q + 4 * (lane / 32)) * 4) =
+                    f32v4{acc[i][j][q], acc[i][j][q + 1], acc[i][j][q + 2], acc[i][j][q + 3]};
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        constexpr uint32_t eights = BN / 16, step = kLanes / eights;
+        const uint32_t c = n0 + wn + lane % eights * 8;
+        for (uint32_t q = lane / eights; q < 32; q += step) {
+            const uint32_t r = m0 + wm + 32 * i + q;
+            const f32v4 *from = reinterpret_cast<const f32v4 *>(mine + q * kRowBytes + lane % eights * 32);
+            const f32v4 lo = from[0], hi = from[1];
+            float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+            if (r < p.m && c < p.n) finish8(e, r, c, min(p.n - c, 8u), v);
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    }
+}
+
+// The parts of a split contraction, added in order.
+__global__ __launch_bounds__(256) void product_join_kernel(const float *parts, uint32_t splits, uint32_t m, uint32_t n,
+                                                           Epilogue e) {
+    const uint32_t per_row = (n + 7) / 8;
+    const uint64_t all = (uint64_t)m * per_row, part = (uint64_t)m * n;
+    for (uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (uint64_t)gridDim.x * 256) {
+        const uint64_t r = i / per_row;
+        const uint32_t c = (uint32_t)(i % per_row) * 8, k = min(n - c, 8u);
+        float v[8], w[8];
+        load8(parts, 1, r * n + c, k, v);
+        for (uint32_t s = 1; s < splits; ++s) {
+            load8(parts, 1, s * part + r * n + c, k, w);
+#pragma unroll
+            for (uint32_t j = 0; j < 8; ++j) v[j] += w[j];
+        }
+        finish8(e, r, c, k, v);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// few rows: bound by reading the weights
+// ---------------------------------------------------------------------------
+
+// 16 rows of B against 16 MT rows of A, both along the contraction.  The waves of a
+// block take its blocks of 64 in turn, STEP at a time, straight from memory into
+// the registers of the matrix instructions, and add their sums through LDS.
+template <uint32_t MT, uint32_t WAVES, uint32_t STEP>
+__global__ __launch_bounds__(WAVES * 64) void product_rows_kernel(ProductArgs p) {
+    __shared__ f32v4 part[WAVES][MT][kLanes];
+    const uint32_t lane = lane_id(), wave = (uint32_t)__builtin_amdgcn_readfirstlane(threadIdx.x / kLanes);
+    const uint32_t ntiles = (p.n + 15) / 16, n0 = blockIdx.x % ntiles * 16, m0 = blockIdx.x / ntiles * 16 * MT;
+    const uint32_t fr = lane % 16, fc = 8 * (lane / 16);
+    const uint16_t *b = p.b + (uint64_t)min(n0 + fr, p.n - 1) * p.ldb;
+    const uint16_t *a[MT];
+#pragma unroll
+    for (uint32_t i = 0; i < MT; ++i) a[i] = p.a + (uint64_t)min(m0 + 16 * i + fr, p.m - 1) * p.lda;
+    f32v4 acc[MT];
+#pragma unroll
+    for (uint32_t i = 0; i < MT; ++i) acc[i] = f32v4{0.0f, 0.0f, 0.0f, 0.0f};
+    const uint32_t whole = p.k / kPBlock;
+    uint32_t kb = wave * STEP;
+    for (; kb + STEP <= whole; kb += WAVES * STEP) {
+        bf16v8 fb[STEP][2], fa[STEP][MT][2];
+#pragma unroll
+        for (uint32_t u = 0; u < STEP; ++u)
+#pragma unroll
+            for (uint32_t h = 0; h < 2; ++h) {
+                const uint64_t at = (uint64_t)(kb + u) * kPBlock + 32 * h + fc;
+                fb[u][h] = __builtin_bit_cast(bf16v8, (u32v4)__builtin_nontemporal_load(reinterpret_cast<const u32v4a2 *>(b + at)));
+#pragma unroll
+                for (uint32_t i = 0; i < MT; ++i)
+                    fa[u][i][h] = __builtin_bit_cast(bf16v8, (u32v4) * reinterpret_cast<const u32v4a2 *>(a[i] + at));
+            }
+#pragma unroll
+        for (uint32_t u = 0; u < STEP; ++u)
+#pragma unroll
+            for (uint32_t h = 0; h < 2; ++h)
+#pragma unroll
+                for (uint32_t i = 0; i < MT; ++i)
+                    acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[u][h], fa[u][i][h], acc[i], 0, 0, 0);
+    }
+    // what is left of this wave's last turn, the contraction's ragged end in it
+    for (uint32_t u = 0; u < STEP && kb + u < p.blocks; ++u)
+#pragma unroll
+        for (uint32_t h = 0; h < 2; ++h) {
+            const uint32_t at = (kb + u) * kPBlock + 32 * h + fc, n = at < p.k ? p.k - at : 0u;
+            Eight<false> wb, wa;
+            wb.load(b, at, n, false);
+#pragma unroll
+            for (uint32_t i = 0; i < MT; ++i) {
+                wa.load(a[i], at, n, false);
+                acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16v8, wb.w[0]),
+                                                                 __builtin_bit_cast(bf16v8, wa.w[0]), acc[i], 0, 0, 0);
+            }
+        }
+#pragma unroll
+    for (uint32_t i = 0; i < MT; ++i) part[wave][i][lane] = acc[i];
+    __syncthreads();
+    // a lane of the sums holds four consecutive columns of one row: two lanes' make eight
+    if (lane >= 32) return;
+    for (uint32_t i = wave; i < MT; i += WAVES) {
+        const uint32_t from = lane % 16 + 32 * (lane / 16);
+        f32v4 lo = part[0][i][from], hi = part[0][i][from + 16];
+#pragma unroll
+        for (uint32_t w = 1; w < WAVES; ++w) {
+            lo += part[w][i][from];
+            hi += part[w][i][from + 16];
+        }
+        float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        const uint32_t r = m0 + 16 * i + lane % 16, c = n0 + 8 * (lane / 16);
+        if (r < p.m && c < p.n) finish8(p.e, r, c, min(p.n - c, 8u), v);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// the gradient of the pre-activation, and of the bias
+// ---------------------------------------------------------------------------
+
+struct SlopeArgs {
+    const void *dout;
+    const uint16_t *pre;
+    uint16_t *dpre;
+    float *parts;
+    uint64_t dout_stride, pre_stride, dpre_stride;
+    uint32_t rows, cols, row_step, act, dout_f32;
+    float scale;
+};
+// A block takes 64 * 8 columns and, over its four waves, every fourth row of its run of rows.
+constexpr uint32_t kSWaves = 4;
+__global__ __launch_bounds__(kSWaves * kLanes) void slope_kernel(SlopeArgs a) {
+    __shared__ float sums[kSWaves][kLanes * 8];
+    const uint32_t lane = lane_id(), wave = threadIdx.x / kLanes;
+    const uint32_t c = (blockIdx.x * kLanes + lane) * 8, n = c < a.cols ? min(a.cols - c, 8u) : 0u;
+    const uint64_t r1 = min((uint64_t)a.rows, (uint64_t)(blockIdx.y + 1) * a.row_step);
+    float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    for (uint64_t r = (uint64_t)blockIdx.y * a.row_step + wave; r < r1; r += kSWaves) {
+        float d[8];
+        load8(a.dout, a.dout_f32, r * a.dout_stride + c, n, d);
+        if (a.act != ZC_ACT_NONE) {
+            Eight<false> v;
+            v.load(a.pre, r * a.pre_stride + c, n, true);
+#pragma unroll
+            for (uint32_t i = 0; i < 8; ++i) d[i] = sloped(d[i], v[i], a.act);
+        }
+#pragma unroll
+        for (uint32_t i = 0; i < 8; ++i) {
+            d[i] *= a.scale;
+            acc[i] += d[i];
+        }
+        if (a.dpre) store_values<false>(a.dpre + r * a.dpre_stride + c, pack8(d), n);
+    }
+    if (!a.parts) return;
+#pragma unroll
+    for (uint32_t i = 0; i < 8; ++i) sums[wave][lane * 8 + i] = acc[i];
+    __syncthreads();
+    for (uint32_t i = threadIdx.x; i < kLanes * 8; i += kSWaves * kLanes) {
+        const uint32_t col = blockIdx.x * kLanes * 8 + i;
+        float s = sums[0][i];
+#pragma unroll
+        for (uint32_t w = 1; w < kSWaves; ++w) s += sums[w][i];
+        if (col < a.cols) a.parts[(uint64_t)blockIdx.y * a.cols + col] = s;
+    }
+}
+// The parts of a column's sum, added in order: 64 columns a block, in 16 runs of parts.
+constexpr uint32_t kRuns = 16;
+__global__ __launch_bounds__(kLanes * kRuns) void column_sums_kernel(const float *parts, uint32_t count, uint32_t cols,
+                                                                     float *out) {
+    __shared__ float run[kRuns][kLanes];
+    const uint32_t c = blockIdx.x * kLanes + lane_id(), w = threadIdx.x / kLanes;
+    float v = 0.0f;
+    if (c < cols)
+        for (uint32_t i = count * w / kRuns; i < count * (w + 1) / kRuns; ++i) v += parts[(uint64_t)i * cols + c];
+    run[w][lane_id()] = v;
+    __syncthreads();
+    if (w || c >= cols) return;
+#pragma unroll
+    for (uint32_t i = 1; i < kRuns; ++i) v += run[i][lane_id()];
+    out[c] = v;
+}
+
+// ---------------------------------------------------------------------------
+// which kernel
+// ---------------------------------------------------------------------------
+
+enum Tile { kT128, kT128Deep, kT256x128, kT256, kTAny };
+struct ProductChoice {
+    uint32_t rows_mt;  // > 0: product_rows_kernel with so many tiles of 16 rows
+    Tile tile;
+    uint32_t splits;
+};
+
+// The shape with the least time by a model: a round of workgroups over the 256 CUs takes
+// so many us for each block of 64 of the contraction, and some for its start and end.
+static ProductChoice product_choice(uint64_t m, uint64_t n, uint64_t k, bool along, bool direct) {
+    ProductChoice c = {0, kT128, 1};
+    if (along && m <= 32 && ceil_div(n, 16) * ceil_div(m, 16) < (1u << 22)) {
+        c.rows_mt = m <= 16 ? 1 : 2;
+        return c;
+    }
+    const double blocks = (double)ceil_div(k, kPBlock);
+    const auto time = [](uint64_t t, uint64_t at_once, double us) { return (double)ceil_div(t, at_once) * us; };
+    const uint64_t t128 = ceil_div(m, 128) * ceil_div(n, 128);
+    const double per = direct ? 1.0 : 2.5;
+    double best = time(t128, 512, per * 1.1 * blocks + 4.0);
+    const auto offer = [&](Tile tile, uint32_t splits, double us) {
+        if (us < best) {
+            best = us;
+            c.tile = tile;
+            c.splits = splits;
+        }
+    };
+    if (direct) {
+        offer(kT256, 1, time(ceil_div(m, 256) * ceil_div(n, 256), 256, 1.3 * blocks + 9.0));
+        offer(kT256x128, 1, time(ceil_div(m, 256) * ceil_div(n, 128), 256, 0.85 * blocks + 6.0));
+        offer(kT128Deep, 1, time(t128, 256, 0.55 * blocks + 4.0));
+    } else {
+        c.tile = kTAny;
+    }
+    for (uint32_t s = 2; s <= 8; s *= 2) {
+        const uint64_t bytes = m * n * 4 * s;
+        if (bytes > ZC_MATMUL_WORKSPACE_MAX || blocks < 4 * s) break;
+        const double add = 4.0 + 2.0 * (double)bytes / 4.0e6;
+        if (direct)
+            offer(kT128Deep, s, time(t128 * s, 256, 0.55 * blocks / s + 4.0) + add);
+        else
+            offer(kTAny, s, time(t128 * s, 512, per * 1.1 * blocks / s + 4.0) + add);
+    }
+    return c;
+}
+
+template <bool XA, bool XB>
+static void launch_tiles(const ProductArgs &p, Tile tile, dim3 grid, Launches &on) {
+    const dim3 block(kPThreads);
+    switch (tile) {
+        case kT256: return on.launch((product_kernel<256, 256, 2, XA, XB, true>), grid, block, p);
+        case kT256x128: return on.launch((product_kernel<256, 128, 3, XA, XB, true>), grid, block, p);
+        case kT128Deep: return on.launch((product_kernel<128, 128, 3, XA, XB, true>), grid, block, p);
+        case kT128: return on.launch((product_kernel<128, 128, 2, XA, XB, true>), grid, block, p);
+        default: return on.launch((product_kernel<128, 128, 1, XA, XB, false>), grid, block, p);
+    }
+}
+
+// Straight loads into LDS take 16 bytes at a time from 32-bit offsets.
+static bool direct_ok(const void *p, uint64_t ld) { return aligned(p, 16) && ld % 8 == 0 && ld <= (1u << 22); }
+
+static zc_status launch_product(ProductArgs p, uint64_t m, uint64_t n, uint64_t k, bool xa, bool xb, void *ws,
+                                uint64_t ws_bytes, void *stream) {
+    p.m = (uint32_t)m;
+    p.n = (uint32_t)n;
+    p.k = (uint32_t)k;
+    p.blocks = (uint32_t)ceil_div(k, kPBlock);
+    const bool direct = direct_ok(p.a, p.lda) && direct_ok(p.b, p.ldb);
+    // a whole block may be loaded unless its last chunks pass the end of the operand
+    p.direct = p.k / kPBlock;
+    if (k % kPBlock == 0 && p.direct && ((xa && m % 8) || (xb && n % 8))) --p.direct;
+    ProductChoice c = product_choice(m, n, k, !xa && !xb, direct);
+    if (!ws || ws_bytes < zc_matmul_workspace_bytes(m, n, k)) c.splits = 1;
+    if (c.splits == 1 && !direct && !c.rows_mt) c.tile = kTAny;
+    const uint64_t tm = c.tile == kT256 || c.tile == kT256x128 ? 256 : 128, tn = c.tile == kT256 ? 256 : 128;
+    const uint64_t tiles = c.rows_mt ? ceil_div(m, 16 * c.rows_mt) * ceil_div(n, 16) : ceil_div(m, tm) * ceil_div(n, tn);
+    const uint32_t threads = c.rows_mt ? 512 : kPThreads;
+    if (tiles > 0xFFFFFFFFull / threads - 8) return ZC_ERR_INVALID_ARG;
+    Launches on(stream);
+    if (c.rows_mt) {
+        const dim3 grid((uint32_t)tiles);
+        if (c.rows_mt == 1)
+            on.launch((product_rows_kernel<1, 8, 4>), grid, dim3(512), p);
+        else
+            on.launch((product_rows_kernel<2, 8, 4>), grid, dim3(512), p);
+        return on.status();
+    }
+    if (c.splits > 1) p.parts = static_cast<float *>(ws);
+    const dim3 grid((uint32_t)(ceil_div(tiles, 8) * 8), c.splits);
+    if (!xa && !xb) launch_tiles<false, false>(p, c.tile, grid, on);
+    if (!xa && xb) launch_tiles<false, true>(p, c.tile, grid, on);
+    if (xa && xb) launch_tiles<true, true>(p, c.tile, grid, on);
+    if (c.splits > 1) {
+        const uint64_t units = ceil_div(m * ceil_div(n, 8), 256);
+        on.launch(product_join_kernel, dim3((uint32_t)(units < 4096 ? units : 4096)), dim3(256), p.parts, c.splits, p.m,
+                  p.n, p.e);
+    }
+    return on.status();
+}
+
+static bool real_type(uint32_t t) { return t == ZC_F32 || t == ZC_BF16; }
+static bool typed_aligned(const void *p, uint32_t type) { return aligned(p, type == ZC_F32 ? 4 : 2); }
+static bool row_ok(uint64_t stride, uint64_t cols) { return stride >= cols && stride <= kMaxStride; }
+static bool finite_float(float v) { return v - v == 0.0f; }
+
+// A gradient: add + product.
+static zc_status gradient(ProductArgs p, uint64_t m, uint64_t n, uint64_t k, bool xa, const void *d_add,
+                          uint32_t add_type, uint64_t add_stride, void *d_out, uint32_t out_type, uint64_t out_stride,
+                          void *ws, uint64_t ws_bytes, void *stream) {
+    if (!real_type(out_type) || !row_ok(out_stride, n) || (d_add && (!real_type(add_type) || !row_ok(add_stride, n))))
+        return ZC_ERR_INVALID_ARG;
+    if (!m || !n) return ZC_OK;
+    if (!d_out || (k && (!p.a || !p.b))) return ZC_ERR_INVALID_ARG;
+    if (!aligned(p.a, 2) || !aligned(p.b, 2) || !typed_aligned(d_out, out_type) ||
+        (d_add && !typed_aligned(d_add, add_type)) || !aligned(ws, 16))
+        return ZC_ERR_MISALIGNED;
+    p.e.res = d_add;
+    p.e.res_f32 = add_type == ZC_F32;
+    p.e.res_stride = add_stride;
+    p.e.out = d_out;
+    p.e.out_f32 = out_type == ZC_F32;
+    p.e.out_stride = out_stride;
+    p.e.scale = 1.0f;
+    return launch_product(p, m, n, k, xa, true, ws, ws_bytes, stream);
+}
+
+constexpr uint32_t kSlopeRuns = 64;  // runs of rows whose column sums are parts
+
+}  // namespace moe
+}  // namespace zc
+
+using namespace zc::moe;
+
+extern "C" uint64_t zc_matmul_workspace_bytes(uint64_t rows, uint64_t cols, uint64_t contraction) {
+    if (rows > kMaxRows || cols > kMaxRows || contraction > kMaxRows || !rows || !cols) return 0;
+    uint64_t most = 0;
+    for (int along = 0; along < 2; ++along)
+        for (int direct = 0; direct < 2; ++direct) {
+            const ProductChoice c = product_choice(rows, cols, contraction, along != 0, direct != 0);
+            if (c.splits > 1 && rows * cols * 4 * c.splits > most) most = rows * cols * 4 * c.splits;
+        }
+    return most;
+}
+
+extern "C" zc_status zc_matmul(const void *d_a, uint64_t m, uint64_t a_stride, const void *d_w, uint64_t n, uint64_t k,
+                               uint64_t w_stride, const zc_epilogue *epilogue, void *d_out, uint32_t out_type,
+                               uint64_t out_stride, void *d_workspace, uint64_t workspace_bytes, void *stream) {
+    if (m > kMaxRows || n > kMaxCols || k > kMaxCols || !row_ok(a_stride, k) || !row_ok(w_stride, k) ||
+        !real_type(out_type) || !row_ok(out_stride, n))
+        return ZC_ERR_INVALID_ARG;
+    ProductArgs p = {};
+    p.e.scale = 1.0f;
+    if (epilogue) {
+        const zc_epilogue &e = *epilogue;
+        if (e.activation > ZC_ACT_SIGMOID || !finite_float(e.scale) || (e.d_bias && !real_type(e.bias_type)) ||
+            (e.d_residual && (!real_type(e.residual_type) || !row_ok(e.residual_stride, n))) ||
+            (e.d_pre && !row_ok(e.pre_stride, n)))
+            return ZC_ERR_INVALID_ARG;
+        p.e.bias = e.d_bias;
+        p.e.bias_f32 = e.bias_type == ZC_F32;
+        p.e.res = e.d_residual;
+        p.e.res_f32 = e.residual_type == ZC_F32;
+        p.e.res_stride = e.residual_stride;
+        p.e.pre = static_cast<uint16_t *>(e.d_pre);
+        p.e.pre_stride = e.pre_stride;
+        p.e.act = e.activation;
+        p.e.scale = e.scale;
+    }
+    if (!m || !n) return ZC_OK;
+    if (!d_out || (k && (!d_a || !d_w))) return ZC_ERR_INVALID_ARG;
+    if (!aligned(d_a, 2) || !aligned(d_w, 2) || !typed_aligned(d_out, out_type) || !aligned(d_workspace, 16) ||
+        (p.e.bias && !typed_aligned(p.e.bias, epilogue->bias_type)) ||
+        (p.e.res && !typed_aligned(p.e.res, epilogue->residual_type)) || !aligned(p.e.pre, 2))
+        return ZC_ERR_MISALIGNED;
+    p.a = static_cast<const uint16_t *>(d_a);
+    p.b = static_cast<const uint16_t *>(d_w);
+    p.lda = a_stride;
+    p.ldb = w_stride;
+    p.e.out = d_out;
+    p.e.out_f32 = out_type == ZC_F32;
+    p.e.out_stride = out_stride;
+    return launch_product(p, m, n, k, false, false, d_workspace, workspace_bytes, stream);
+}
+
+extern "C" uint64_t zc_activation_backward_workspace_bytes(uint64_t rows, uint64_t cols) {
+    if (rows > kMaxRows || cols > kMaxCols || !rows || !cols) return 0;
+    return ceil_div(kSlopeRuns * cols * 4, 256) * 256;
+}
+
+extern "C" zc_status zc_activation_backward(const void *d_dout, uint32_t dout_type, uint64_t rows, uint64_t cols,
+                                            uint64_t dout_stride, const void *d_pre, uint64_t pre_stride,
+                                            uint32_t activation, float scale, void *d_dpre, uint64_t dpre_stride,
+                                            float *d_dbias, void *d_workspace, uint64_t workspace_bytes,
+                                            void *stream) {
+    const bool sloped = activation != ZC_ACT_NONE;
+    if (!real_type(dout_type) || rows > kMaxRows || cols > kMaxCols || activation > ZC_ACT_SIGMOID ||
+        !finite_float(scale) || !row_ok(dout_stride, cols) || (sloped && !row_ok(pre_stride, cols)) ||
+        (d_dpre && !row_ok(dpre_stride, cols)))
+        return ZC_ERR_INVALID_ARG;
+    if (!cols || (!rows && !d_dbias) || (!d_dpre && !d_dbias)) return ZC_OK;
+    if (rows && (!d_dout || (sloped && !d_pre) || (d_dbias && !d_workspace))) return ZC_ERR_INVALID_ARG;
+    if (!typed_aligned(d_dout, dout_type) || (sloped && !aligned(d_pre, 2)) || !aligned(d_dpre, 2) || !aligned(d_dbias, 4) ||
+        !aligned(d_workspace, 16))
+        return ZC_ERR_MISALIGNED;
+    if (rows && d_dbias && workspace_bytes < zc_activation_backward_workspace_bytes(rows, cols)) return ZC_ERR_CAPACITY;
+    SlopeArgs a = {};
+    a.dout = d_dout;
+    a.pre = static_cast<const uint16_t *>(d_pre);
+    a.dpre = static_cast<uint16_t *>(d_dpre);
+    a.parts = d_dbias ? static_cast<float *>(d_workspace) : nullptr;
+    a.dout_stride = dout_stride;
+    a.pre_stride = pre_stride;
+    a.dpre_stride = dpre_stride;
+    a.rows = (uint32_t)rows;
+    a.cols = (uint32_t)cols;
+    a.row_step = (uint32_t)ceil_div(ceil_div(rows, kSlopeRuns), kSWaves) * kSWaves;
+    a.act = activation;
+    a.dout_f32 = dout_type == ZC_F32;
+    a.scale = scale;
+    const uint32_t runs = rows ? (uint32_t)ceil_div(rows, a.row_step) : 0;
+    Launches on(stream);
+    if (rows) on.launch(slope_kernel, dim3((uint32_t)ceil_div(cols, kLanes * 8), runs), dim3(kSWaves * kLanes), a);
+    if (d_dbias)
+        on.launch(column_sums_kernel, dim3((uint32_t)ceil_div(cols, kLanes)), dim3(kLanes * kRuns), a.parts, runs, a.cols,
+                  d_dbias);
+    return on.status();
+}
+
+extern "C" zc_status zc_matmul_dgrad(const void *d_dpre, uint64_t m, uint64_t n, uint64_t dpre_stride, const void *d_w,
+                                     uint64_t k, uint64_t w_stride, const void *d_add, uint32_t add_type,
+                                     uint64_t add_stride, void *d_dx, uint32_t dx_type, uint64_t dx_stride,
+                                     void *d_workspace, uint64_t workspace_bytes, void *stream) {
+    if (m > kMaxRows || n > kMaxCols || k > kMaxCols || !row_ok(dpre_stride, n) || !row_ok(w_stride, k))
+        return ZC_ERR_INVALID_ARG;
+    ProductArgs p = {};
+    p.a = static_cast<const uint16_t *>(d_dpre);
+    p.b = static_cast<const uint16_t *>(d_w);
+    p.lda = dpre_stride;
+    p.ldb = w_stride;
+    return gradient(p, m, k, n, false, d_add, add_type, add_stride, d_dx, dx_type, dx_stride, d_workspace,
+                    workspace_bytes, stream);
+}
+
+extern "C" zc_status zc_matmul_wgrad(const void *d_dpre, uint64_t m, uint64_t n, uint64_t dpre_stride, const void *d_a,
+                                     uint64_t k, uint64_t a_stride, const void *d_add, uint32_t add_type,
+                                     uint64_t add_stride, void *d_dw, uint32_t dw_type, uint64_t dw_stride,
+                                     void *d_workspace, uint64_t workspace_bytes, void *stream) {
+    if (m > kMaxRows || n > kMaxCols || k > kMaxCols || !row_ok(dpre_stride, n) || !row_ok(a_stride, k))
+        return ZC_ERR_INVALID_ARG;
+    ProductArgs p = {};
+    p.a = static_cast<const uint16_t *>(d_dpre);
+    p.b = static_cast<const uint16_t *>(d_a);
+    p.lda = dpre_stride;
+    p.ldb = a_stride;
+    return gradient(p, n, k, m, true, d_add, add_type, add_stride, d_dw, dw_type, dw_stride, d_workspace,
+                    workspace_bytes, stream);
+}

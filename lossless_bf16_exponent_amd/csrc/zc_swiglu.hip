@@ -6,7 +6,7 @@ namespace zc {
 namespace moe {
 
 constexpr uint32_t kGThreads = 256;
-constexpr uint32_t kGLanes = 16;  // lanes of a block of 128 columns, 8 values each
+constexpr uint32_t kGLanes = kKeepLanes;  // lanes of a block of 128 columns, 8 values each
 constexpr uint32_t kGBlocks = kGThreads / kGLanes;
 
 struct GateArgs {
@@ -70,23 +70,6 @@ __device__ __forceinline__ void gradients8(const float (&g)[8], const float (&u)
         dg[i] = d * u[i] * (o.s * fmaf(g[i], o.rest, 1.0f)) * o.unit;
         du[i] = d * (g[i] * o.s) * o.unit;
     }
-}
-
-// The 8 values' 8-bit form under the block's scale (16 lanes a block); lane 0
-// writes the scale.
-__device__ __forceinline__ void keep8(const u32v4 &w, uint8_t *q, uint8_t *s, uint32_t sub) {
-    uint32_t m = 0;
-#pragma unroll
-    for (uint32_t i = 0; i < 4; ++i) m = finite_max(m, w[i]);
-    m = group_max<kGLanes>(m);
-    typedef Fp8<ZC_FP8_E4M3> F;
-    const uint32_t byte = scale_byte(m, F::kTop);
-    const float inv = scale_inverse(byte);
-    uint2 r;
-    r.x = F::pack4(bf_lo(w[0]) * inv, bf_hi(w[0]) * inv, bf_lo(w[1]) * inv, bf_hi(w[1]) * inv);
-    r.y = F::pack4(bf_lo(w[2]) * inv, bf_hi(w[2]) * inv, bf_lo(w[3]) * inv, bf_hi(w[3]) * inv);
-    *reinterpret_cast<uint2 *>(q) = r;
-    if (sub == 0) *s = (uint8_t)byte;
 }
 
 // Everything is read once and written once: non-temporal accesses (65536 x 2048
