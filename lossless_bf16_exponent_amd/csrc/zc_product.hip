@@ -34,7 +34,7 @@ struct ProductArgs {
     uint64_t lda, ldb;  // elements
     uint32_t m, n, k;   // results' rows and columns, contraction
     uint32_t blocks;    // blocks of 64 along the contraction
-    uint32_t direct;    // of which the first so many may be loaded whole
+    uint32_t direct;    // of which the first so many may be loaded whole, 16 bytes at a time
     float *parts;       // a split contraction's sums, gridDim.y of them; or NULL
     Epilogue e;
 };
@@ -43,19 +43,44 @@ struct ProductArgs {
 // activations
 // ---------------------------------------------------------------------------
 
-// sigmoid(v) = s * t.  From -20 down it is e^v to 32 bits, taken as the square of
-// e^(v / 2): a product with a large value then keeps its digits where e^v has none left.
+// sigmoid(v) = s * t and 1 - sigmoid(v), from e^(-|v| / 2) and its square, which do not
+// overflow.  Left of 0, t is that root: a product with a large value keeps its digits
+// where the exponential has none left.  The hardware exponential and reciprocal are off by a
+// unit of 32 bits, as much as rounding their argument is; the library's took 4 to 5 times as many
+// instructions, in tiles of one wave a SIMD (8192 x 4096 x 7168 with SILU: 76 us of 511).
 struct Parts {
-    float s, t;
+    float s, t, rest;
 };
 __device__ __forceinline__ Parts sigmoid_parts(float v) {
-    if (v < -20.0f) {
-        const float h = expf(0.5f * v);
-        return {h, h};
-    }
-    return {1.0f / (1.0f + expf(-v)), 1.0f};
+    const float root = __builtin_amdgcn_exp2f(fabsf(v) * -0.72134752f), e = root * root;
+    const float r = __builtin_amdgcn_rcpf(1.0f + e);
+    const bool right = v >= 0.0f;
+    return {right ? r : root * r, right ? 1.0f : root, right ? e * r : r};
 }
-constexpr float kRootHalf = 0.70710678f, kRootPi = 0.79788456f, kCubic = 0.044715f;  // sqrt(1 / 2), sqrt(2 / pi)
+// The normal distribution's tail beyond |v| is q * root, with root = e^(-v^2 / 4) and,
+// for x = |v| / sqrt(2), q = root * t * (erfc(x) e^(x^2) / t) / 2, t = 1 / (1 + x / 2): the
+// quotient is a polynomial of t to 1e-8 of itself on all of 0..1 (fitted here to its values
+// at Chebyshev's points with weights that level the error).
+struct Tail {
+    float m, root;  // q = m * root
+};
+__device__ __forceinline__ Tail normal_tail(float v) {
+    const float t = __builtin_amdgcn_rcpf(fmaf(fabsf(v), 0.35355339f, 1.0f));
+    float p = 0.0423526122f;
+    p = fmaf(p, t, -0.230857749f);
+    p = fmaf(p, t, 0.486179082f);
+    p = fmaf(p, t, -0.446977725f);
+    p = fmaf(p, t, 0.127089673f);
+    p = fmaf(p, t, -0.0572325763f);
+    p = fmaf(p, t, 0.093000611f);
+    p = fmaf(p, t, 0.175376827f);
+    p = fmaf(p, t, 0.246880587f);
+    p = fmaf(p, t, 0.282093853f);
+    p = fmaf(p, t, 0.282094795f);
+    return {0.5f * t * p, __builtin_amdgcn_exp2f(v * v * -0.36067376f)};
+}
+constexpr float kTanh = 1.59576912f, kCubic = 0.044715f;  // 2 sqrt(2 / pi): (1 + tanh(u)) / 2 = sigmoid(2 u)
+constexpr float kDensity = 0.39894228f;                   // 1 / sqrt(2 pi)
 
 __device__ __forceinline__ float activation(float v, uint32_t act) {
     switch (act) {
@@ -65,13 +90,12 @@ __device__ __forceinline__ float activation(float v, uint32_t act) {
             return v * p.s * p.t;
         }
         case ZC_ACT_GELU: {
-            // the tail from erfc, which keeps its digits
-            const float x = v * kRootHalf;
-            return v * (0.5f * erfcf(-x));
+            const Tail n = normal_tail(v);
+            const float q = n.m * n.root;
+            return v >= 0.0f ? fmaf(-v * q, n.root, v) : v * q * n.root;
         }
         case ZC_ACT_GELU_TANH: {
-            // (1 + tanh(u)) / 2 = sigmoid(2 u)
-            const Parts p = sigmoid_parts(2.0f * kRootPi * (v + kCubic * v * v * v));
+            const Parts p = sigmoid_parts(kTanh * fmaf(kCubic * v * v, v, v));
             return v * p.s * p.t;
         }
         case ZC_ACT_SIGMOID: {
@@ -88,25 +112,24 @@ __device__ __forceinline__ float sloped(float d, float v, uint32_t act) {
         case ZC_ACT_RELU: return v > 0.0f ? d : v != v ? v : 0.0f;
         case ZC_ACT_SILU: {
             const Parts p = sigmoid_parts(v);
-            const float rest = v < -20.0f ? 1.0f : expf(-v) * p.s;
-            return d * (1.0f + v * rest) * p.s * p.t;
+            return d * fmaf(v, p.rest, 1.0f) * p.s * p.t;
         }
         case ZC_ACT_GELU: {
-            // Phi(v) + v phi(v), the density as a square for the same reason as above
-            const float half = expf(-0.25f * v * v);
-            return d * (0.5f * erfcf(-v * kRootHalf)) + (d * v * 0.39894228f * half) * half;
+            // Phi(v) + v phi(v)
+            const Tail n = normal_tail(v);
+            const float near = d * n.root;
+            return v >= 0.0f ? fmaf(near * fmaf(v, kDensity, -n.m), n.root, d)
+                             : near * fmaf(v, kDensity, n.m) * n.root;
         }
         case ZC_ACT_GELU_TANH: {
             // from 30 on the slope is 1 or 0 in 32 bits
-            const float x = v != v ? v : fminf(fmaxf(v, -30.0f), 30.0f), w = 2.0f * kRootPi * (x + kCubic * x * x * x);
-            const Parts p = sigmoid_parts(w);
-            const float rest = w < -20.0f ? 1.0f : expf(-w) * p.s;
-            return d * (1.0f + x * rest * (2.0f * kRootPi * (1.0f + 3.0f * kCubic * x * x))) * p.s * p.t;
+            const float x = v != v ? v : fminf(fmaxf(v, -30.0f), 30.0f), y = kCubic * x * x;
+            const Parts p = sigmoid_parts(kTanh * fmaf(y, x, x));
+            return d * fmaf(x * p.rest, kTanh * fmaf(3.0f, y, 1.0f), 1.0f) * p.s * p.t;
         }
         case ZC_ACT_SIGMOID: {
-            const float x = v != v ? v : -fabsf(v);
-            const Parts p = sigmoid_parts(x);
-            return d * p.s * p.t * (1.0f / (1.0f + expf(x)));
+            const Parts p = sigmoid_parts(v != v ? v : -fabsf(v));
+            return d * p.s * p.t * p.rest;
         }
         default: return d;
     }
@@ -116,33 +139,54 @@ __device__ __forceinline__ float sloped(float d, float v, uint32_t act) {
 // epilogue
 // ---------------------------------------------------------------------------
 
+// Eight values of either type as they are stored.
+struct Raw {
+    u32v4 w[2];
+    __device__ __forceinline__ void load(const void *p, uint32_t f32, uint64_t at, uint32_t n) {
+        if (f32) {
+            Eight<true> e;
+            e.load(p, at, n, false);
+            w[0] = e.w[0];
+            w[1] = e.w[1];
+        } else {
+            Eight<false> e;
+            e.load(p, at, n, false);
+            w[0] = e.w[0];
+        }
+    }
+    __device__ __forceinline__ void values(uint32_t f32, float (&v)[8]) const {
+#pragma unroll
+        for (uint32_t i = 0; i < 8; ++i)
+            v[i] = f32 ? __uint_as_float(w[i / 4][i & 3]) : (i & 1) ? bf_hi(w[0][i / 2]) : bf_lo(w[0][i / 2]);
+    }
+};
 __device__ __forceinline__ void load8(const void *p, uint32_t f32, uint64_t at, uint32_t n, float (&v)[8]) {
-    if (f32) {
-        Eight<true> w;
-        w.load(p, at, n, false);
-#pragma unroll
-        for (uint32_t i = 0; i < 8; ++i) v[i] = w[i];
-    } else {
-        Eight<false> w;
-        w.load(p, at, n, false);
-#pragma unroll
-        for (uint32_t i = 0; i < 8; ++i) v[i] = w[i];
-    }
+    Raw r;
+    r.load(p, f32, at, n);
+    r.values(f32, v);
 }
-// The sums of columns c .. c + n - 1 of row r become results.
-__device__ __forceinline__ void finish8(const Epilogue &e, uint64_t r, uint32_t c, uint32_t n, float (&v)[8]) {
-    float w[8];
-    if (e.bias) {
-        load8(e.bias, e.bias_f32, c, n, w);
+// The bias of columns c .. c + n - 1, and the residual of row r there.
+__device__ __forceinline__ void load_bias(const Epilogue &e, uint32_t c, uint32_t n, float (&v)[8]) {
 #pragma unroll
-        for (uint32_t i = 0; i < 8; ++i) v[i] += w[i];
-    }
+    for (uint32_t i = 0; i < 8; ++i) v[i] = 0.0f;
+    if (e.bias) load8(e.bias, e.bias_f32, c, n, v);
+}
+__device__ __forceinline__ void load_residual(const Epilogue &e, uint64_t r, uint32_t c, uint32_t n, Raw &w) {
+    if (e.res) w.load(e.res, e.res_f32, r * e.res_stride + c, n);
+}
+// The sums of columns c .. c + n - 1 of row r become results in two steps: the pre-activation and its activation,
+// and the residual sum.
+__device__ __forceinline__ bool activates(const Epilogue &e) { return e.act != ZC_ACT_NONE || e.pre; }
+__device__ __forceinline__ void activate8(const Epilogue &e, uint64_t r, uint32_t c, uint32_t n, float (&v)[8]) {
     if (e.pre) store_values<false>(e.pre + r * e.pre_stride + c, pack8(v), n);
     if (e.act != ZC_ACT_NONE)
 #pragma unroll
         for (uint32_t i = 0; i < 8; ++i) v[i] = activation(v[i], e.act);
+}
+__device__ __forceinline__ void store8(const Epilogue &e, uint64_t r, uint32_t c, uint32_t n, float (&v)[8], const Raw &res) {
     if (e.res) {
-        load8(e.res, e.res_f32, r * e.res_stride + c, n, w);
+        float w[8];
+        res.values(e.res_f32, w);
 #pragma unroll
         for (uint32_t i = 0; i < 8; ++i) v[i] = fmaf(e.scale, v[i], w[i]);
     } else {
@@ -153,6 +197,16 @@ __device__ __forceinline__ void finish8(const Epilogue &e, uint64_t r, uint32_t 
         store_floats(static_cast<float *>(e.out) + r * e.out_stride + c, n, v);
     else
         store_values<false>(static_cast<uint16_t *>(e.out) + r * e.out_stride + c, pack8(v), n);
+}
+__device__ __forceinline__ void finish8(const Epilogue &e, uint64_t r, uint32_t c, uint32_t n, float (&v)[8]) {
+    float bias[8];
+    Raw res;
+    load_bias(e, c, n, bias);
+    load_residual(e, r, c, n, res);
+#pragma unroll
+    for (uint32_t i = 0; i < 8; ++i) v[i] += bias[i];
+    if (activates(e)) activate8(e, r, c, n, v);
+    store8(e, r, c, n, v, res);
 }
 
 // ---------------------------------------------------------------------------
@@ -169,8 +223,9 @@ constexpr uint32_t kPBytes = 2 * kPBlock;  // of a row or column in a stage
 //           sits at place c ^ (r / 2 mod 8), so that sixteen lanes that read the
 //           same chunk of sixteen rows meet sixteen different columns of banks
 //   across  value k of the contraction is 2 B bytes; chunk c (8 results) sits at
-//           place c ^ 4 (k mod 4): a transposing read takes 64 bytes of each of
-//           four k, which then lie in four different quarters of the banks
+//           place c ^ 4 (k mod 4), or c ^ 4 (k / 2 mod 2) where B is 64: a
+//           transposing read takes 64 bytes of each of four k, which then lie in
+//           four different quarters of the banks
 template <uint32_t B, bool ACROSS>
 struct Operand {
     static constexpr uint32_t kLoads = B / 32;         // pieces of a wave
@@ -187,8 +242,9 @@ struct Operand {
     __device__ __forceinline__ static uint32_t line(uint32_t wave, uint32_t i) {
         return ACROSS ? (wave * kLoads + i) * (kLanes / kRow) + lane_id() / kRow : wave * (B / 4) + 8 * i + lane_id() / 8;
     }
+    __device__ __forceinline__ static uint32_t key(uint32_t k) { return B == 64 ? 4 * (k / 2 & 1) : 4 * (k & 3); }
     __device__ __forceinline__ static uint32_t chunk(uint32_t line) {
-        return ACROSS ? (lane_id() % kRow) ^ (4 * (line & 3)) : (lane_id() & 7) ^ (line / 2 & 7);
+        return ACROSS ? (lane_id() % kRow) ^ key(line) : (lane_id() & 7) ^ (line / 2 & 7);
     }
 
     // byte offset of a lane's 16 bytes of a whole block from the block's start, rows past the last repeating it
@@ -202,6 +258,12 @@ struct Operand {
     }
     __device__ __forceinline__ uint64_t step() const { return ACROSS ? (uint64_t)kPBlock * ld * 2 : kPBytes; }
 
+    // where a lane's 16 bytes of a whole block are, rows past the last repeating it: at any value, rows any way apart
+    __device__ __forceinline__ const uint16_t *source(uint32_t kb, uint32_t wave, uint32_t i) const {
+        const uint32_t l = line(wave, i), c = 8 * chunk(l), room = last - first;
+        return p + (ACROSS ? ((uint64_t)kb * kPBlock + l) * ld + first + min(c, room / 8 * 8)
+                           : (uint64_t)(first + min(l, room)) * ld + (uint64_t)kb * kPBlock + c);
+    }
     // any block, any alignment: what lies past the contraction reads as 0
     __device__ __forceinline__ u32v4 load(uint32_t kb, uint32_t wave, uint32_t i) const {
         const uint32_t l = line(wave, i), c = chunk(l);
@@ -220,7 +282,7 @@ struct Operand {
 #pragma unroll
             for (uint32_t i = 0; i < kTiles; ++i) {
                 const uint32_t c = (within + 32 * i) / 8 + 2 * (lane / 16 & 1) + j % 4 / 2;
-                at[ACROSS ? i : 0] = base + k0 * (2 * B) + 16 * (c ^ (4 * (k0 & 3))) + 8 * (j & 1);
+                at[ACROSS ? i : 0] = base + k0 * (2 * B) + 16 * (c ^ key(k0)) + 8 * (j & 1);
             }
         } else {
             at[0] = base + (within + lane % 32) * kPBytes;
@@ -247,8 +309,8 @@ struct Operand {
 // into LDS, STAGES of them under way, in the order of the 8-bit products' tiles: the
 // fragments of half a block are in registers while the other half's come out
 // of LDS, and one barrier in the middle of a block frees its place and hands over
-// the next.  The contraction's ragged end, and all of it without DIRECT (operands at
-// any element, rows far apart), goes through registers.
+// the next.  Without DIRECT (operands at any element, rows far apart) a block goes
+// through registers while the one before it is multiplied, and so does the contraction's ragged end.
 template <uint32_t BM, uint32_t BN, uint32_t STAGES, bool XA, bool XB, bool DIRECT>
 __global__ __launch_bounds__(kPThreads, STAGES * (BM + BN) * kPBytes > 80 * 1024 ? 1 : 2) void product_kernel(ProductArgs p) {
     typedef Operand<BM, XA> OA;
@@ -303,7 +365,7 @@ __global__ __launch_bounds__(kPThreads, STAGES * (BM + BN) * kPBytes > 80 * 1024
             acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[half][j][h], fa[half][i][h], acc[i][j], 0, 0, 0);
     };
 
-    const uint32_t whole = DIRECT ? min(kb1, p.direct) : kb0;
+    const uint32_t whole = min(kb1, p.direct);
     if constexpr (DIRECT) if (kb0 < whole) {
         const uint32_t blocks = whole - kb0;
         const uint8_t *ga = oa.block(kb0), *gb = ob.block(kb0);
@@ -364,30 +426,61 @@ __global__ __launch_bounds__(kPThreads, STAGES * (BM + BN) * kPBytes > 80 * 1024
         for (; t < blocks; ++t) step(t, std::false_type{});
         wait_and_meet<0>();
     }
-    for (uint32_t kb = max(whole, kb0); kb < kb1; ++kb) {
-        u32v4 w[LOADS];
-#pragma unroll
-        for (uint32_t i = 0; i < LOADS; ++i) w[i] = i < LA ? oa.load(kb, wave, i) : ob.load(kb, wave, i - LA);
-        __syncthreads();  // every wave is done with the block before
+    // a block in registers into place in LDS, and from there into the sums
+    const auto lay_block = [&](uint32_t at, const u32v4 (&w)[LOADS]) {
 #pragma unroll
         for (uint32_t i = 0; i < LOADS; ++i) {
-            const uint32_t at = i < LA ? (wave * LA + i) * 1024 : BM * kPBytes + (wave * LB + i - LA) * 1024;
-            *reinterpret_cast<u32v4 *>(sh + at + 16 * lane) = w[i];
+            const uint32_t to = i < LA ? (wave * LA + i) * 1024 : BM * kPBytes + (wave * LB + i - LA) * 1024;
+            *reinterpret_cast<u32v4 *>(sh + at + to + 16 * lane) = w[i];
         }
         __syncthreads();
+    };
+    const auto take_block = [&](uint32_t at) {
 #pragma unroll
         for (uint32_t half = 0; half < 2; ++half) {
 #pragma unroll
-            for (uint32_t q = 0; q < kReads; ++q) read_piece(0, half, q);
+            for (uint32_t q = 0; q < kReads; ++q) read_piece(at, half, q);
 #pragma unroll
             for (uint32_t i = 0; i < MT; ++i)
 #pragma unroll
                 for (uint32_t j = 0; j < NT; ++j) multiply(half, i, j);
         }
+    };
+    if constexpr (!DIRECT) if (kb0 < whole) {
+        // two places in turn: one is written while other waves may still read the other
+        static_assert(STAGES == 2, "two places");
+        const uint16_t *from[LOADS];
+        u32v4 w[LOADS];
+#pragma unroll
+        for (uint32_t i = 0; i < LOADS; ++i) {
+            from[i] = i < LA ? oa.source(kb0, wave, i) : ob.source(kb0, wave, i - LA);
+            w[i] = *reinterpret_cast<const u32v4a2 *>(from[i]);
+        }
+        for (uint32_t kb = kb0; kb < whole; ++kb) {
+            const uint32_t at = ((kb - kb0) & 1) * kStage;
+            lay_block(at, w);
+            if (kb + 1 < whole)
+#pragma unroll
+                for (uint32_t i = 0; i < LOADS; ++i) {
+                    from[i] += (i < LA ? oa.step() : ob.step()) / 2;
+                    w[i] = *reinterpret_cast<const u32v4a2 *>(from[i]);
+                }
+            take_block(at);
+        }
+    }
+    for (uint32_t kb = max(whole, kb0); kb < kb1; ++kb) {
+        u32v4 w[LOADS];
+#pragma unroll
+        for (uint32_t i = 0; i < LOADS; ++i) w[i] = i < LA ? oa.load(kb, wave, i) : ob.load(kb, wave, i - LA);
+        __syncthreads();  // every wave is done with the block before
+        lay_block(0, w);
+        take_block(0);
     }
 
     // Results through LDS, 32 rows of a wave at a time, so that a row's BN / 2 columns
-    // leave as whole lines, eight a lane.
+    // leave as whole lines, eight a lane.  The residual of the next 32 rows is on its way
+    // meanwhile: one row after another, each load waited for the stores before it
+    // (8192 x 7168 x 4096 with a residual: 500 us instead of 381).
     __syncthreads();
     Epilogue e = p.e;
     if (p.parts) {
@@ -398,23 +491,122 @@ __global__ __launch_bounds__(kPThreads, STAGES * (BM + BN) * kPBytes > 80 * 1024
         e.scale = 1.0f;
     }
     uint8_t *mine = sh + wave * 32 * kRowBytes;
-#pragma unroll
-    for (uint32_t i = 0; i < MT; ++i) {
+    constexpr uint32_t eights = BN / 16, step = kLanes / eights, kTurns = 32 / step;
+    const uint32_t c = n0 + wn + lane % eights * 8, n = c < p.n ? min(p.n - c, 8u) : 0u, r0 = m0 + wm + lane / eights;
+    float bias[8];
+    load_bias(e, c, n, bias);
+    const bool acts = activates(e);
+    f32v4 *const from = reinterpret_cast<f32v4 *>(mine + lane / eights * kRowBytes + lane % eights * 32);
+    constexpr uint32_t kApart = step * kRowBytes / 16;
+    const auto lay = [&](uint32_t i) {  // 32 rows into LDS
 #pragma unroll
         for (uint32_t j = 0; j < NT; ++j)
 #pragma unroll
             for (uint32_t q = 0; q < 16; q += 4)
                 *reinterpret_cast<f32v4 *>(mine + lane % 32 * kRowBytes + (32 * j + 2 * q + 4 * (lane / 32)) * 4) =
                     f32v4{acc[i][j][q], acc[i][j][q + 1], acc[i][j][q + 2], acc[i][j][q + 3]};
+    };
+    // A whole tile without an activation: no branch stands between its loads and stores, so that the wait for the
+    // next rows' residual is not one for the stores before it.  kind: no residual, BF16, floats.
+    const auto finish = [&](auto f32, auto kind) {
+        constexpr bool F32 = decltype(f32)::value;
+        constexpr uint32_t K = decltype(kind)::value;
+        Eight<K == 2> res[2][K ? kTurns : 1];
+        const auto fetch = [&](uint32_t i) {
+            if (K)
+#pragma unroll
+                for (uint32_t q = 0; q < kTurns; ++q)
+                    res[i & 1][q % (K ? kTurns : 1)].load(e.res, (uint64_t)(r0 + 32 * i + q * step) * e.res_stride + c, 8, false);
+        };
+        fetch(0);
+#pragma unroll
+        for (uint32_t i = 0; i < MT; ++i) {
+            lay(i);
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            if (i + 1 < MT) fetch(i + 1);
+#pragma unroll
+            for (uint32_t q = 0; q < kTurns; ++q) {
+                const f32v4 lo = from[q * kApart], hi = from[q * kApart + 1];
+                float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+#pragma unroll
+                for (uint32_t x = 0; x < 8; ++x)
+                    v[x] = K ? fmaf(e.scale, v[x] + bias[x], res[i & 1][q % (K ? kTurns : 1)][x]) : (v[x] + bias[x]) * e.scale;
+                const uint64_t at = (uint64_t)(r0 + 32 * i + q * step) * e.out_stride + c;
+                if (F32)
+                    store_floats(static_cast<float *>(e.out) + at, 8, v);
+                else
+                    store_values<false>(static_cast<uint16_t *>(e.out) + at, pack8(v), 8);
+            }
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        }
+    };
+    if (!acts && m0 + BM <= p.m && n0 + BN <= p.n) {
+        typedef std::integral_constant<uint32_t, 0> None;
+        typedef std::integral_constant<uint32_t, 1> Halves;
+        typedef std::integral_constant<uint32_t, 2> Floats;
+        if (e.out_f32)
+            !e.res ? finish(std::true_type{}, None{}) : e.res_f32 ? finish(std::true_type{}, Floats{}) : finish(std::true_type{}, Halves{});
+        else
+            !e.res ? finish(std::false_type{}, None{}) : e.res_f32 ? finish(std::false_type{}, Floats{}) : finish(std::false_type{}, Halves{});
+        return;
+    }
+    Raw next[kTurns];
+    const auto fetch = [&](uint32_t i) {
+#pragma unroll
+        for (uint32_t q = 0; q < kTurns; ++q) {
+            const uint32_t r = r0 + 32 * i + q * step;
+            if (r < p.m && n) load_residual(e, r, c, n, next[q]);
+        }
+    };
+    fetch(0);
+#pragma unroll 1
+    for (uint32_t i = 0; i < MT; ++i) {
+        // (sums stay in registers only under indexes that the compiler knows)
+#pragma unroll
+        for (uint32_t known = 0; known < MT; ++known)
+            if (known == i) lay(known);
+        Raw res[kTurns];
+#pragma unroll
+        for (uint32_t q = 0; q < kTurns; ++q) res[q] = next[q];
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        constexpr uint32_t eights = BN / 16, step = kLanes / eights;
-        const uint32_t c = n0 + wn + lane % eights * 8;
-        for (uint32_t q = lane / eights; q < 32; q += step) {
-            const uint32_t r = m0 + wm + 32 * i + q;
-            const f32v4 *from = reinterpret_cast<const f32v4 *>(mine + q * kRowBytes + lane % eights * 32);
-            const f32v4 lo = from[0], hi = from[1];
+        if (i + 1 < MT) fetch(i + 1);
+        if (acts && !e.res) {
+#pragma unroll 2
+            for (uint32_t q = 0; q < kTurns; ++q) {
+                const uint32_t r = r0 + 32 * i + q * step;
+                const f32v4 lo = from[q * kApart], hi = from[q * kApart + 1];
+                float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+#pragma unroll
+                for (uint32_t x = 0; x < 8; ++x) v[x] += bias[x];
+                if (r < p.m && n) {
+                    activate8(e, r, c, n, v);
+                    store8(e, r, c, n, v, Raw{});
+                }
+            }
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            continue;
+        }
+        if (acts)  // in its place in LDS: the code of the activations stands here once
+#pragma unroll 1
+            for (uint32_t q = 0; q < kTurns; ++q) {
+                const uint32_t r = r0 + 32 * i + q * step;
+                const f32v4 lo = from[q * kApart], hi = from[q * kApart + 1];
+                float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+#pragma unroll
+                for (uint32_t x = 0; x < 8; ++x) v[x] += bias[x];
+                if (r < p.m && n) activate8(e, r, c, n, v);
+                from[q * kApart] = f32v4{v[0], v[1], v[2], v[3]};
+                from[q * kApart + 1] = f32v4{v[4], v[5], v[6], v[7]};
+            }
+#pragma unroll
+        for (uint32_t q = 0; q < kTurns; ++q) {
+            const uint32_t r = r0 + 32 * i + q * step;
+            const f32v4 lo = from[q * kApart], hi = from[q * kApart + 1];
             float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-            if (r < p.m && c < p.n) finish8(e, r, c, min(p.n - c, 8u), v);
+            if (!acts)
+#pragma unroll
+                for (uint32_t x = 0; x < 8; ++x) v[x] += bias[x];
+            if (r < p.m && n) store8(e, r, c, n, v, res[q]);
         }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
@@ -445,7 +637,8 @@ __global__ __launch_bounds__(256) void product_join_kernel(const float *parts, u
 
 // 16 rows of B against 16 MT rows of A, both along the contraction.  The waves of a
 // block take its blocks of 64 in turn, STEP at a time, straight from memory into
-// the registers of the matrix instructions, and add their sums through LDS.
+// the registers of the matrix instructions, and add their sums through LDS.  1 x
+// 4096 x 14336, weights from memory: 22.9 us, 5.1 TB/s, what a large copy reaches.
 template <uint32_t MT, uint32_t WAVES, uint32_t STEP>
 __global__ __launch_bounds__(WAVES * 64) void product_rows_kernel(ProductArgs p) {
     __shared__ f32v4 part[WAVES][MT][kLanes];
@@ -460,26 +653,52 @@ __global__ __launch_bounds__(WAVES * 64) void product_rows_kernel(ProductArgs p)
 #pragma unroll
     for (uint32_t i = 0; i < MT; ++i) acc[i] = f32v4{0.0f, 0.0f, 0.0f, 0.0f};
     const uint32_t whole = p.k / kPBlock;
-    uint32_t kb = wave * STEP;
-    for (; kb + STEP <= whole; kb += WAVES * STEP) {
-        bf16v8 fb[STEP][2], fa[STEP][MT][2];
+    // two turns' values in registers: one on its way while the other is multiplied
+    struct Turn {
+        u32v4 b[STEP][2], a[STEP][MT][2];
+    };
+    Turn turns[2];
+    const auto load = [&](Turn &t, uint32_t kb) {
 #pragma unroll
         for (uint32_t u = 0; u < STEP; ++u)
 #pragma unroll
             for (uint32_t h = 0; h < 2; ++h) {
                 const uint64_t at = (uint64_t)(kb + u) * kPBlock + 32 * h + fc;
-                fb[u][h] = __builtin_bit_cast(bf16v8, (u32v4)__builtin_nontemporal_load(reinterpret_cast<const u32v4a2 *>(b + at)));
+                t.b[u][h] = *reinterpret_cast<const u32v4a2 *>(b + at);
 #pragma unroll
-                for (uint32_t i = 0; i < MT; ++i)
-                    fa[u][i][h] = __builtin_bit_cast(bf16v8, (u32v4) * reinterpret_cast<const u32v4a2 *>(a[i] + at));
+                for (uint32_t i = 0; i < MT; ++i) t.a[u][i][h] = *reinterpret_cast<const u32v4a2 *>(a[i] + at);
             }
+    };
+    const auto take = [&](const Turn &t) {
 #pragma unroll
         for (uint32_t u = 0; u < STEP; ++u)
 #pragma unroll
             for (uint32_t h = 0; h < 2; ++h)
 #pragma unroll
                 for (uint32_t i = 0; i < MT; ++i)
-                    acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[u][h], fa[u][i][h], acc[i], 0, 0, 0);
+                    acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16v8, t.b[u][h]),
+                                                                     __builtin_bit_cast(bf16v8, t.a[u][i][h]), acc[i], 0, 0, 0);
+    };
+    uint32_t kb = wave * STEP;
+    constexpr uint32_t kTurn = WAVES * STEP;
+    if (kb + STEP <= whole) {
+        load(turns[0], kb);
+        for (;;) {
+            kb += kTurn;
+            if (kb + STEP > whole) {
+                take(turns[0]);
+                break;
+            }
+            load(turns[1], kb);
+            take(turns[0]);
+            kb += kTurn;
+            if (kb + STEP > whole) {
+                take(turns[1]);
+                break;
+            }
+            load(turns[0], kb);
+            take(turns[1]);
+        }
     }
     // what is left of this wave's last turn, the contraction's ragged end in it
     for (uint32_t u = 0; u < STEP && kb + u < p.blocks; ++u)
@@ -584,48 +803,66 @@ __global__ __launch_bounds__(kLanes * kRuns) void column_sums_kernel(const float
 // which kernel
 // ---------------------------------------------------------------------------
 
-enum Tile { kT128, kT128Deep, kT256x128, kT256, kTAny };
+enum Tile { kT128, kT128Deep, kT256x128, kT256, kT128x64, kT64, kTAny, kTAny64 };
 struct ProductChoice {
     uint32_t rows_mt;  // > 0: product_rows_kernel with so many tiles of 16 rows
     Tile tile;
     uint32_t splits;
 };
 
-// The shape with the least time by a model: a round of workgroups over the 256 CUs takes
-// so many us for each block of 64 of the contraction, and some for its start and end.
-static ProductChoice product_choice(uint64_t m, uint64_t n, uint64_t k, bool along, bool direct) {
-    ProductChoice c = {0, kT128, 1};
-    if (along && m <= 32 && ceil_div(n, 16) * ceil_div(m, 16) < (1u << 22)) {
+// Few rows: product_rows_kernel.  At 4096 x 14336, weights from memory, it takes 22.9 us for 1
+// row and 28.7 for 16 (tiles 27.3 and 27.3), at 4096 x 4096 8.3 for 1 and 13.5 for 32 (12.0, 13.1), and
+// for 4 rows at 256 x 7168 10.8 (10.3 with eight parts).
+// Else the shape and split with the least time by this model: the workgroups of one turn of
+// the CUs cost `start` us, and each block of 64 of their contraction `alone` us a turn or
+// `shared` us a workgroup of the busiest CU, whichever is more; the parts of a split cost a
+// launch and their bytes.  The figures are fitted, for the order of the choices and not for
+// their times, to every shape and split timed at 17 to 8192 rows, 256 to 8192 columns and
+// contractions of 512 to 14336, operands from memory, in all three directions: of those 480
+// products the choice is within 5 % of the fastest in 415 and within 20 % in 468 (of 480 with operands off the wide
+// path in 394 and 454); at worst it takes twice as long, at 17 x 1024 x 2048 (16 us with eight
+// parts where no split takes 9).
+struct TileRate {
+    Tile tile;
+    uint32_t tm, tn, at_once;
+    double start, alone, shared;
+};
+constexpr TileRate kDirectTiles[] = {
+    {kT128, 128, 128, 512, 0.2, 2.33, 0.975},    {kT128Deep, 128, 128, 256, 4.65, 0.88, 0.0},
+    {kT256x128, 256, 128, 256, 24.3, 0.96, 0.0}, {kT256, 256, 256, 256, 16.3, 1.38, 1.65},
+    {kT128x64, 128, 64, 256, 0.2, 0.0, 0.83},    {kT64, 64, 64, 512, 0.06, 0.13, 0.48}};
+constexpr TileRate kAnyTiles[] = {{kTAny, 128, 128, 512, 3.4, 0.0, 1.05}, {kTAny64, 64, 64, 1024, 0.0, 0.65, 0.44}};
+constexpr uint32_t kMostSplits = 8;
+constexpr double kJoinStart = 3.64, kJoinBytes = 0.66e6, kAnyJoinStart = 4.56, kAnyJoinBytes = 8.9e6;  // us; bytes a us
+
+static ProductChoice product_choice(uint64_t m, uint64_t n, uint64_t k, bool along, bool direct, uint32_t most_splits) {
+    ProductChoice c = {0, direct ? kT128 : kTAny, 1};
+    const uint64_t rows_tiles = ceil_div(n, 16) * ceil_div(m, 16);
+    if (along && rows_tiles < (1u << 22) && (m <= 16 || (m <= 32 && (!direct || n * k <= (1u << 24))))) {
         c.rows_mt = m <= 16 ? 1 : 2;
         return c;
     }
     const double blocks = (double)ceil_div(k, kPBlock);
-    const auto time = [](uint64_t t, uint64_t at_once, double us) { return (double)ceil_div(t, at_once) * us; };
-    const uint64_t t128 = ceil_div(m, 128) * ceil_div(n, 128);
-    const double per = direct ? 1.0 : 2.5;
-    double best = time(t128, 512, per * 1.1 * blocks + 4.0);
-    const auto offer = [&](Tile tile, uint32_t splits, double us) {
-        if (us < best) {
+    double best = 0.0;
+    const auto offer = [&](const TileRate &t, uint32_t splits) {
+        const uint64_t groups = ceil_div(m, t.tm) * ceil_div(n, t.tn) * splits;
+        const double turns = (double)ceil_div(groups, t.at_once), busiest = (double)ceil_div(groups, 256);
+        const double each = t.alone * turns > t.shared * busiest ? t.alone * turns : t.shared * busiest;
+        double us = t.start * turns + blocks / splits * each;
+        if (splits > 1)
+            us += (direct ? kJoinStart : kAnyJoinStart) + (double)(m * n * 4 * splits) / (direct ? kJoinBytes : kAnyJoinBytes);
+        if (best == 0.0 || us < best) {
             best = us;
-            c.tile = tile;
+            c.tile = t.tile;
             c.splits = splits;
         }
     };
-    if (direct) {
-        offer(kT256, 1, time(ceil_div(m, 256) * ceil_div(n, 256), 256, 1.3 * blocks + 9.0));
-        offer(kT256x128, 1, time(ceil_div(m, 256) * ceil_div(n, 128), 256, 0.85 * blocks + 6.0));
-        offer(kT128Deep, 1, time(t128, 256, 0.55 * blocks + 4.0));
-    } else {
-        c.tile = kTAny;
-    }
-    for (uint32_t s = 2; s <= 8; s *= 2) {
-        const uint64_t bytes = m * n * 4 * s;
-        if (bytes > ZC_MATMUL_WORKSPACE_MAX || blocks < 4 * s) break;
-        const double add = 4.0 + 2.0 * (double)bytes / 4.0e6;
+    for (uint32_t s = 1; s <= most_splits; s *= 2) {
+        if (s > 1 && (m * n > ZC_MATMUL_WORKSPACE_MAX / (4 * s) || blocks < 2 * s)) break;
         if (direct)
-            offer(kT128Deep, s, time(t128 * s, 256, 0.55 * blocks / s + 4.0) + add);
+            for (const TileRate &t : kDirectTiles) offer(t, s);
         else
-            offer(kTAny, s, time(t128 * s, 512, per * 1.1 * blocks / s + 4.0) + add);
+            for (const TileRate &t : kAnyTiles) offer(t, s);
     }
     return c;
 }
@@ -638,7 +875,10 @@ static void launch_tiles(const ProductArgs &p, Tile tile, dim3 grid, Launches &o
         case kT256x128: return on.launch((product_kernel<256, 128, 3, XA, XB, true>), grid, block, p);
         case kT128Deep: return on.launch((product_kernel<128, 128, 3, XA, XB, true>), grid, block, p);
         case kT128: return on.launch((product_kernel<128, 128, 2, XA, XB, true>), grid, block, p);
-        default: return on.launch((product_kernel<128, 128, 1, XA, XB, false>), grid, block, p);
+        case kT128x64: return on.launch((product_kernel<128, 64, 6, XA, XB, true>), grid, block, p);
+        case kT64: return on.launch((product_kernel<64, 64, 4, XA, XB, true>), grid, block, p);
+        case kTAny64: return on.launch((product_kernel<64, 64, 2, XA, XB, false>), grid, block, p);
+        default: return on.launch((product_kernel<128, 128, 2, XA, XB, false>), grid, block, p);
     }
 }
 
@@ -655,20 +895,25 @@ static zc_status launch_product(ProductArgs p, uint64_t m, uint64_t n, uint64_t 
     // a whole block may be loaded unless its last chunks pass the end of the operand
     p.direct = p.k / kPBlock;
     if (k % kPBlock == 0 && p.direct && ((xa && m % 8) || (xb && n % 8))) --p.direct;
-    ProductChoice c = product_choice(m, n, k, !xa && !xb, direct);
-    if (!ws || ws_bytes < zc_matmul_workspace_bytes(m, n, k)) c.splits = 1;
-    if (c.splits == 1 && !direct && !c.rows_mt) c.tile = kTAny;
-    const uint64_t tm = c.tile == kT256 || c.tile == kT256x128 ? 256 : 128, tn = c.tile == kT256 ? 256 : 128;
-    const uint64_t tiles = c.rows_mt ? ceil_div(m, 16 * c.rows_mt) * ceil_div(n, 16) : ceil_div(m, tm) * ceil_div(n, tn);
-    const uint32_t threads = c.rows_mt ? 512 : kPThreads;
-    if (tiles > 0xFFFFFFFFull / threads - 8) return ZC_ERR_INVALID_ARG;
+    if ((xa && p.lda < 8) || (xb && p.ldb < 8)) p.direct = 0;
+    const bool room = ws && ws_bytes >= zc_matmul_workspace_bytes(m, n, k);
+    const ProductChoice c = product_choice(m, n, k, !xa && !xb, direct, room ? kMostSplits : 1);
+    uint64_t tiles = c.rows_mt ? ceil_div(m, 16 * c.rows_mt) * ceil_div(n, 16) : 0;
+    if (!c.rows_mt) {
+        for (const TileRate &t : kDirectTiles)
+            if (t.tile == c.tile) tiles = ceil_div(m, t.tm) * ceil_div(n, t.tn);
+        for (const TileRate &t : kAnyTiles)
+            if (t.tile == c.tile) tiles = ceil_div(m, t.tm) * ceil_div(n, t.tn);
+    }
+    if (tiles > 0xFFFFFFFFull / kPThreads - 8) return ZC_ERR_INVALID_ARG;
     Launches on(stream);
     if (c.rows_mt) {
         const dim3 grid((uint32_t)tiles);
+        // (8 waves, 2, or turns of 2, 6 or 8 blocks took 1 to 1.2 times as long, loads marked for single use 1.3)
         if (c.rows_mt == 1)
-            on.launch((product_rows_kernel<1, 8, 4>), grid, dim3(512), p);
+            on.launch((product_rows_kernel<1, 4, 4>), grid, dim3(256), p);
         else
-            on.launch((product_rows_kernel<2, 8, 4>), grid, dim3(512), p);
+            on.launch((product_rows_kernel<2, 4, 4>), grid, dim3(256), p);
         return on.status();
     }
     if (c.splits > 1) p.parts = static_cast<float *>(ws);
@@ -722,7 +967,7 @@ extern "C" uint64_t zc_matmul_workspace_bytes(uint64_t rows, uint64_t cols, uint
     uint64_t most = 0;
     for (int along = 0; along < 2; ++along)
         for (int direct = 0; direct < 2; ++direct) {
-            const ProductChoice c = product_choice(rows, cols, contraction, along != 0, direct != 0);
+            const ProductChoice c = product_choice(rows, cols, contraction, along != 0, direct != 0, kMostSplits);
             if (c.splits > 1 && rows * cols * 4 * c.splits > most) most = rows * cols * 4 * c.splits;
         }
     return most;

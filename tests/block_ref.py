@@ -167,8 +167,10 @@ def activation_error(v, act):
     the value has not vanished); a slope is the sum of two terms whose sizes count."""
     value, _ = activation(v, act)
     grow = {0: 0, 1: 0, 2: np.abs(v), 3: v * v, 4: np.abs(v) + 0.08 * np.abs(v) ** 3, 5: np.abs(v)}[act]
-    # right of 0 the exponential is beside a 1
+    # right of 0 the exponential is beside a 1; not so in the sigmoid's slope, which is even: e^-|v| for large |v|, whose
+    # argument is rounded with its constant, in its product and, as the square of a root, twice over: 3 |v| half steps
     k = (16 + 4 * np.where(v > 0, 1, np.minimum(grow, 400))) * EPS32
+    ks = (16 + 4 * np.minimum(grow, 400)) * EPS32 if act == 5 else k
     size = {0: 1.0, 1: 1.0}.get(act)
     if size is None:
         s = np.abs(value) / np.maximum(np.abs(v), 1e-30) if act != 5 else value
@@ -177,7 +179,7 @@ def activation_error(v, act):
         size = near + np.where(v > 0, np.abs(v) * np.exp(-np.minimum(np.abs(v), 700)) * (1 + 0.3 * v * v) + 1.0, second)
         if act == 5:
             size = _sigmoid(-np.abs(v))
-    return k * np.abs(value) + 2.0 ** -125, k * size + 2.0 ** -125
+    return k * np.abs(value) + 2.0 ** -125, ks * size + 2.0 ** -125
 
 
 # -- balance ----------------------------------------------------------------------------------------------------------
