@@ -15,7 +15,7 @@ SOURCES = [os.path.join(CSRC, f) for f in ("zc_compress.hip", "zc_decode.hip", "
 # The mixture-of-experts operators (include/zc_moe.h): in the shipped library,
 # not in the codec's test and timeline builds.
 MOE_SOURCES = [os.path.join(CSRC, f) for f in ("zc_route.hip", "zc_exchange.hip", "zc_fp8.hip", "zc_matmul.hip",
-                                               "zc_swiglu.hip", "zc_norm.hip", "zc_balance.hip", "zc_product.hip")]
+                                               "zc_swiglu.hip", "zc_norm.hip", "zc_norm_backward.hip", "zc_balance.hip", "zc_product.hip")]
 ARCH = "gfx950"
 
 # Packed-FP32 instructions stay disabled for every HIP translation unit.

@@ -1,0 +1,507 @@
+// Gradients of the norms on both sides of a block, its gate and the residual sum,
+// MI355X / gfx950.  Bound by memory: every array is read once and written once, and
+// the sums over the rows are kept in registers.
+#include "zc_norm.h"
+
+namespace zc {
+namespace moe {
+
+// ---------------------------------------------------------------------------
+// any rows
+// ---------------------------------------------------------------------------
+
+// With v^ the normed value and u = dy * w the gradient there, that of v is
+//   1 / deviation * (u - v^ mean(u v^) [- mean(u) for LAYER]).
+// A team's lanes keep their columns from row to row, so the sums over the rows
+// stay in registers until the team's last row and leave as one part a team; a
+// second launch adds the parts in order.  BIAS: with the biases' sums.  Columns past
+// the end read as 0 and have a gradient of 0, so they add nothing.
+template <bool F32S, bool BIAS, uint32_t TEAM, uint32_t CHUNKS>
+__global__ __launch_bounds__(block_threads(TEAM)) void norm_backward_kernel(NormArgs a) {
+    __shared__ float parts[2][kMaxWaves][4];
+    Team<TEAM> team = {parts, 0};
+    const uint32_t sub = threadIdx.x % TEAM, index = blockIdx.x * block_teams(TEAM) + threadIdx.x / TEAM;
+    uint32_t n[CHUNKS];
+    float dw1[CHUNKS][8], dgate[CHUNKS][8], dw2[CHUNKS][8], db1[BIAS ? CHUNKS : 1][8], db2[BIAS ? CHUNKS : 1][8];
+#pragma unroll
+    for (uint32_t i = 0; i < CHUNKS; ++i) {
+        const uint32_t c = (i * TEAM + sub) * 8;
+        n[i] = c < a.cols ? min(a.cols - c, 8u) : 0u;
+#pragma unroll
+        for (uint32_t j = 0; j < 8; ++j) {
+            dw1[i][j] = dgate[i][j] = dw2[i][j] = 0.0f;
+            if (BIAS) db1[BIAS ? i : 0][j] = db2[BIAS ? i : 0][j] = 0.0f;
+        }
+    }
+    const bool pre = a.before.kind != ZC_NORM_NONE, post = a.after.kind != ZC_NORM_NONE;
+    for (uint64_t row = index; row < a.rows; row += (uint64_t)gridDim.x * block_teams(TEAM)) {
+        Eight<F32S> x[CHUNKS], dr[CHUNKS];
+        Eight<false> dy[CHUNKS], z[CHUNKS];
+#pragma unroll
+        for (uint32_t i = 0; i < CHUNKS; ++i) {
+            const uint32_t c = (i * TEAM + sub) * 8;
+            if (a.dy && pre) x[i].load(a.x, row * a.x_stride + c, n[i], true);
+            dr[i].clear();
+            dy[i].clear();
+            if (a.dy) dy[i].load(a.dy, row * a.dy_stride + c, n[i], true);
+            if (a.dr) dr[i].load(a.dr, row * a.dr_stride + c, n[i], true);
+            if (a.z) z[i].load(a.z, row * a.z_stride + c, n[i], true);
+        }
+        float g[CHUNKS][8];  // the gradient of r
+        if (a.dy && pre) {
+            const Stat s = row_stat<TEAM, CHUNKS>(x, n, a.before.kind, a.before.eps, a.inv_cols, team);
+            float t[2] = {0.0f, 0.0f};
+#pragma unroll
+            for (uint32_t i = 0; i < CHUNKS; ++i) {
+                float w[8];
+                load_param(a.before.w, (i * TEAM + sub) * 8, n[i], 1.0f, w);
+#pragma unroll
+                for (uint32_t j = 0; j < 8; ++j) {
+                    const float v = normed(x[i][j], s);
+                    dw2[i][j] = fmaf(dy[i][j], v, dw2[i][j]);
+                    if (BIAS) db2[BIAS ? i : 0][j] += dy[i][j];
+                    g[i][j] = dy[i][j] * w[j];
+                    t[0] = fmaf(g[i][j], v, t[0]);
+                    t[1] += g[i][j];
+                }
+            }
+            team.sum(t);
+            const float m0 = t[0] * a.inv_cols, m1 = a.before.kind == ZC_NORM_LAYER ? t[1] * a.inv_cols : 0.0f;
+#pragma unroll
+            for (uint32_t i = 0; i < CHUNKS; ++i)
+#pragma unroll
+                for (uint32_t j = 0; j < 8; ++j)
+                    g[i][j] = fmaf((fmaf(-normed(x[i][j], s), m0, g[i][j]) - m1) * s.rs, s.unit, dr[i][j]);
+        } else {
+#pragma unroll
+            for (uint32_t i = 0; i < CHUNKS; ++i)
+#pragma unroll
+                for (uint32_t j = 0; j < 8; ++j) g[i][j] = dr[i][j] + dy[i][j];
+        }
+        if (a.r)
+#pragma unroll
+            for (uint32_t i = 0; i < CHUNKS; ++i)
+                store_stream<F32S>(a.r, row * a.r_stride + (i * TEAM + sub) * 8, n[i], g[i], a.wide);
+        if (!a.z) {
+            if (a.drow_gate && sub == 0) a.drow_gate[row] = 0.0f;
+            continue;
+        }
+        const float rg = a.row_gate ? a.row_gate[row] : 1.0f;
+        Stat s = {0.0f, 0.0f, 1.0f, 1.0f};
+        if (post) s = row_stat<TEAM, CHUNKS>(z, n, a.after.kind, a.after.eps, a.inv_cols, team);
+        float t[3] = {0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (uint32_t i = 0; i < CHUNKS; ++i) {
+            const uint32_t c = (i * TEAM + sub) * 8;
+            float gate[8], w[8], h[8];
+#pragma unroll
+            for (uint32_t j = 0; j < 8; ++j) {
+                g[i][j] = c + j < a.cols ? a.scale * g[i][j] : 0.0f;  // at gate * row_gate * h
+                h[j] = z[i][j];
+                w[j] = 1.0f;
+            }
+            if (post) {
+                load_param(a.after.w, c, n[i], 1.0f, w);
+#pragma unroll
+                for (uint32_t j = 0; j < 8; ++j) h[j] = normed(h[j], s) * w[j];
+                if (a.after.b.p) {
+                    float b[8];
+                    load_param(a.after.b, c, n[i], 0.0f, b);
+#pragma unroll
+                    for (uint32_t j = 0; j < 8; ++j) h[j] += b[j];
+                }
+            }
+            load_param(a.gate, c, n[i], 1.0f, gate);
+#pragma unroll
+            for (uint32_t j = 0; j < 8; ++j) {
+                dgate[i][j] = fmaf(rg * g[i][j], h[j], dgate[i][j]);
+                t[0] = fmaf(gate[j] * g[i][j], h[j], t[0]);
+                const float dh = rg * gate[j] * g[i][j], v = normed(z[i][j], s);
+                dw1[i][j] = fmaf(dh, v, dw1[i][j]);
+                if (BIAS) db1[BIAS ? i : 0][j] += dh;
+                g[i][j] = dh * w[j];
+                t[1] = fmaf(g[i][j], v, t[1]);
+                t[2] += g[i][j];
+            }
+        }
+        if (a.drow_gate || (post && a.dz)) team.sum(t);
+        if (a.drow_gate && sub == 0) a.drow_gate[row] = t[0];
+        if (!a.dz) continue;
+        const float m0 = t[1] * a.inv_cols, m1 = a.after.kind == ZC_NORM_LAYER ? t[2] * a.inv_cols : 0.0f;
+#pragma unroll
+        for (uint32_t i = 0; i < CHUNKS; ++i) {
+            if (post)
+#pragma unroll
+                for (uint32_t j = 0; j < 8; ++j)
+                    g[i][j] = (fmaf(-normed(z[i][j], s), m0, g[i][j]) - m1) * s.rs * s.unit;
+            store_bf(a.dz + row * a.dz_stride + (i * TEAM + sub) * 8, pack8(g[i]), n[i], a.wide);
+        }
+    }
+#pragma unroll
+    for (uint32_t i = 0; i < CHUNKS; ++i) {
+        const auto leave = [&](uint32_t sum, const float (&v)[8]) {
+            if (a.sums >> sum & 1)
+                store_floats(a.parts + sum * a.part_stride + (uint64_t)index * a.cols + (i * TEAM + sub) * 8, n[i], v);
+        };
+        leave(kDW1, dw1[i]);
+        leave(kDGate, dgate[i]);
+        leave(kDW2, dw2[i]);
+        if (BIAS) {
+            leave(kDB1, db1[BIAS ? i : 0]);
+            leave(kDB2, db2[BIAS ? i : 0]);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// whole rows
+// ---------------------------------------------------------------------------
+
+// Both halves' statistics at once: x before the norm `before`, z before the norm `after`.
+template <uint32_t TEAM, uint32_t CHUNKS, typename X, typename Z>
+__device__ __forceinline__ void both_stats(const X &x, const Z &z, const uint32_t (&n)[CHUNKS], const NormArgs &a, bool pre,
+                                           bool post, Stat &sx, Stat &sz, Team<TEAM> &team) {
+    sx = sz = {0.0f, 0.0f, 1.0f, 1.0f};
+    const bool lx = pre && a.before.kind == ZC_NORM_LAYER, lz = post && a.after.kind == ZC_NORM_LAYER;
+    float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (lx || lz) {
+        float u[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (uint32_t i = 0; i < CHUNKS; ++i)
+#pragma unroll
+            for (uint32_t j = 0; j < 8; ++j) {
+                u[0] += x[i][j];
+                u[1] += z[i][j];
+            }
+        team.sum(u);
+        sx.mean = lx ? u[0] * a.inv_cols : 0.0f;
+        sz.mean = lz ? u[1] * a.inv_cols : 0.0f;
+#pragma unroll
+        for (uint32_t i = 0; i < CHUNKS; ++i)
+#pragma unroll
+            for (uint32_t j = 0; j < 8; ++j) {
+                const float dx = n[i] ? x[i][j] - sx.mean : 0.0f, dz = n[i] ? z[i][j] - sz.mean : 0.0f;
+                t[0] = fmaf(dx, dx, t[0]);
+                t[1] = fmaf(dz, dz, t[1]);
+                t[2] += dx;
+                t[3] += dz;
+            }
+        team.sum(t);
+        if (lx) {
+            sx.rest = t[2] * a.inv_cols;
+            const float left = fmaf(-sx.rest, t[2], t[0]);
+            t[0] = left < 0.0f ? 0.0f : left;
+        }
+        if (lz) {
+            sz.rest = t[3] * a.inv_cols;
+            const float left = fmaf(-sz.rest, t[3], t[1]);
+            t[1] = left < 0.0f ? 0.0f : left;
+        }
+    } else {
+        float u[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (uint32_t i = 0; i < CHUNKS; ++i)
+#pragma unroll
+            for (uint32_t j = 0; j < 8; ++j) {
+                u[0] = fmaf(x[i][j], x[i][j], u[0]);
+                u[1] = fmaf(z[i][j], z[i][j], u[1]);
+            }
+        team.sum(u);
+        t[0] = u[0];
+        t[1] = u[1];
+    }
+    sx.rs = __builtin_amdgcn_rsqf(fmaf(t[0], a.inv_cols, a.before.eps));
+    sz.rs = __builtin_amdgcn_rsqf(fmaf(t[1], a.inv_cols, a.after.eps));
+    // squares outside the range of a float: one row at a time
+    if (pre && (!(t[0] <= 0x1p120f) || (t[0] < 0x1p-80f && a.before.eps < 0x1p-58f)))
+        sx = row_stat<TEAM, CHUNKS>(x, n, a.before.kind, a.before.eps, a.inv_cols, team);
+    if (post && (!(t[1] <= 0x1p120f) || (t[1] < 0x1p-80f && a.after.eps < 0x1p-58f)))
+        sz = row_stat<TEAM, CHUNKS>(z, n, a.after.kind, a.after.eps, a.inv_cols, team);
+}
+
+// As the kernel above, with the next row's loads on their way while a row is worked on, weights and gate in
+// registers, and no branch around a load or store.
+template <bool F32S, bool F32P, bool BIAS, uint32_t TEAM, uint32_t CHUNKS>
+__global__ __launch_bounds__(block_threads(TEAM)) void norm_backward_whole_kernel(NormArgs a) {
+    __shared__ float parts[2][kMaxWaves][4];
+    Team<TEAM> team = {parts, 0};
+    const uint32_t sub = threadIdx.x % TEAM;
+    const uint32_t index = (uint32_t)__builtin_amdgcn_readfirstlane(blockIdx.x * block_teams(TEAM) + threadIdx.x / TEAM);
+    uint32_t n[CHUNKS];
+    float dw1[CHUNKS][8], dgate[CHUNKS][8], dw2[CHUNKS][8], db1[BIAS ? CHUNKS : 1][8], db2[BIAS ? CHUNKS : 1][8];
+    Eight<F32P> w1[CHUNKS], gate[CHUNKS], w2[CHUNKS];
+    const bool pre = a.dy && a.before.kind != ZC_NORM_NONE, post = a.z && a.after.kind != ZC_NORM_NONE;
+#pragma unroll
+    for (uint32_t i = 0; i < CHUNKS; ++i) {
+        const uint32_t c = (i * TEAM + sub) * 8;
+        n[i] = c < a.cols ? 8u : 0u;
+        keep_param<F32P>(post ? a.after.w : Param{}, c, n[i], 1.0f, w1[i]);
+        keep_param<F32P>(a.z ? a.gate : Param{}, c, n[i], 1.0f, gate[i]);
+        keep_param<F32P>(pre ? a.before.w : Param{}, c, n[i], 1.0f, w2[i]);
+#pragma unroll
+        for (uint32_t j = 0; j < 8; ++j) {
+            dw1[i][j] = dgate[i][j] = dw2[i][j] = 0.0f;
+            if (BIAS) db1[BIAS ? i : 0][j] = db2[BIAS ? i : 0][j] = 0.0f;
+        }
+    }
+    struct Loaded {
+        Eight<F32S> x[CHUNKS], dr[CHUNKS];
+        Eight<false> z[CHUNKS], dy[CHUNKS];
+    };
+    const auto fetch = [&](uint32_t t, Loaded &v) {
+        const Row rx = row_of(a.x, t * a.x_stride, a.cols, F32S ? 4 : 2), rz = row_of(a.z, t * a.z_stride, a.cols, 2);
+        const Row rd = row_of(a.dr, t * a.dr_stride, a.cols, F32S ? 4 : 2), ry = row_of(a.dy, t * a.dy_stride, a.cols, 2);
+#pragma unroll
+        for (uint32_t i = 0; i < CHUNKS; ++i) {
+            const uint32_t c = (i * TEAM + sub) * 8;
+            load_row<F32S>(rx, c, v.x[i]);
+            load_row<false>(rz, c, v.z[i]);
+            load_row<false>(ry, c, v.dy[i]);
+            load_row<F32S>(rd, c, v.dr[i]);
+        }
+    };
+    const uint32_t step = gridDim.x * block_teams(TEAM);
+    uint32_t row = index;
+    Loaded v;
+    if (row < a.rows) fetch(row, v);
+    while (row < a.rows) {
+        Loaded next;
+        fetch(row + step < a.rows ? row + step : a.rows - 1, next);
+#pragma unroll
+        for (uint32_t i = 0; i < CHUNKS; ++i) {
+            stay_packed(w1[i]);
+            stay_packed(gate[i]);
+            stay_packed(w2[i]);
+        }
+        const float rg = a.row_gate ? a.row_gate[row] : 1.0f;
+        Stat sx, sz;
+        if (pre || post) both_stats<TEAM, CHUNKS>(v.x, v.z, n, a, pre, post, sx, sz, team);
+#pragma unroll
+        for (uint32_t i = 0; i < CHUNKS; ++i) {
+            stay_packed(v.x[i]);
+            stay_packed(v.z[i]);
+            stay_packed(v.dy[i]);
+            stay_packed(v.dr[i]);
+        }
+        float g[CHUNKS][8];  // the gradient of r
+        if (pre) {
+            float t[2] = {0.0f, 0.0f};
+#pragma unroll
+            for (uint32_t i = 0; i < CHUNKS; ++i)
+#pragma unroll
+                for (uint32_t j = 0; j < 8; ++j) {
+                    const float h = normed(v.x[i][j], sx), d = v.dy[i][j];
+                    dw2[i][j] = fmaf(d, h, dw2[i][j]);
+                    if (BIAS) db2[BIAS ? i : 0][j] += d;
+                    g[i][j] = d * w2[i][j];
+                    t[0] = fmaf(g[i][j], h, t[0]);
+                    t[1] += g[i][j];
+                }
+            team.sum(t);
+            const float m0 = t[0] * a.inv_cols, m1 = a.before.kind == ZC_NORM_LAYER ? t[1] * a.inv_cols : 0.0f;
+#pragma unroll
+            for (uint32_t i = 0; i < CHUNKS; ++i) stay_packed(v.x[i]);
+#pragma unroll
+            for (uint32_t i = 0; i < CHUNKS; ++i)
+#pragma unroll
+                for (uint32_t j = 0; j < 8; ++j)
+                    g[i][j] = fmaf((fmaf(-normed(v.x[i][j], sx), m0, g[i][j]) - m1) * sx.rs, sx.unit, v.dr[i][j]);
+        } else {
+#pragma unroll
+            for (uint32_t i = 0; i < CHUNKS; ++i)
+#pragma unroll
+                for (uint32_t j = 0; j < 8; ++j) g[i][j] = v.dr[i][j] + v.dy[i][j];
+        }
+        const Row rr = row_of(a.r, row * a.r_stride, a.cols, F32S ? 4 : 2);
+#pragma unroll
+        for (uint32_t i = 0; i < CHUNKS; ++i) store_row<F32S>(rr, (i * TEAM + sub) * 8, g[i]);
+        float t[3] = {0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (uint32_t i = 0; i < CHUNKS; ++i) {
+            float b[8];
+            if (post && a.after.b.p) load_param(a.after.b, (i * TEAM + sub) * 8, n[i], 0.0f, b);
+#pragma unroll
+            for (uint32_t j = 0; j < 8; ++j) {
+                const float h0 = v.z[i][j], zh = post ? normed(h0, sz) : h0;
+                const float h = post && a.after.b.p ? fmaf(zh, w1[i][j], b[j]) : zh * w1[i][j];
+                const float e = n[i] ? a.scale * g[i][j] : 0.0f, ge = gate[i][j] * e;
+                dgate[i][j] = fmaf(rg * e, h, dgate[i][j]);
+                t[0] = fmaf(ge, h, t[0]);
+                const float dh = rg * ge;
+                dw1[i][j] = fmaf(dh, zh, dw1[i][j]);
+                if (BIAS) db1[BIAS ? i : 0][j] += dh;
+                g[i][j] = dh * w1[i][j];
+                t[1] = fmaf(g[i][j], zh, t[1]);
+                t[2] += g[i][j];
+            }
+        }
+        if (a.drow_gate || post) team.sum(t);
+        if (a.drow_gate && sub == 0) a.drow_gate[row] = t[0];
+        const float m0 = t[1] * a.inv_cols, m1 = a.after.kind == ZC_NORM_LAYER ? t[2] * a.inv_cols : 0.0f;
+        const Row rz = row_of(a.dz, row * a.dz_stride, a.cols, 2);
+#pragma unroll
+        for (uint32_t i = 0; i < CHUNKS; ++i) {
+            stay_packed(v.z[i]);
+            if (post)
+#pragma unroll
+                for (uint32_t j = 0; j < 8; ++j)
+                    g[i][j] = (fmaf(-normed(v.z[i][j], sz), m0, g[i][j]) - m1) * sz.rs * sz.unit;
+            store_row<false>(rz, (i * TEAM + sub) * 8, g[i]);
+        }
+        row += step;
+        v = next;
+    }
+#pragma unroll
+    for (uint32_t i = 0; i < CHUNKS; ++i) {
+        const auto leave = [&](uint32_t sum, const float (&s)[8]) {
+            if (a.sums >> sum & 1)
+                store_floats(a.parts + sum * a.part_stride + (uint64_t)index * a.cols + (i * TEAM + sub) * 8, n[i], s);
+        };
+        leave(kDW1, dw1[i]);
+        leave(kDGate, dgate[i]);
+        leave(kDW2, dw2[i]);
+        if (BIAS) {
+            leave(kDB1, db1[BIAS ? i : 0]);
+            leave(kDB2, db2[BIAS ? i : 0]);
+        }
+    }
+}
+
+// The parts of the sums over the rows, added in order: 64 columns a block, their
+// parts cut into 16 runs.
+struct SumArgs {
+    const float *parts;
+    float *out[kSums];
+    uint64_t part_stride;
+    uint32_t count, cols, live;  // live: sums that have parts; the others are zeros
+};
+constexpr uint32_t kSumRuns = 16;
+__global__ __launch_bounds__(kLanes * kSumRuns) void norm_sums_kernel(SumArgs a) {
+    __shared__ float run[kSumRuns][kLanes];
+    float *out = a.out[blockIdx.y];
+    if (!out) return;
+    const uint32_t c = blockIdx.x * kLanes + lane_id(), w = threadIdx.x / kLanes;
+    float v = 0.0f;
+    if (c < a.cols && (a.live >> blockIdx.y & 1)) {
+        const uint32_t i0 = (uint32_t)((uint64_t)a.count * w / kSumRuns), i1 = (uint32_t)((uint64_t)a.count * (w + 1) / kSumRuns);
+        const float *src = a.parts + blockIdx.y * a.part_stride + (uint64_t)i0 * a.cols + c;
+#pragma unroll 8
+        for (uint32_t i = i0; i < i1; ++i, src += a.cols) v += *src;
+    }
+    run[w][lane_id()] = v;
+    __syncthreads();
+    if (w || c >= a.cols) return;
+#pragma unroll
+    for (uint32_t i = 1; i < kSumRuns; ++i) v += run[i][lane_id()];
+    out[c] = v;
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+
+static void launch_backward(const NormArgs &a, const Shape &s, bool whole, bool f32, bool f32p, bool bias, dim3 grid,
+                            Launches &on) {
+    with_shape(s, [&](auto team, auto chunks) {
+        constexpr uint32_t T = decltype(team)::value, C = decltype(chunks)::value;
+        const auto pick = [&](auto f32_t, auto bias_t) {
+            constexpr bool S = decltype(f32_t)::value, B = decltype(bias_t)::value;
+            on.launch(!whole ? norm_backward_kernel<S, B, T, C>
+                      : f32p ? norm_backward_whole_kernel<S, true, B, T, C>
+                             : norm_backward_whole_kernel<S, false, B, T, C>,
+                      grid, dim3(block_threads(T)), a);
+        };
+        if (f32)
+            bias ? pick(std::true_type{}, std::true_type{}) : pick(std::true_type{}, std::false_type{});
+        else
+            bias ? pick(std::false_type{}, std::true_type{}) : pick(std::false_type{}, std::false_type{});
+    });
+}
+
+}  // namespace moe
+}  // namespace zc
+
+using namespace zc::moe;
+
+extern "C" uint64_t zc_norm_backward_workspace_bytes(uint64_t rows, uint64_t cols) {
+    if (rows > kMaxRows || cols > ZC_NORM_MAX_COLS || !rows || !cols) return 0;
+    const Shape s = shape_of(cols);
+    return ceil_div(backward_blocks(rows, s) * block_teams(s.team) * cols * kSums * 4, 256) * 256;
+}
+
+extern "C" zc_status zc_norm_backward(const void *d_r, uint32_t stream_type, uint64_t rows, uint64_t cols,
+                                      uint64_t r_stride, const void *d_z, uint64_t z_stride,
+                                      const zc_norm_config *cfg, const void *d_dr, uint64_t dr_stride,
+                                      const void *d_dy, uint64_t dy_stride, void *d_dx, uint64_t dx_stride,
+                                      void *d_dz, uint64_t dz_stride, const zc_norm_grads *grads, void *d_workspace,
+                                      uint64_t workspace_bytes, void *stream) {
+    const zc_status bad = check(cfg, stream_type, rows, cols, d_z != nullptr);
+    if (bad == ZC_ERR_INVALID_ARG || r_stride < cols || r_stride > kMaxStride || !stride_ok(d_z, z_stride, cols) ||
+        !stride_ok(d_dr, dr_stride, cols) || !stride_ok(d_dy, dy_stride, cols) || !stride_ok(d_dx, dx_stride, cols) ||
+        !stride_ok(d_dz, dz_stride, cols) || (d_dz && !d_z))
+        return ZC_ERR_INVALID_ARG;
+    if (bad) return bad;
+    if (!cols) return ZC_OK;
+    SumArgs sum = {};
+    float *const row_gate = grads ? grads->d_row_gate : nullptr;
+    if (grads) {
+        sum.out[kDW1] = grads->d_weight_after;
+        sum.out[kDB1] = grads->d_bias_after;
+        sum.out[kDGate] = grads->d_gate;
+        sum.out[kDW2] = grads->d_weight_before;
+        sum.out[kDB2] = grads->d_bias_before;
+    }
+    uint32_t asked = 0;
+    for (uint32_t k = 0; k < kSums; ++k) {
+        if (!aligned(sum.out[k], 4)) return ZC_ERR_MISALIGNED;
+        asked |= (uint32_t)(sum.out[k] != nullptr) << k;
+    }
+    if (!asked && (!rows || (!d_dx && !d_dz && !row_gate))) return ZC_OK;
+    const uint32_t size = stream_type == ZC_F32 ? 4 : 2;
+    if (!aligned(d_r, size) || !aligned(d_z, 2) || !aligned(d_dr, size) || !aligned(d_dy, 2) || !aligned(d_dx, size) ||
+        !aligned(d_dz, 2) || !aligned(row_gate, 4) || !aligned(d_workspace, 16))
+        return ZC_ERR_MISALIGNED;
+    NormArgs a = common(*cfg, rows, cols);
+    a.x = d_r;
+    a.z = static_cast<const uint16_t *>(d_z);
+    a.dr = d_dr;
+    a.dy = static_cast<const uint16_t *>(d_dy);
+    a.r = d_dx;
+    a.dz = static_cast<uint16_t *>(d_dz);
+    a.drow_gate = row_gate;
+    a.x_stride = r_stride;
+    a.z_stride = z_stride;
+    a.dr_stride = dr_stride;
+    a.dy_stride = dy_stride;
+    a.r_stride = dx_stride;
+    a.dz_stride = dz_stride;
+    // which sums have anything to add: the rest are zeros
+    uint32_t live = 0;
+    if (d_z) live |= 1u << kDGate | (a.after.kind != ZC_NORM_NONE ? 1u << kDW1 | 1u << kDB1 : 0u);
+    if (d_dy && a.before.kind != ZC_NORM_NONE) live |= 1u << kDW2 | 1u << kDB2;
+    if (!rows) live = 0;
+    a.sums = asked & live;
+    const Shape s = shape_of(cols);
+    const uint64_t blocks = rows ? backward_blocks(rows, s) : 0, count = blocks * block_teams(s.team);
+    a.part_stride = sum.part_stride = count * cols;
+    sum.count = (uint32_t)count;
+    sum.cols = (uint32_t)cols;
+    sum.live = a.sums;
+    if (rows && !d_r) return ZC_ERR_INVALID_ARG;
+    if (a.sums) {
+        if (!d_workspace) return ZC_ERR_INVALID_ARG;
+        if (workspace_bytes < zc_norm_backward_workspace_bytes(rows, cols)) return ZC_ERR_CAPACITY;
+        a.parts = static_cast<float *>(d_workspace);
+        sum.parts = a.parts;
+    }
+    const bool f32 = stream_type == ZC_F32;
+    a.wide = cols % 8 == 0 && wide8(d_dx, dx_stride, f32) && wide8(d_dz, dz_stride);
+    const bool whole = a.wide && wide8(d_r, r_stride, f32) && wide8(d_dr, dr_stride, f32) && wide8(d_dy, dy_stride) &&
+                       wide8(d_z, z_stride);
+    Launches on(stream);
+    if (rows && (a.sums || d_dx || d_dz || row_gate))
+        launch_backward(a, s, whole, f32, any_float(*cfg, d_z != nullptr), a.sums & (1u << kDB1 | 1u << kDB2),
+                        dim3((uint32_t)blocks), on);
+    if (asked) on.launch(norm_sums_kernel, dim3((uint32_t)ceil_div(cols, kLanes), kSums), dim3(kLanes * kSumRuns), sum);
+    return on.status();
+}
