@@ -109,45 +109,48 @@ struct Team {
     }
 };
 
-// The normed value of v is (v * unit - mean - rest) * rs; rest is what rounding
-// the mean left of it, which counts where the deviation is small beside the mean.
-// unit is 1 unless the squares
-// would leave the range of a float: above 2^120 in sum (infinities and NaN among
-// them), or below 2^-80 with an eps that does not cover them; the row is then
-// taken 2^-80 or 2^80 times as large, which is exact for all values that matter.
+// The normed value of v is (v - mean) * k - off: k is 1 / deviation, and off what rounding the
+// mean left of it, which counts where the deviation is small beside the mean.  Where the
+// squares would leave the range of a float (above 2^120 in sum, infinities and NaN among
+// them, or below 2^-80 with an eps that does not cover them), the row is measured
+// 2^-80 or 2^80 times as large, which is exact for all values that matter.
 struct Stat {
-    float mean, rest, rs, unit;
+    float mean, off, k;
 };
-__device__ __forceinline__ float normed(float v, const Stat &s) { return (fmaf(v, s.unit, -s.mean) - s.rest) * s.rs; }
+// MEAN: there may be a mean.
+template <bool MEAN = true>
+__device__ __forceinline__ float normed(float v, const Stat &s) {
+    return MEAN ? fmaf(v - s.mean, s.k, -s.off) : v * s.k;
+}
 
 template <uint32_t TEAM, uint32_t CHUNKS, typename V>
 __device__ __forceinline__ Stat row_stat(const V &v, const uint32_t (&n)[CHUNKS], uint32_t kind, float eps,
                                          float inv_cols, Team<TEAM> &team) {
-    Stat s = {0.0f, 0.0f, 1.0f, 1.0f};
+    float mean = 0.0f, rest = 0.0f, unit = 1.0f;
     float var = 0.0f;
     const auto measure = [&]() {
-        s.mean = s.rest = 0.0f;
+        mean = rest = 0.0f;
         if (kind == ZC_NORM_LAYER) {
             float t[1] = {0.0f};
 #pragma unroll
             for (uint32_t i = 0; i < CHUNKS; ++i)
 #pragma unroll
-                for (uint32_t j = 0; j < 8; ++j) t[0] = fmaf(v[i][j], s.unit, t[0]);
+                for (uint32_t j = 0; j < 8; ++j) t[0] = fmaf(v[i][j], unit, t[0]);
             team.sum(t);
-            s.mean = t[0] * inv_cols;
+            mean = t[0] * inv_cols;
             float u[2] = {0.0f, 0.0f};
 #pragma unroll
             for (uint32_t i = 0; i < CHUNKS; ++i)
 #pragma unroll
                 for (uint32_t j = 0; j < 8; ++j) {
-                    const float d = j < n[i] ? fmaf(v[i][j], s.unit, -s.mean) : 0.0f;
+                    const float d = j < n[i] ? fmaf(v[i][j], unit, -mean) : 0.0f;
                     u[0] = fmaf(d, d, u[0]);
                     u[1] += d;
                 }
             team.sum(u);
-            s.rest = u[1] * inv_cols;
+            rest = u[1] * inv_cols;
             // (where the difference is lost in rounding: not below 0, and NaN stays)
-            const float left = fmaf(-s.rest, u[1], u[0]);
+            const float left = fmaf(-rest, u[1], u[0]);
             var = left < 0.0f ? 0.0f : left;
         } else {
             float t[1] = {0.0f};
@@ -155,7 +158,7 @@ __device__ __forceinline__ Stat row_stat(const V &v, const uint32_t (&n)[CHUNKS]
             for (uint32_t i = 0; i < CHUNKS; ++i)
 #pragma unroll
                 for (uint32_t j = 0; j < 8; ++j) {
-                    const float d = v[i][j] * s.unit;
+                    const float d = v[i][j] * unit;
                     t[0] = fmaf(d, d, t[0]);
                 }
             team.sum(t);
@@ -164,12 +167,12 @@ __device__ __forceinline__ Stat row_stat(const V &v, const uint32_t (&n)[CHUNKS]
     };
     measure();
     if (!(var <= 0x1p120f) || (var < 0x1p-80f && eps < 0x1p-58f)) {
-        s.unit = var < 1.0f ? 0x1p80f : 0x1p-80f;
+        unit = var < 1.0f ? 0x1p80f : 0x1p-80f;
         measure();
     }
     // eps in the row's unit (for large rows it is nothing beside their squares)
-    s.rs = __builtin_amdgcn_rsqf(fmaf(var, inv_cols, eps * s.unit * s.unit));
-    return s;
+    const float rs = __builtin_amdgcn_rsqf(fmaf(var, inv_cols, eps * unit * unit));
+    return {mean / unit, rest * rs, rs * unit};
 }
 
 // ---------------------------------------------------------------------------
@@ -300,15 +303,17 @@ inline zc_status check(const zc_norm_config *cfg, uint32_t stream_type, uint64_t
     return ZC_OK;
 }
 
-inline NormArgs common(const zc_norm_config &cfg, uint64_t rows, uint64_t cols) {
+inline NormArgs common(const zc_norm_config &cfg, uint64_t rows, uint64_t cols, bool branch) {
     NormArgs a = {};
-    a.after = side(cfg.after);
     a.before = side(cfg.before);
-    a.gate = {cfg.d_gate, cfg.gate_type == ZC_F32};
-    a.row_gate = cfg.d_row_gate;
+    if (branch) {
+        a.after = side(cfg.after);
+        a.gate = {cfg.d_gate, cfg.gate_type == ZC_F32};
+        a.row_gate = cfg.d_row_gate;
+        a.scale = cfg.scale;
+    }
     a.rows = (uint32_t)rows;
     a.cols = (uint32_t)cols;
-    a.scale = cfg.scale;
     a.inv_cols = 1.0f / (float)cols;
     return a;
 }

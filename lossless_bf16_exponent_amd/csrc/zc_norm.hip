@@ -34,7 +34,7 @@ __global__ __launch_bounds__(block_threads(TEAM)) void norm_kernel(NormArgs a) {
             for (uint32_t i = 0; i < CHUNKS; ++i) z[i].load(a.z, row * a.z_stride + (i * TEAM + sub) * 8, n[i], true);
             const float share = a.row_gate ? a.scale * a.row_gate[row] : a.scale;
             const bool on = a.after.kind != ZC_NORM_NONE;
-            Stat s = {0.0f, 0.0f, 1.0f, 1.0f};
+            Stat s = {0.0f, 0.0f, 1.0f};
             if (on) s = row_stat<TEAM, CHUNKS>(z, n, a.after.kind, a.after.eps, a.inv_cols, team);
 #pragma unroll
             for (uint32_t i = 0; i < CHUNKS; ++i) {
@@ -153,7 +153,7 @@ __global__ __launch_bounds__(block_threads(TEAM), whole_waves(TEAM)) void norm_w
         }
         float v[CHUNKS][8];
         const float share = a.row_gate ? a.scale * a.row_gate[row] : a.scale;
-        Stat s = {0.0f, 0.0f, 1.0f, 1.0f};
+        Stat s = {0.0f, 0.0f, 1.0f};
         if (post) s = row_stat<TEAM, CHUNKS>(z, n, a.after.kind, a.after.eps, a.inv_cols, team);
 #pragma unroll
         for (uint32_t i = 0; i < CHUNKS; ++i) {
@@ -259,7 +259,7 @@ extern "C" zc_status zc_norm(const void *d_x, uint32_t stream_type, uint64_t row
     if (!aligned(d_x, size) || !aligned(d_z, 2) || !aligned(d_r, size) || !aligned(d_y, 2) || !aligned(d_yq, 16) ||
         !aligned(d_yq_scales, 4))
         return ZC_ERR_MISALIGNED;
-    NormArgs a = common(*cfg, rows, cols);
+    NormArgs a = common(*cfg, rows, cols, d_z != nullptr);
     a.x = d_x;
     a.z = static_cast<const uint16_t *>(d_z);
     a.r = d_r;

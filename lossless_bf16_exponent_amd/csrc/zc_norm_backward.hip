@@ -71,7 +71,7 @@ __global__ __launch_bounds__(block_threads(TEAM)) void norm_backward_kernel(Norm
             for (uint32_t i = 0; i < CHUNKS; ++i)
 #pragma unroll
                 for (uint32_t j = 0; j < 8; ++j)
-                    g[i][j] = fmaf((fmaf(-normed(x[i][j], s), m0, g[i][j]) - m1) * s.rs, s.unit, dr[i][j]);
+                    g[i][j] = fmaf(fmaf(-normed(x[i][j], s), m0, g[i][j]) - m1, s.k, dr[i][j]);
         } else {
 #pragma unroll
             for (uint32_t i = 0; i < CHUNKS; ++i)
@@ -87,7 +87,7 @@ __global__ __launch_bounds__(block_threads(TEAM)) void norm_backward_kernel(Norm
             continue;
         }
         const float rg = a.row_gate ? a.row_gate[row] : 1.0f;
-        Stat s = {0.0f, 0.0f, 1.0f, 1.0f};
+        Stat s = {0.0f, 0.0f, 1.0f};
         if (post) s = row_stat<TEAM, CHUNKS>(z, n, a.after.kind, a.after.eps, a.inv_cols, team);
         float t[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -133,7 +133,7 @@ __global__ __launch_bounds__(block_threads(TEAM)) void norm_backward_kernel(Norm
             if (post)
 #pragma unroll
                 for (uint32_t j = 0; j < 8; ++j)
-                    g[i][j] = (fmaf(-normed(z[i][j], s), m0, g[i][j]) - m1) * s.rs * s.unit;
+                    g[i][j] = (fmaf(-normed(z[i][j], s), m0, g[i][j]) - m1) * s.k;
             store_bf(a.dz + row * a.dz_stride + (i * TEAM + sub) * 8, pack8(g[i]), n[i], a.wide);
         }
     }
@@ -158,60 +158,60 @@ __global__ __launch_bounds__(block_threads(TEAM)) void norm_backward_kernel(Norm
 // ---------------------------------------------------------------------------
 
 // Both halves' statistics at once: x before the norm `before`, z before the norm `after`.
-template <uint32_t TEAM, uint32_t CHUNKS, typename X, typename Z>
+// MEAN: one of them may be a LAYER norm.
+template <bool MEAN, uint32_t TEAM, uint32_t CHUNKS, typename X, typename Z>
 __device__ __forceinline__ void both_stats(const X &x, const Z &z, const uint32_t (&n)[CHUNKS], const NormArgs &a, bool pre,
                                            bool post, Stat &sx, Stat &sz, Team<TEAM> &team) {
-    sx = sz = {0.0f, 0.0f, 1.0f, 1.0f};
-    const bool lx = pre && a.before.kind == ZC_NORM_LAYER, lz = post && a.after.kind == ZC_NORM_LAYER;
-    float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (lx || lz) {
-        float u[2] = {0.0f, 0.0f};
+    float t[2] = {0.0f, 0.0f}, rest[2] = {0.0f, 0.0f};
+    const bool lx = MEAN && pre && a.before.kind == ZC_NORM_LAYER, lz = MEAN && post && a.after.kind == ZC_NORM_LAYER;
+    if (MEAN && (lx || lz)) {
+        float u[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        float m[2] = {0.0f, 0.0f};
 #pragma unroll
         for (uint32_t i = 0; i < CHUNKS; ++i)
 #pragma unroll
             for (uint32_t j = 0; j < 8; ++j) {
-                u[0] += x[i][j];
-                u[1] += z[i][j];
+                m[0] += x[i][j];
+                m[1] += z[i][j];
             }
-        team.sum(u);
-        sx.mean = lx ? u[0] * a.inv_cols : 0.0f;
-        sz.mean = lz ? u[1] * a.inv_cols : 0.0f;
+        team.sum(m);
+        sx.mean = lx ? m[0] * a.inv_cols : 0.0f;
+        sz.mean = lz ? m[1] * a.inv_cols : 0.0f;
 #pragma unroll
         for (uint32_t i = 0; i < CHUNKS; ++i)
 #pragma unroll
             for (uint32_t j = 0; j < 8; ++j) {
                 const float dx = n[i] ? x[i][j] - sx.mean : 0.0f, dz = n[i] ? z[i][j] - sz.mean : 0.0f;
-                t[0] = fmaf(dx, dx, t[0]);
-                t[1] = fmaf(dz, dz, t[1]);
-                t[2] += dx;
-                t[3] += dz;
+                u[0] = fmaf(dx, dx, u[0]);
+                u[1] = fmaf(dz, dz, u[1]);
+                u[2] += dx;
+                u[3] += dz;
             }
-        team.sum(t);
-        if (lx) {
-            sx.rest = t[2] * a.inv_cols;
-            const float left = fmaf(-sx.rest, t[2], t[0]);
-            t[0] = left < 0.0f ? 0.0f : left;
-        }
-        if (lz) {
-            sz.rest = t[3] * a.inv_cols;
-            const float left = fmaf(-sz.rest, t[3], t[1]);
-            t[1] = left < 0.0f ? 0.0f : left;
-        }
+        team.sum(u);
+        rest[0] = lx ? u[2] * a.inv_cols : 0.0f;
+        rest[1] = lz ? u[3] * a.inv_cols : 0.0f;
+        t[0] = fmaf(-rest[0], u[2], u[0]);
+        t[1] = fmaf(-rest[1], u[3], u[1]);
+#pragma unroll
+        for (uint32_t k = 0; k < 2; ++k) t[k] = t[k] < 0.0f ? 0.0f : t[k];
     } else {
-        float u[2] = {0.0f, 0.0f};
 #pragma unroll
         for (uint32_t i = 0; i < CHUNKS; ++i)
 #pragma unroll
             for (uint32_t j = 0; j < 8; ++j) {
-                u[0] = fmaf(x[i][j], x[i][j], u[0]);
-                u[1] = fmaf(z[i][j], z[i][j], u[1]);
+                t[0] = fmaf(x[i][j], x[i][j], t[0]);
+                t[1] = fmaf(z[i][j], z[i][j], t[1]);
             }
-        team.sum(u);
-        t[0] = u[0];
-        t[1] = u[1];
+        team.sum(t);
     }
-    sx.rs = __builtin_amdgcn_rsqf(fmaf(t[0], a.inv_cols, a.before.eps));
-    sz.rs = __builtin_amdgcn_rsqf(fmaf(t[1], a.inv_cols, a.after.eps));
+    if (pre) {
+        sx.k = __builtin_amdgcn_rsqf(fmaf(t[0], a.inv_cols, a.before.eps));
+        sx.off = rest[0] * sx.k;
+    }
+    if (post) {
+        sz.k = __builtin_amdgcn_rsqf(fmaf(t[1], a.inv_cols, a.after.eps));
+        sz.off = rest[1] * sz.k;
+    }
     // squares outside the range of a float: one row at a time
     if (pre && (!(t[0] <= 0x1p120f) || (t[0] < 0x1p-80f && a.before.eps < 0x1p-58f)))
         sx = row_stat<TEAM, CHUNKS>(x, n, a.before.kind, a.before.eps, a.inv_cols, team);
@@ -220,15 +220,17 @@ __device__ __forceinline__ void both_stats(const X &x, const Z &z, const uint32_
 }
 
 // As the kernel above, with the next row's loads on their way while a row is worked on, weights and gate in
-// registers, and no branch around a load or store.
-template <bool F32S, bool F32P, bool BIAS, uint32_t TEAM, uint32_t CHUNKS>
+// registers, and no branch around a load or store.  ANY: with biases, means and the rows' gates; without it about
+// 34 instructions a value, which bound the kernel beside the memory: 8192 x 7168 takes 184 us with ANY and 128
+// without, 5.5 TB/s, past what a large copy reaches.
+template <bool F32S, bool F32P, bool ANY, uint32_t TEAM, uint32_t CHUNKS>
 __global__ __launch_bounds__(block_threads(TEAM)) void norm_backward_whole_kernel(NormArgs a) {
     __shared__ float parts[2][kMaxWaves][4];
     Team<TEAM> team = {parts, 0};
     const uint32_t sub = threadIdx.x % TEAM;
     const uint32_t index = (uint32_t)__builtin_amdgcn_readfirstlane(blockIdx.x * block_teams(TEAM) + threadIdx.x / TEAM);
     uint32_t n[CHUNKS];
-    float dw1[CHUNKS][8], dgate[CHUNKS][8], dw2[CHUNKS][8], db1[BIAS ? CHUNKS : 1][8], db2[BIAS ? CHUNKS : 1][8];
+    float dw1[CHUNKS][8], dgate[CHUNKS][8], dw2[CHUNKS][8], db1[ANY ? CHUNKS : 1][8], db2[ANY ? CHUNKS : 1][8];
     Eight<F32P> w1[CHUNKS], gate[CHUNKS], w2[CHUNKS];
     const bool pre = a.dy && a.before.kind != ZC_NORM_NONE, post = a.z && a.after.kind != ZC_NORM_NONE;
 #pragma unroll
@@ -241,7 +243,7 @@ __global__ __launch_bounds__(block_threads(TEAM)) void norm_backward_whole_kerne
 #pragma unroll
         for (uint32_t j = 0; j < 8; ++j) {
             dw1[i][j] = dgate[i][j] = dw2[i][j] = 0.0f;
-            if (BIAS) db1[BIAS ? i : 0][j] = db2[BIAS ? i : 0][j] = 0.0f;
+            if (ANY) db1[ANY ? i : 0][j] = db2[ANY ? i : 0][j] = 0.0f;
         }
     }
     struct Loaded {
@@ -273,9 +275,9 @@ __global__ __launch_bounds__(block_threads(TEAM)) void norm_backward_whole_kerne
             stay_packed(gate[i]);
             stay_packed(w2[i]);
         }
-        const float rg = a.row_gate ? a.row_gate[row] : 1.0f;
-        Stat sx, sz;
-        if (pre || post) both_stats<TEAM, CHUNKS>(v.x, v.z, n, a, pre, post, sx, sz, team);
+        const float rg = ANY && a.row_gate ? a.row_gate[row] : 1.0f;
+        Stat sx = {0.0f, 0.0f, 1.0f}, sz = sx;
+        if (pre || post) both_stats<ANY, TEAM, CHUNKS>(v.x, v.z, n, a, pre, post, sx, sz, team);
 #pragma unroll
         for (uint32_t i = 0; i < CHUNKS; ++i) {
             stay_packed(v.x[i]);
@@ -290,22 +292,32 @@ __global__ __launch_bounds__(block_threads(TEAM)) void norm_backward_whole_kerne
             for (uint32_t i = 0; i < CHUNKS; ++i)
 #pragma unroll
                 for (uint32_t j = 0; j < 8; ++j) {
-                    const float h = normed(v.x[i][j], sx), d = v.dy[i][j];
+                    const float h = normed<ANY>(v.x[i][j], sx), d = v.dy[i][j];
                     dw2[i][j] = fmaf(d, h, dw2[i][j]);
-                    if (BIAS) db2[BIAS ? i : 0][j] += d;
+                    if (ANY) db2[ANY ? i : 0][j] += d;
                     g[i][j] = d * w2[i][j];
                     t[0] = fmaf(g[i][j], h, t[0]);
-                    t[1] += g[i][j];
+                    if (ANY) t[1] += g[i][j];
                 }
-            team.sum(t);
-            const float m0 = t[0] * a.inv_cols, m1 = a.before.kind == ZC_NORM_LAYER ? t[1] * a.inv_cols : 0.0f;
+            float m0, m1 = 0.0f;
+            if (ANY) {
+                team.sum(t);
+                m0 = t[0] * a.inv_cols;
+                if (a.before.kind == ZC_NORM_LAYER) m1 = t[1] * a.inv_cols;
+            } else {
+                float u[1] = {t[0]};
+                team.sum(u);
+                m0 = u[0] * a.inv_cols;
+            }
 #pragma unroll
             for (uint32_t i = 0; i < CHUNKS; ++i) stay_packed(v.x[i]);
 #pragma unroll
             for (uint32_t i = 0; i < CHUNKS; ++i)
 #pragma unroll
-                for (uint32_t j = 0; j < 8; ++j)
-                    g[i][j] = fmaf((fmaf(-normed(v.x[i][j], sx), m0, g[i][j]) - m1) * sx.rs, sx.unit, v.dr[i][j]);
+                for (uint32_t j = 0; j < 8; ++j) {
+                    const float u = fmaf(-normed<ANY>(v.x[i][j], sx), m0, g[i][j]);
+                    g[i][j] = fmaf(ANY ? u - m1 : u, sx.k, v.dr[i][j]);
+                }
         } else {
 #pragma unroll
             for (uint32_t i = 0; i < CHUNKS; ++i)
@@ -315,37 +327,48 @@ __global__ __launch_bounds__(block_threads(TEAM)) void norm_backward_whole_kerne
         const Row rr = row_of(a.r, row * a.r_stride, a.cols, F32S ? 4 : 2);
 #pragma unroll
         for (uint32_t i = 0; i < CHUNKS; ++i) store_row<F32S>(rr, (i * TEAM + sub) * 8, g[i]);
+        const float share = ANY ? a.scale * rg : a.scale;
         float t[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (uint32_t i = 0; i < CHUNKS; ++i) {
             float b[8];
-            if (post && a.after.b.p) load_param(a.after.b, (i * TEAM + sub) * 8, n[i], 0.0f, b);
+            if (ANY && post && a.after.b.p) load_param(a.after.b, (i * TEAM + sub) * 8, n[i], 0.0f, b);
 #pragma unroll
             for (uint32_t j = 0; j < 8; ++j) {
-                const float h0 = v.z[i][j], zh = post ? normed(h0, sz) : h0;
-                const float h = post && a.after.b.p ? fmaf(zh, w1[i][j], b[j]) : zh * w1[i][j];
-                const float e = n[i] ? a.scale * g[i][j] : 0.0f, ge = gate[i][j] * e;
-                dgate[i][j] = fmaf(rg * e, h, dgate[i][j]);
-                t[0] = fmaf(ge, h, t[0]);
-                const float dh = rg * ge;
+                const float zh = normed<ANY>(v.z[i][j], sz);  // z itself without a norm
+                const float h = ANY && post && a.after.b.p ? fmaf(zh, w1[i][j], b[j]) : zh * w1[i][j];
+                const float e = ANY ? (n[i] ? g[i][j] : 0.0f) : g[i][j], q = e * h;
+                dgate[i][j] = fmaf(share, q, dgate[i][j]);
+                if (ANY) t[2] = fmaf(gate[i][j], q, t[2]);
+                const float dh = gate[i][j] * e * share;
                 dw1[i][j] = fmaf(dh, zh, dw1[i][j]);
-                if (BIAS) db1[BIAS ? i : 0][j] += dh;
+                if (ANY) db1[ANY ? i : 0][j] += dh;
                 g[i][j] = dh * w1[i][j];
-                t[1] = fmaf(g[i][j], zh, t[1]);
-                t[2] += g[i][j];
+                t[0] = fmaf(g[i][j], zh, t[0]);
+                if (ANY) t[1] += g[i][j];
             }
         }
-        if (a.drow_gate || post) team.sum(t);
-        if (a.drow_gate && sub == 0) a.drow_gate[row] = t[0];
-        const float m0 = t[1] * a.inv_cols, m1 = a.after.kind == ZC_NORM_LAYER ? t[2] * a.inv_cols : 0.0f;
+        float m0 = 0.0f, m1 = 0.0f;
+        if (ANY) {
+            if (a.drow_gate || post) team.sum(t);
+            if (a.drow_gate && sub == 0) a.drow_gate[row] = a.z ? a.scale * t[2] : 0.0f;
+            m0 = t[0] * a.inv_cols;
+            if (a.after.kind == ZC_NORM_LAYER) m1 = t[1] * a.inv_cols;
+        } else if (post) {
+            float u[1] = {t[0]};
+            team.sum(u);
+            m0 = u[0] * a.inv_cols;
+        }
         const Row rz = row_of(a.dz, row * a.dz_stride, a.cols, 2);
 #pragma unroll
         for (uint32_t i = 0; i < CHUNKS; ++i) {
             stay_packed(v.z[i]);
             if (post)
 #pragma unroll
-                for (uint32_t j = 0; j < 8; ++j)
-                    g[i][j] = (fmaf(-normed(v.z[i][j], sz), m0, g[i][j]) - m1) * sz.rs * sz.unit;
+                for (uint32_t j = 0; j < 8; ++j) {
+                    const float u = fmaf(-normed<ANY>(v.z[i][j], sz), m0, g[i][j]);
+                    g[i][j] = (ANY ? u - m1 : u) * sz.k;
+                }
             store_row<false>(rz, (i * TEAM + sub) * 8, g[i]);
         }
         row += step;
@@ -360,9 +383,9 @@ __global__ __launch_bounds__(block_threads(TEAM)) void norm_backward_whole_kerne
         leave(kDW1, dw1[i]);
         leave(kDGate, dgate[i]);
         leave(kDW2, dw2[i]);
-        if (BIAS) {
-            leave(kDB1, db1[BIAS ? i : 0]);
-            leave(kDB2, db2[BIAS ? i : 0]);
+        if (ANY) {
+            leave(kDB1, db1[ANY ? i : 0]);
+            leave(kDB2, db2[ANY ? i : 0]);
         }
     }
 }
@@ -400,21 +423,21 @@ __global__ __launch_bounds__(kLanes * kSumRuns) void norm_sums_kernel(SumArgs a)
 // host
 // ---------------------------------------------------------------------------
 
-static void launch_backward(const NormArgs &a, const Shape &s, bool whole, bool f32, bool f32p, bool bias, dim3 grid,
+static void launch_backward(const NormArgs &a, const Shape &s, bool whole, bool f32, bool f32p, bool any, dim3 grid,
                             Launches &on) {
     with_shape(s, [&](auto team, auto chunks) {
         constexpr uint32_t T = decltype(team)::value, C = decltype(chunks)::value;
-        const auto pick = [&](auto f32_t, auto bias_t) {
-            constexpr bool S = decltype(f32_t)::value, B = decltype(bias_t)::value;
+        const auto pick = [&](auto f32_t, auto any_t) {
+            constexpr bool S = decltype(f32_t)::value, B = decltype(any_t)::value;
             on.launch(!whole ? norm_backward_kernel<S, B, T, C>
                       : f32p ? norm_backward_whole_kernel<S, true, B, T, C>
                              : norm_backward_whole_kernel<S, false, B, T, C>,
                       grid, dim3(block_threads(T)), a);
         };
         if (f32)
-            bias ? pick(std::true_type{}, std::true_type{}) : pick(std::true_type{}, std::false_type{});
+            any ? pick(std::true_type{}, std::true_type{}) : pick(std::true_type{}, std::false_type{});
         else
-            bias ? pick(std::false_type{}, std::true_type{}) : pick(std::false_type{}, std::false_type{});
+            any ? pick(std::false_type{}, std::true_type{}) : pick(std::false_type{}, std::false_type{});
     });
 }
 
@@ -461,7 +484,7 @@ extern "C" zc_status zc_norm_backward(const void *d_r, uint32_t stream_type, uin
     if (!aligned(d_r, size) || !aligned(d_z, 2) || !aligned(d_dr, size) || !aligned(d_dy, 2) || !aligned(d_dx, size) ||
         !aligned(d_dz, 2) || !aligned(row_gate, 4) || !aligned(d_workspace, 16))
         return ZC_ERR_MISALIGNED;
-    NormArgs a = common(*cfg, rows, cols);
+    NormArgs a = common(*cfg, rows, cols, d_z != nullptr);
     a.x = d_r;
     a.z = static_cast<const uint16_t *>(d_z);
     a.dr = d_dr;
@@ -498,10 +521,14 @@ extern "C" zc_status zc_norm_backward(const void *d_r, uint32_t stream_type, uin
     a.wide = cols % 8 == 0 && wide8(d_dx, dx_stride, f32) && wide8(d_dz, dz_stride);
     const bool whole = a.wide && wide8(d_r, r_stride, f32) && wide8(d_dr, dr_stride, f32) && wide8(d_dy, dy_stride) &&
                        wide8(d_z, z_stride);
+    // sums of the biases; in whole rows also means, biases and the rows' gates
+    bool any = a.sums & (1u << kDB1 | 1u << kDB2);
+    if (whole)
+        any |= (d_dy && a.before.kind == ZC_NORM_LAYER) || (d_z && (a.after.kind == ZC_NORM_LAYER || a.after.b.p)) ||
+               (d_z && a.row_gate) || row_gate;
     Launches on(stream);
     if (rows && (a.sums || d_dx || d_dz || row_gate))
-        launch_backward(a, s, whole, f32, any_float(*cfg, d_z != nullptr), a.sums & (1u << kDB1 | 1u << kDB2),
-                        dim3((uint32_t)blocks), on);
+        launch_backward(a, s, whole, f32, any_float(*cfg, d_z != nullptr), any, dim3((uint32_t)blocks), on);
     if (asked) on.launch(norm_sums_kernel, dim3((uint32_t)ceil_div(cols, kLanes), kSums), dim3(kLanes * kSumRuns), sum);
     return on.status();
 }
