@@ -746,29 +746,43 @@ struct SlopeArgs {
     uint32_t rows, cols, row_step, act, dout_f32;
     float scale;
 };
-// A block takes 64 * 8 columns and, over its four waves, every fourth row of its run of rows.
+// A block takes 64 * 8 columns and, over its four waves, every fourth row of its run of rows, two rows of a wave
+// on their way at once.  Bound by memory: 8192 x 4096 with
+// SILU 50 us, 4 TB/s (64 runs of rows, a row of a wave at a time: 87).
 constexpr uint32_t kSWaves = 4;
+template <bool WIDE>
 __global__ __launch_bounds__(kSWaves * kLanes) void slope_kernel(SlopeArgs a) {
     __shared__ float sums[kSWaves][kLanes * 8];
     const uint32_t lane = lane_id(), wave = threadIdx.x / kLanes;
     const uint32_t c = (blockIdx.x * kLanes + lane) * 8, n = c < a.cols ? min(a.cols - c, 8u) : 0u;
     const uint64_t r1 = min((uint64_t)a.rows, (uint64_t)(blockIdx.y + 1) * a.row_step);
     float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    for (uint64_t r = (uint64_t)blockIdx.y * a.row_step + wave; r < r1; r += kSWaves) {
+    const auto fetch = [&](uint64_t r, Raw &d, Eight<false> &v) {
+        if (r >= r1) return;
+        d.load(a.dout, a.dout_f32, r * a.dout_stride + c, n);
+        if (a.act != ZC_ACT_NONE) v.load(a.pre, r * a.pre_stride + c, n, true);
+    };
+    const auto work = [&](uint64_t r, const Raw &raw, const Eight<false> &v) {
+        if (r >= r1) return;
         float d[8];
-        load8(a.dout, a.dout_f32, r * a.dout_stride + c, n, d);
-        if (a.act != ZC_ACT_NONE) {
-            Eight<false> v;
-            v.load(a.pre, r * a.pre_stride + c, n, true);
+        raw.values(a.dout_f32, d);
+        if (a.act != ZC_ACT_NONE)
 #pragma unroll
             for (uint32_t i = 0; i < 8; ++i) d[i] = sloped(d[i], v[i], a.act);
-        }
 #pragma unroll
         for (uint32_t i = 0; i < 8; ++i) {
             d[i] *= a.scale;
             acc[i] += d[i];
         }
-        if (a.dpre) store_values<false>(a.dpre + r * a.dpre_stride + c, pack8(d), n);
+        if (a.dpre) store_values<WIDE>(a.dpre + r * a.dpre_stride + c, pack8(d), n);
+    };
+    for (uint64_t r = (uint64_t)blockIdx.y * a.row_step + wave; r < r1; r += 2 * kSWaves) {
+        Raw d0, d1;
+        Eight<false> v0, v1;
+        fetch(r, d0, v0);
+        fetch(r + kSWaves, d1, v1);
+        work(r, d0, v0);
+        work(r + kSWaves, d1, v1);
     }
     if (!a.parts) return;
 #pragma unroll
@@ -955,7 +969,7 @@ static zc_status gradient(ProductArgs p, uint64_t m, uint64_t n, uint64_t k, boo
     return launch_product(p, m, n, k, xa, true, ws, ws_bytes, stream);
 }
 
-constexpr uint32_t kSlopeRuns = 64;  // runs of rows whose column sums are parts
+constexpr uint32_t kSlopeRuns = 256;  // runs of rows whose column sums are parts, at most
 
 }  // namespace moe
 }  // namespace zc
@@ -1050,7 +1064,10 @@ extern "C" zc_status zc_activation_backward(const void *d_dout, uint32_t dout_ty
     a.scale = scale;
     const uint32_t runs = rows ? (uint32_t)ceil_div(rows, a.row_step) : 0;
     Launches on(stream);
-    if (rows) on.launch(slope_kernel, dim3((uint32_t)ceil_div(cols, kLanes * 8), runs), dim3(kSWaves * kLanes), a);
+    const bool wide = cols % 8 == 0 && aligned(d_dpre, 16) && dpre_stride % 8 == 0;
+    if (rows)
+        on.launch(wide ? slope_kernel<true> : slope_kernel<false>, dim3((uint32_t)ceil_div(cols, kLanes * 8), runs),
+                  dim3(kSWaves * kLanes), a);
     if (d_dbias)
         on.launch(column_sums_kernel, dim3((uint32_t)ceil_div(cols, kLanes)), dim3(kLanes * kRuns), a.parts, runs, a.cols,
                   d_dbias);

@@ -55,7 +55,7 @@ def test_sizes(moe):
     assert moe.zc_matmul_workspace_bytes(256, 256, 8192) > 0
     assert moe.zc_activation_backward_workspace_bytes(8192, 4096) % 256 == 0
     assert moe.zc_activation_backward_workspace_bytes(8192, 4096) >= 4 * 4096
-    for t, e, s in ((1, 1, 1), (8192, 256, 1), (1 << 20, 1024, 1024), (100, 1024, 1024)):
+    for t, e, s in ((0, 8, 1), (1, 1, 1), (8192, 256, 1), (1 << 20, 1024, 1024), (100, 1024, 1024)):
         n = moe.zc_balance_workspace_bytes(t, e, s)
         assert n % 256 == 0 and 0 < n <= moe.ZC_BALANCE_WORKSPACE_MAX
     assert moe.zc_balance_workspace_bytes(8, 0, 1) == 0 and moe.zc_balance_workspace_bytes(8, 1025, 1) == 0
