@@ -32,7 +32,7 @@ struct NormArgs {
     uint64_t x_stride, z_stride, r_stride, y_stride, dr_stride, dy_stride, dz_stride, q_stride, qs_stride;
     uint64_t part_stride;  // floats of one sum's parts
     uint32_t rows, cols, sums;  // sums: which are asked for, a bit each
-    uint32_t wide;
+    uint32_t wide;  // any rows: the results' start on 16 bytes
     float scale, inv_cols;
 };
 
@@ -125,20 +125,21 @@ __device__ __forceinline__ float normed(float v, const Stat &s) {
 
 template <uint32_t TEAM, uint32_t CHUNKS, typename V>
 __device__ __forceinline__ Stat row_stat(const V &v, const uint32_t (&n)[CHUNKS], uint32_t kind, float eps,
-                                         float inv_cols, Team<TEAM> &team) {
+                                         float inv_cols, Team<TEAM> &team, float tail = 0.0f, bool in_tail = false) {
     float mean = 0.0f, rest = 0.0f, unit = 1.0f;
     float var = 0.0f;
     const auto measure = [&]() {
         mean = rest = 0.0f;
         if (kind == ZC_NORM_LAYER) {
-            float t[1] = {0.0f};
+            float t[1] = {tail * unit};
 #pragma unroll
             for (uint32_t i = 0; i < CHUNKS; ++i)
 #pragma unroll
                 for (uint32_t j = 0; j < 8; ++j) t[0] = fmaf(v[i][j], unit, t[0]);
             team.sum(t);
             mean = t[0] * inv_cols;
-            float u[2] = {0.0f, 0.0f};
+            const float last = in_tail ? fmaf(tail, unit, -mean) : 0.0f;
+            float u[2] = {last * last, last};
 #pragma unroll
             for (uint32_t i = 0; i < CHUNKS; ++i)
 #pragma unroll
@@ -153,7 +154,7 @@ __device__ __forceinline__ Stat row_stat(const V &v, const uint32_t (&n)[CHUNKS]
             const float left = fmaf(-rest, u[1], u[0]);
             var = left < 0.0f ? 0.0f : left;
         } else {
-            float t[1] = {0.0f};
+            float t[1] = {tail * unit * (tail * unit)};
 #pragma unroll
             for (uint32_t i = 0; i < CHUNKS; ++i)
 #pragma unroll
@@ -176,27 +177,28 @@ __device__ __forceinline__ Stat row_stat(const V &v, const uint32_t (&n)[CHUNKS]
 }
 
 // ---------------------------------------------------------------------------
-// whole rows
+// rows through descriptors
 // ---------------------------------------------------------------------------
 
-// Rows that start on 16 bytes and are whole pieces of 8 values are reached through a
-// descriptor of their own: what lies past the row's end reads as 0 and is not written,
-// without a branch, so that a load on its way is waited for by its place among the loads and
-// stores and not by the end of them all.  A descriptor of no bytes stands for an array that is not there.
+// A row is reached through a descriptor of its own (buffer accesses take any value as their
+// start): what lies past its end reads as 0 and is not written, without a branch, so that a load
+// on its way is waited for by its place among the loads and stores and not by the end of them all.
+// A descriptor of no bytes stands for an array that is not there.  `cols` are the row's
+// whole pieces of 8; the values behind them are its tail, one a lane.
 typedef __amdgpu_buffer_rsrc_t Row;
 __device__ __forceinline__ Row row_of(const void *base, uint64_t at, uint32_t cols, uint32_t size) {
     // (word 3: plain 32-bit data)
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(static_cast<const uint8_t *>(base)) + at * size, 0,
                                              base ? (int)(cols * size) : 0, 0x00020000);
 }
-constexpr int kOnce = 2;  // nothing reads it again
-template <bool F32>
+// ONCE: nothing reads it again, and rows start on 16 bytes, so that no line is shared by two accesses.
+template <bool F32, bool ONCE>
 __device__ __forceinline__ void load_row(Row r, uint32_t c, Eight<F32> &v) {
 #pragma unroll
     for (uint32_t i = 0; i < (F32 ? 2 : 1); ++i)
-        v.w[i] = __builtin_bit_cast(u32v4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)(c * (F32 ? 4 : 2) + 16 * i), 0, kOnce));
+        v.w[i] = __builtin_bit_cast(u32v4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)(c * (F32 ? 4 : 2) + 16 * i), 0, ONCE ? 2 : 0));
 }
-template <bool F32>
+template <bool F32, bool ONCE>
 __device__ __forceinline__ void store_row(Row r, uint32_t c, const float (&v)[8]) {
     if (F32) {
 #pragma unroll
@@ -204,10 +206,29 @@ __device__ __forceinline__ void store_row(Row r, uint32_t c, const float (&v)[8]
             __builtin_amdgcn_raw_buffer_store_b128(
                 u32v4{__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
                       __float_as_uint(v[4 * i + 3])},
-                r, (int)(c * 4 + 16 * i), 0, kOnce);
+                r, (int)(c * 4 + 16 * i), 0, ONCE ? 2 : 0);
     } else {
-        __builtin_amdgcn_raw_buffer_store_b128(pack8(v), r, (int)(c * 2), 0, kOnce);
+        __builtin_amdgcn_raw_buffer_store_b128(pack8(v), r, (int)(c * 2), 0, ONCE ? 2 : 0);
     }
+}
+
+// One value of a row's tail.
+template <bool F32>
+__device__ __forceinline__ float load_tail(Row r, uint32_t c) {
+    if (F32) return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, (int)(c * 4), 0, 0));
+    return bf_one((uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, (int)(c * 2), 0, 0));
+}
+template <bool F32>
+__device__ __forceinline__ void store_tail(Row r, uint32_t c, float v) {
+    if (F32)
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), r, (int)(c * 4), 0, 0);
+    else
+        __builtin_amdgcn_raw_buffer_store_b16(bf_round(v), r, (int)(c * 2), 0, 0);
+}
+__device__ __forceinline__ float keep_tail(const Param &q, uint32_t c, bool on, float otherwise) {
+    if (!on) return 0.0f;
+    if (!q.p) return otherwise;
+    return q.f32 ? static_cast<const float *>(q.p)[c] : bf_one(static_cast<const uint16_t *>(q.p)[c]);
 }
 
 // Keeps packed values packed: the compiler would unpack what does not change once for all rows.

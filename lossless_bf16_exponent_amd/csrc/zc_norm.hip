@@ -8,9 +8,10 @@ namespace zc {
 namespace moe {
 
 // ---------------------------------------------------------------------------
-// any rows
+// rows of any length with their 8-bit blocks
 // ---------------------------------------------------------------------------
 
+// The lanes hold their columns as the 8-bit blocks want them, the ragged last ones too.
 template <bool F32S, uint32_t TEAM, uint32_t CHUNKS>
 __global__ __launch_bounds__(block_threads(TEAM)) void norm_kernel(NormArgs a) {
     __shared__ float parts[2][kMaxWaves][4];
@@ -104,47 +105,59 @@ __global__ __launch_bounds__(block_threads(TEAM)) void norm_kernel(NormArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// whole rows
+// all others
 // ---------------------------------------------------------------------------
 
 // A team takes rows in turn, the next row's loads on their way while it works on one;
-// weights and gate stay in registers.  Q: with the 8-bit blocks of y.
-template <bool F32S, bool F32P, bool Q, uint32_t TEAM, uint32_t CHUNKS>
-__global__ __launch_bounds__(block_threads(TEAM), whole_waves(TEAM)) void norm_whole_kernel(NormArgs a) {
+// weights and gate stay in registers.  WIDE: rows start on 16 bytes and have no tail.  Q: with
+// the 8-bit blocks of y (WIDE only).  8192 x 7168, norms on both sides and a gate: 82 us, 5.7 TB/s, past what
+// a large copy reaches; without the loads ahead and with loads under conditions 158.
+template <bool F32S, bool F32P, bool WIDE, bool Q, uint32_t TEAM, uint32_t CHUNKS>
+__global__ __launch_bounds__(block_threads(TEAM), whole_waves(TEAM)) void norm_rows_kernel(NormArgs a) {
     __shared__ float parts[2][kMaxWaves][4];
     Team<TEAM> team = {parts, 0};
-    const uint32_t sub = threadIdx.x % TEAM;
+    const uint32_t sub = threadIdx.x % TEAM, whole = a.cols / 8 * 8, ct = whole + sub;
+    const bool in_tail = !WIDE && ct < a.cols;
     uint32_t n[CHUNKS];
     Eight<F32P> w1[CHUNKS], gate[CHUNKS], w2[CHUNKS];
     const bool post = a.z && a.after.kind != ZC_NORM_NONE, pre = a.before.kind != ZC_NORM_NONE;
 #pragma unroll
     for (uint32_t i = 0; i < CHUNKS; ++i) {
         const uint32_t c = (i * TEAM + sub) * 8;
-        n[i] = c < a.cols ? 8u : 0u;
+        n[i] = c < whole ? 8u : 0u;
         keep_param<F32P>(post ? a.after.w : Param{}, c, n[i], 1.0f, w1[i]);
         keep_param<F32P>(a.z ? a.gate : Param{}, c, n[i], 1.0f, gate[i]);
         keep_param<F32P>(pre ? a.before.w : Param{}, c, n[i], 1.0f, w2[i]);
     }
+    const float w1t = keep_tail(post ? a.after.w : Param{}, ct, in_tail, 1.0f), b1t = keep_tail(post ? a.after.b : Param{}, ct, in_tail, 0.0f);
+    const float gatet = keep_tail(a.z ? a.gate : Param{}, ct, in_tail, 1.0f);
+    const float w2t = keep_tail(pre ? a.before.w : Param{}, ct, in_tail, 1.0f), b2t = keep_tail(pre ? a.before.b : Param{}, ct, in_tail, 0.0f);
     const uint32_t step = gridDim.x * block_teams(TEAM);
     uint32_t row = (uint32_t)__builtin_amdgcn_readfirstlane(blockIdx.x * block_teams(TEAM) + threadIdx.x / TEAM);
     if (row >= a.rows) return;
     Eight<F32S> x[CHUNKS];
     Eight<false> z[CHUNKS];
-    const auto fetch = [&](uint32_t t, Eight<F32S> (&vx)[CHUNKS], Eight<false> (&vz)[CHUNKS]) {
-        const Row rx = row_of(a.x, t * a.x_stride, a.cols, F32S ? 4 : 2), rz = row_of(a.z, t * a.z_stride, a.cols, 2);
+    float xt = 0.0f, zt = 0.0f;
+    const auto fetch = [&](uint32_t t, Eight<F32S> (&vx)[CHUNKS], Eight<false> (&vz)[CHUNKS], float &tx, float &tz) {
+        const Row rx = row_of(a.x, t * a.x_stride, whole, F32S ? 4 : 2), rz = row_of(a.z, t * a.z_stride, whole, 2);
 #pragma unroll
         for (uint32_t i = 0; i < CHUNKS; ++i) {
-            load_row<false>(rz, (i * TEAM + sub) * 8, vz[i]);
-            load_row<F32S>(rx, (i * TEAM + sub) * 8, vx[i]);
+            load_row<false, WIDE>(rz, (i * TEAM + sub) * 8, vz[i]);
+            load_row<F32S, WIDE>(rx, (i * TEAM + sub) * 8, vx[i]);
+        }
+        if (!WIDE) {
+            tz = load_tail<false>(row_of(a.z, t * a.z_stride, a.cols, 2), ct);
+            tx = load_tail<F32S>(row_of(a.x, t * a.x_stride, a.cols, F32S ? 4 : 2), ct);
         }
     };
-    fetch(row, x, z);
+    fetch(row, x, z, xt, zt);
     for (;;) {
         // past the last row: that one again, so that no branch stands around the loads
         const uint32_t after = row + step < a.rows ? row + step : a.rows - 1;
         Eight<F32S> nx[CHUNKS];
         Eight<false> nz[CHUNKS];
-        fetch(after, nx, nz);
+        float nxt = 0.0f, nzt = 0.0f;
+        fetch(after, nx, nz, nxt, nzt);
 #pragma unroll
         for (uint32_t i = 0; i < CHUNKS; ++i) {
             stay_packed(w1[i]);
@@ -154,7 +167,10 @@ __global__ __launch_bounds__(block_threads(TEAM), whole_waves(TEAM)) void norm_w
         float v[CHUNKS][8];
         const float share = a.row_gate ? a.scale * a.row_gate[row] : a.scale;
         Stat s = {0.0f, 0.0f, 1.0f};
-        if (post) s = row_stat<TEAM, CHUNKS>(z, n, a.after.kind, a.after.eps, a.inv_cols, team);
+        if (post) s = row_stat<TEAM, CHUNKS>(z, n, a.after.kind, a.after.eps, a.inv_cols, team, zt, in_tail);
+        float vt = 0.0f;
+        if (!WIDE) vt = a.z ? fmaf(share, gatet * (post ? fmaf(normed(zt, s), w1t, b1t) : zt), xt) : xt;
+        if (!WIDE) vt = in_tail ? vt : 0.0f;
 #pragma unroll
         for (uint32_t i = 0; i < CHUNKS; ++i) {
             stay_packed(x[i]);
@@ -171,11 +187,13 @@ __global__ __launch_bounds__(block_threads(TEAM), whole_waves(TEAM)) void norm_w
                 v[i][j] = a.z ? fmaf(share, gate[i][j] * h, x[i][j]) : x[i][j];
             }
         }
-        const Row rr = row_of(a.r, row * a.r_stride, a.cols, F32S ? 4 : 2);
+        const Row rr = row_of(a.r, row * a.r_stride, whole, F32S ? 4 : 2);
 #pragma unroll
-        for (uint32_t i = 0; i < CHUNKS; ++i) store_row<F32S>(rr, (i * TEAM + sub) * 8, v[i]);
+        for (uint32_t i = 0; i < CHUNKS; ++i) store_row<F32S, WIDE>(rr, (i * TEAM + sub) * 8, v[i]);
+        if (!WIDE) store_tail<F32S>(row_of(a.r, row * a.r_stride, a.cols, F32S ? 4 : 2), ct, vt);
         if (pre) {
-            s = row_stat<TEAM, CHUNKS>(v, n, a.before.kind, a.before.eps, a.inv_cols, team);
+            s = row_stat<TEAM, CHUNKS>(v, n, a.before.kind, a.before.eps, a.inv_cols, team, vt, in_tail);
+            if (!WIDE) vt = fmaf(normed(vt, s), w2t, b2t);
 #pragma unroll
             for (uint32_t i = 0; i < CHUNKS; ++i) {
                 float b[8];
@@ -187,9 +205,10 @@ __global__ __launch_bounds__(block_threads(TEAM), whole_waves(TEAM)) void norm_w
                 }
             }
         }
-        const Row ry = row_of(a.y, row * a.y_stride, a.cols, 2);
+        const Row ry = row_of(a.y, row * a.y_stride, whole, 2);
 #pragma unroll
-        for (uint32_t i = 0; i < CHUNKS; ++i) store_row<false>(ry, (i * TEAM + sub) * 8, v[i]);
+        for (uint32_t i = 0; i < CHUNKS; ++i) store_row<false, WIDE>(ry, (i * TEAM + sub) * 8, v[i]);
+        if (!WIDE) store_tail<false>(row_of(a.y, row * a.y_stride, a.cols, 2), ct, vt);
         if (Q)
 #pragma unroll
             for (uint32_t i = 0; i < CHUNKS; ++i) {
@@ -208,6 +227,8 @@ __global__ __launch_bounds__(block_threads(TEAM), whole_waves(TEAM)) void norm_w
             x[i] = nx[i];
             z[i] = nz[i];
         }
+        xt = nxt;
+        zt = nzt;
     }
 }
 
@@ -223,19 +244,22 @@ static void launch_norm(const NormArgs &a, const Shape &s, bool f32, Launches &o
         on.launch(f32 ? norm_kernel<true, T, C> : norm_kernel<false, T, C>, grid, dim3(block_threads(T)), a);
     });
 }
-static void launch_whole(const NormArgs &a, const Shape &s, bool f32, bool f32p, Launches &on) {
+static void launch_rows(const NormArgs &a, const Shape &s, bool f32, bool f32p, bool wide, Launches &on) {
     // as many blocks as the device holds at once
     const uint64_t blocks = ceil_div(a.rows, block_teams(s.team)), most = 256 * (4 * whole_waves(s.team) * kLanes / block_threads(s.team));
     const dim3 grid((uint32_t)(blocks < most ? blocks : most));
     with_shape(s, [&](auto team, auto chunks) {
         constexpr uint32_t T = decltype(team)::value, C = decltype(chunks)::value;
-        const auto pick = [&](auto q) {
-            constexpr bool Q = decltype(q)::value;
-            on.launch(f32 ? (f32p ? norm_whole_kernel<true, true, Q, T, C> : norm_whole_kernel<true, false, Q, T, C>)
-                          : (f32p ? norm_whole_kernel<false, true, Q, T, C> : norm_whole_kernel<false, false, Q, T, C>),
+        const auto pick = [&](auto wide_t, auto q_t) {
+            constexpr bool W = decltype(wide_t)::value, Q = decltype(q_t)::value;
+            on.launch(f32 ? (f32p ? norm_rows_kernel<true, true, W, Q, T, C> : norm_rows_kernel<true, false, W, Q, T, C>)
+                          : (f32p ? norm_rows_kernel<false, true, W, Q, T, C> : norm_rows_kernel<false, false, W, Q, T, C>),
                       grid, dim3(block_threads(T)), a);
         };
-        a.yq ? pick(std::true_type{}) : pick(std::false_type{});
+        if (a.yq)
+            pick(std::true_type{}, std::true_type{});
+        else
+            wide ? pick(std::true_type{}, std::false_type{}) : pick(std::false_type{}, std::false_type{});
     });
 }
 
@@ -276,10 +300,11 @@ extern "C" zc_status zc_norm(const void *d_x, uint32_t stream_type, uint64_t row
     a.wide = cols % 8 == 0 && wide8(d_r, r_stride, f32) && wide8(d_y, y_stride);
     const Shape s = shape_of(cols);
     Launches on(stream);
-    if (a.wide && wide8(d_x, x_stride, f32) && wide8(d_z, z_stride))
-        launch_whole(a, s, f32, any_float(*cfg, d_z != nullptr), on);
-    else
+    const bool wide = a.wide && wide8(d_x, x_stride, f32) && wide8(d_z, z_stride);
+    if (a.yq && !wide)
         launch_norm(a, s, f32, on);
+    else
+        launch_rows(a, s, f32, any_float(*cfg, d_z != nullptr), wide, on);
     return on.status();
 }
 

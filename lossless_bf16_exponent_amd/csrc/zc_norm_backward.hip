@@ -7,166 +7,19 @@ namespace zc {
 namespace moe {
 
 // ---------------------------------------------------------------------------
-// any rows
-// ---------------------------------------------------------------------------
-
-// With v^ the normed value and u = dy * w the gradient there, that of v is
-//   1 / deviation * (u - v^ mean(u v^) [- mean(u) for LAYER]).
-// A team's lanes keep their columns from row to row, so the sums over the rows
-// stay in registers until the team's last row and leave as one part a team; a
-// second launch adds the parts in order.  BIAS: with the biases' sums.  Columns past
-// the end read as 0 and have a gradient of 0, so they add nothing.
-template <bool F32S, bool BIAS, uint32_t TEAM, uint32_t CHUNKS>
-__global__ __launch_bounds__(block_threads(TEAM)) void norm_backward_kernel(NormArgs a) {
-    __shared__ float parts[2][kMaxWaves][4];
-    Team<TEAM> team = {parts, 0};
-    const uint32_t sub = threadIdx.x % TEAM, index = blockIdx.x * block_teams(TEAM) + threadIdx.x / TEAM;
-    uint32_t n[CHUNKS];
-    float dw1[CHUNKS][8], dgate[CHUNKS][8], dw2[CHUNKS][8], db1[BIAS ? CHUNKS : 1][8], db2[BIAS ? CHUNKS : 1][8];
-#pragma unroll
-    for (uint32_t i = 0; i < CHUNKS; ++i) {
-        const uint32_t c = (i * TEAM + sub) * 8;
-        n[i] = c < a.cols ? min(a.cols - c, 8u) : 0u;
-#pragma unroll
-        for (uint32_t j = 0; j < 8; ++j) {
-            dw1[i][j] = dgate[i][j] = dw2[i][j] = 0.0f;
-            if (BIAS) db1[BIAS ? i : 0][j] = db2[BIAS ? i : 0][j] = 0.0f;
-        }
-    }
-    const bool pre = a.before.kind != ZC_NORM_NONE, post = a.after.kind != ZC_NORM_NONE;
-    for (uint64_t row = index; row < a.rows; row += (uint64_t)gridDim.x * block_teams(TEAM)) {
-        Eight<F32S> x[CHUNKS], dr[CHUNKS];
-        Eight<false> dy[CHUNKS], z[CHUNKS];
-#pragma unroll
-        for (uint32_t i = 0; i < CHUNKS; ++i) {
-            const uint32_t c = (i * TEAM + sub) * 8;
-            if (a.dy && pre) x[i].load(a.x, row * a.x_stride + c, n[i], true);
-            dr[i].clear();
-            dy[i].clear();
-            if (a.dy) dy[i].load(a.dy, row * a.dy_stride + c, n[i], true);
-            if (a.dr) dr[i].load(a.dr, row * a.dr_stride + c, n[i], true);
-            if (a.z) z[i].load(a.z, row * a.z_stride + c, n[i], true);
-        }
-        float g[CHUNKS][8];  // the gradient of r
-        if (a.dy && pre) {
-            const Stat s = row_stat<TEAM, CHUNKS>(x, n, a.before.kind, a.before.eps, a.inv_cols, team);
-            float t[2] = {0.0f, 0.0f};
-#pragma unroll
-            for (uint32_t i = 0; i < CHUNKS; ++i) {
-                float w[8];
-                load_param(a.before.w, (i * TEAM + sub) * 8, n[i], 1.0f, w);
-#pragma unroll
-                for (uint32_t j = 0; j < 8; ++j) {
-                    const float v = normed(x[i][j], s);
-                    dw2[i][j] = fmaf(dy[i][j], v, dw2[i][j]);
-                    if (BIAS) db2[BIAS ? i : 0][j] += dy[i][j];
-                    g[i][j] = dy[i][j] * w[j];
-                    t[0] = fmaf(g[i][j], v, t[0]);
-                    t[1] += g[i][j];
-                }
-            }
-            team.sum(t);
-            const float m0 = t[0] * a.inv_cols, m1 = a.before.kind == ZC_NORM_LAYER ? t[1] * a.inv_cols : 0.0f;
-#pragma unroll
-            for (uint32_t i = 0; i < CHUNKS; ++i)
-#pragma unroll
-                for (uint32_t j = 0; j < 8; ++j)
-                    g[i][j] = fmaf(fmaf(-normed(x[i][j], s), m0, g[i][j]) - m1, s.k, dr[i][j]);
-        } else {
-#pragma unroll
-            for (uint32_t i = 0; i < CHUNKS; ++i)
-#pragma unroll
-                for (uint32_t j = 0; j < 8; ++j) g[i][j] = dr[i][j] + dy[i][j];
-        }
-        if (a.r)
-#pragma unroll
-            for (uint32_t i = 0; i < CHUNKS; ++i)
-                store_stream<F32S>(a.r, row * a.r_stride + (i * TEAM + sub) * 8, n[i], g[i], a.wide);
-        if (!a.z) {
-            if (a.drow_gate && sub == 0) a.drow_gate[row] = 0.0f;
-            continue;
-        }
-        const float rg = a.row_gate ? a.row_gate[row] : 1.0f;
-        Stat s = {0.0f, 0.0f, 1.0f};
-        if (post) s = row_stat<TEAM, CHUNKS>(z, n, a.after.kind, a.after.eps, a.inv_cols, team);
-        float t[3] = {0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (uint32_t i = 0; i < CHUNKS; ++i) {
-            const uint32_t c = (i * TEAM + sub) * 8;
-            float gate[8], w[8], h[8];
-#pragma unroll
-            for (uint32_t j = 0; j < 8; ++j) {
-                g[i][j] = c + j < a.cols ? a.scale * g[i][j] : 0.0f;  // at gate * row_gate * h
-                h[j] = z[i][j];
-                w[j] = 1.0f;
-            }
-            if (post) {
-                load_param(a.after.w, c, n[i], 1.0f, w);
-#pragma unroll
-                for (uint32_t j = 0; j < 8; ++j) h[j] = normed(h[j], s) * w[j];
-                if (a.after.b.p) {
-                    float b[8];
-                    load_param(a.after.b, c, n[i], 0.0f, b);
-#pragma unroll
-                    for (uint32_t j = 0; j < 8; ++j) h[j] += b[j];
-                }
-            }
-            load_param(a.gate, c, n[i], 1.0f, gate);
-#pragma unroll
-            for (uint32_t j = 0; j < 8; ++j) {
-                dgate[i][j] = fmaf(rg * g[i][j], h[j], dgate[i][j]);
-                t[0] = fmaf(gate[j] * g[i][j], h[j], t[0]);
-                const float dh = rg * gate[j] * g[i][j], v = normed(z[i][j], s);
-                dw1[i][j] = fmaf(dh, v, dw1[i][j]);
-                if (BIAS) db1[BIAS ? i : 0][j] += dh;
-                g[i][j] = dh * w[j];
-                t[1] = fmaf(g[i][j], v, t[1]);
-                t[2] += g[i][j];
-            }
-        }
-        if (a.drow_gate || (post && a.dz)) team.sum(t);
-        if (a.drow_gate && sub == 0) a.drow_gate[row] = t[0];
-        if (!a.dz) continue;
-        const float m0 = t[1] * a.inv_cols, m1 = a.after.kind == ZC_NORM_LAYER ? t[2] * a.inv_cols : 0.0f;
-#pragma unroll
-        for (uint32_t i = 0; i < CHUNKS; ++i) {
-            if (post)
-#pragma unroll
-                for (uint32_t j = 0; j < 8; ++j)
-                    g[i][j] = (fmaf(-normed(z[i][j], s), m0, g[i][j]) - m1) * s.k;
-            store_bf(a.dz + row * a.dz_stride + (i * TEAM + sub) * 8, pack8(g[i]), n[i], a.wide);
-        }
-    }
-#pragma unroll
-    for (uint32_t i = 0; i < CHUNKS; ++i) {
-        const auto leave = [&](uint32_t sum, const float (&v)[8]) {
-            if (a.sums >> sum & 1)
-                store_floats(a.parts + sum * a.part_stride + (uint64_t)index * a.cols + (i * TEAM + sub) * 8, n[i], v);
-        };
-        leave(kDW1, dw1[i]);
-        leave(kDGate, dgate[i]);
-        leave(kDW2, dw2[i]);
-        if (BIAS) {
-            leave(kDB1, db1[BIAS ? i : 0]);
-            leave(kDB2, db2[BIAS ? i : 0]);
-        }
-    }
-}
-
-// ---------------------------------------------------------------------------
-// whole rows
+// rows
 // ---------------------------------------------------------------------------
 
 // Both halves' statistics at once: x before the norm `before`, z before the norm `after`.
 // MEAN: one of them may be a LAYER norm.
 template <bool MEAN, uint32_t TEAM, uint32_t CHUNKS, typename X, typename Z>
 __device__ __forceinline__ void both_stats(const X &x, const Z &z, const uint32_t (&n)[CHUNKS], const NormArgs &a, bool pre,
-                                           bool post, Stat &sx, Stat &sz, Team<TEAM> &team) {
+                                           bool post, Stat &sx, Stat &sz, Team<TEAM> &team, float xt, float zt, bool in_tail) {
     float t[2] = {0.0f, 0.0f}, rest[2] = {0.0f, 0.0f};
     const bool lx = MEAN && pre && a.before.kind == ZC_NORM_LAYER, lz = MEAN && post && a.after.kind == ZC_NORM_LAYER;
     if (MEAN && (lx || lz)) {
         float u[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        float m[2] = {0.0f, 0.0f};
+        float m[2] = {xt, zt};
 #pragma unroll
         for (uint32_t i = 0; i < CHUNKS; ++i)
 #pragma unroll
@@ -177,6 +30,10 @@ __device__ __forceinline__ void both_stats(const X &x, const Z &z, const uint32_
         team.sum(m);
         sx.mean = lx ? m[0] * a.inv_cols : 0.0f;
         sz.mean = lz ? m[1] * a.inv_cols : 0.0f;
+        u[2] = in_tail ? xt - sx.mean : 0.0f;
+        u[3] = in_tail ? zt - sz.mean : 0.0f;
+        u[0] = u[2] * u[2];
+        u[1] = u[3] * u[3];
 #pragma unroll
         for (uint32_t i = 0; i < CHUNKS; ++i)
 #pragma unroll
@@ -195,6 +52,8 @@ __device__ __forceinline__ void both_stats(const X &x, const Z &z, const uint32_
 #pragma unroll
         for (uint32_t k = 0; k < 2; ++k) t[k] = t[k] < 0.0f ? 0.0f : t[k];
     } else {
+        t[0] = xt * xt;
+        t[1] = zt * zt;
 #pragma unroll
         for (uint32_t i = 0; i < CHUNKS; ++i)
 #pragma unroll
@@ -214,52 +73,116 @@ __device__ __forceinline__ void both_stats(const X &x, const Z &z, const uint32_
     }
     // squares outside the range of a float: one row at a time
     if (pre && (!(t[0] <= 0x1p120f) || (t[0] < 0x1p-80f && a.before.eps < 0x1p-58f)))
-        sx = row_stat<TEAM, CHUNKS>(x, n, a.before.kind, a.before.eps, a.inv_cols, team);
+        sx = row_stat<TEAM, CHUNKS>(x, n, a.before.kind, a.before.eps, a.inv_cols, team, xt, in_tail);
     if (post && (!(t[1] <= 0x1p120f) || (t[1] < 0x1p-80f && a.after.eps < 0x1p-58f)))
-        sz = row_stat<TEAM, CHUNKS>(z, n, a.after.kind, a.after.eps, a.inv_cols, team);
+        sz = row_stat<TEAM, CHUNKS>(z, n, a.after.kind, a.after.eps, a.inv_cols, team, zt, in_tail);
 }
 
-// As the kernel above, with the next row's loads on their way while a row is worked on, weights and gate in
-// registers, and no branch around a load or store.  ANY: with biases, means and the rows' gates; without it about
-// 34 instructions a value, which bound the kernel beside the memory: 8192 x 7168 takes 184 us with ANY and 128
-// without, 5.5 TB/s, past what a large copy reaches.
-template <bool F32S, bool F32P, bool ANY, uint32_t TEAM, uint32_t CHUNKS>
-__global__ __launch_bounds__(block_threads(TEAM)) void norm_backward_whole_kernel(NormArgs a) {
+// With v^ the normed value and u = dy * w the gradient there, that of v is
+//   1 / deviation * (u - v^ mean(u v^) [- mean(u) for LAYER]).
+// A team's lanes keep their columns from row to row, so the sums over the rows
+// stay in registers until the team's last row and leave as one part a team; a
+// second launch adds the parts in order.  The next row's loads are on their way while a row is worked on,
+// and weights and gate stay in registers.  Values past a row's end read as 0, have a gradient of 0, and add nothing.
+//
+// ANY: with biases, means and the rows' gates; without, about 34 instructions a value, which bound the kernel
+// beside the memory: 8192 x 7168 takes 184 us with ANY and 128 without, 5.5 TB/s, past what a large copy
+// reaches (246 without the loads ahead, and with loads under conditions).  Its registers would not hold the parameters
+// beside five sums: ANY has them as floats in LDS, or, of rows past 8192, in memory.  WIDE: as in the forward kernel.
+template <bool F32S, bool F32P, bool WIDE, bool ANY, uint32_t TEAM, uint32_t CHUNKS>
+__global__ __launch_bounds__(block_threads(TEAM)) void norm_backward_kernel(NormArgs a) {
     __shared__ float parts[2][kMaxWaves][4];
     Team<TEAM> team = {parts, 0};
-    const uint32_t sub = threadIdx.x % TEAM;
+    const uint32_t sub = threadIdx.x % TEAM, whole = a.cols / 8 * 8, ct = whole + sub;
+    const bool in_tail = !WIDE && ct < a.cols;
     const uint32_t index = (uint32_t)__builtin_amdgcn_readfirstlane(blockIdx.x * block_teams(TEAM) + threadIdx.x / TEAM);
     uint32_t n[CHUNKS];
     float dw1[CHUNKS][8], dgate[CHUNKS][8], dw2[CHUNKS][8], db1[ANY ? CHUNKS : 1][8], db2[ANY ? CHUNKS : 1][8];
-    Eight<F32P> w1[CHUNKS], gate[CHUNKS], w2[CHUNKS];
+    enum { kW1, kB1, kGate, kW2, kParams };
+    constexpr bool kInLds = ANY && TEAM * CHUNKS <= 1024;
+    constexpr uint32_t kRegs = ANY ? 1 : CHUNKS;
+    Eight<F32P> w1[kRegs], gate[kRegs], w2[kRegs];
+    // (a lane's values in two places, so that lanes side by side read 16 bytes side by side)
+    __shared__ alignas(16) float kept[kInLds ? kParams : 1][2][kInLds ? TEAM * CHUNKS * 4 : 4];
     const bool pre = a.dy && a.before.kind != ZC_NORM_NONE, post = a.z && a.after.kind != ZC_NORM_NONE;
 #pragma unroll
     for (uint32_t i = 0; i < CHUNKS; ++i) {
         const uint32_t c = (i * TEAM + sub) * 8;
-        n[i] = c < a.cols ? 8u : 0u;
-        keep_param<F32P>(post ? a.after.w : Param{}, c, n[i], 1.0f, w1[i]);
-        keep_param<F32P>(a.z ? a.gate : Param{}, c, n[i], 1.0f, gate[i]);
-        keep_param<F32P>(pre ? a.before.w : Param{}, c, n[i], 1.0f, w2[i]);
+        n[i] = c < whole ? 8u : 0u;
+        if (!ANY) {
+            keep_param<F32P>(post ? a.after.w : Param{}, c, n[i], 1.0f, w1[ANY ? 0 : i]);
+            keep_param<F32P>(a.z ? a.gate : Param{}, c, n[i], 1.0f, gate[ANY ? 0 : i]);
+            keep_param<F32P>(pre ? a.before.w : Param{}, c, n[i], 1.0f, w2[ANY ? 0 : i]);
+        }
 #pragma unroll
         for (uint32_t j = 0; j < 8; ++j) {
             dw1[i][j] = dgate[i][j] = dw2[i][j] = 0.0f;
             if (ANY) db1[ANY ? i : 0][j] = db2[ANY ? i : 0][j] = 0.0f;
         }
     }
+    const auto param = [&](uint32_t k) -> Param {
+        return k == kGate ? (a.z ? a.gate : Param{}) : k == kW2 ? (pre ? a.before.w : Param{}) : !post ? Param{} : k == kW1 ? a.after.w : a.after.b;
+    };
+    if constexpr (kInLds) {
+        for (uint32_t q = threadIdx.x; q < TEAM * CHUNKS; q += block_threads(TEAM))
+#pragma unroll
+            for (uint32_t k = 0; k < kParams; ++k) {
+                Eight<true> v;
+                keep_param<true>(param(k), 8 * q, 8 * q < whole ? 8u : 0u, k == kB1 ? 0.0f : 1.0f, v);
+                *reinterpret_cast<u32v4 *>(&kept[k][0][4 * q]) = v.w[0];
+                *reinterpret_cast<u32v4 *>(&kept[k][1][4 * q]) = v.w[1];
+            }
+        __syncthreads();
+    }
+    // parameter k of a lane's chunk i
+    const auto values = [&](auto k_t, uint32_t i, float (&v)[8]) {
+        constexpr uint32_t k = decltype(k_t)::value;
+        if constexpr (kInLds) {
+            const float *at = &kept[k][0][(i * TEAM + sub) * 4];
+#pragma unroll
+            for (uint32_t j = 0; j < 8; ++j) v[j] = at[j / 4 * (TEAM * CHUNKS * 4) + (j & 3)];
+        } else if constexpr (ANY) {
+            load_param(param(k), (i * TEAM + sub) * 8, n[i], k == kB1 ? 0.0f : 1.0f, v);
+#pragma unroll
+            for (uint32_t j = 0; j < 8; ++j) v[j] = n[i] ? v[j] : 0.0f;
+        } else {
+            const Eight<F32P> &e = k == kW1 ? w1[i % kRegs] : k == kGate ? gate[i % kRegs] : w2[i % kRegs];
+#pragma unroll
+            for (uint32_t j = 0; j < 8; ++j) v[j] = k == kB1 ? 0.0f : e[j];
+        }
+    };
+    typedef std::integral_constant<uint32_t, kW1> W1;
+    typedef std::integral_constant<uint32_t, kB1> B1;
+    typedef std::integral_constant<uint32_t, kGate> Gate;
+    typedef std::integral_constant<uint32_t, kW2> W2;
+    const float w1t = keep_tail(post ? a.after.w : Param{}, ct, in_tail, 1.0f);
+    const float b1t = ANY ? keep_tail(post ? a.after.b : Param{}, ct, in_tail, 0.0f) : 0.0f;
+    const float gatet = keep_tail(a.z ? a.gate : Param{}, ct, in_tail, 1.0f);
+    const float w2t = keep_tail(pre ? a.before.w : Param{}, ct, in_tail, 1.0f);
+    float dw1t = 0.0f, db1t = 0.0f, dgatet = 0.0f, dw2t = 0.0f, db2t = 0.0f;
     struct Loaded {
         Eight<F32S> x[CHUNKS], dr[CHUNKS];
         Eight<false> z[CHUNKS], dy[CHUNKS];
+        float xt, drt, zt, dyt;
     };
     const auto fetch = [&](uint32_t t, Loaded &v) {
-        const Row rx = row_of(a.x, t * a.x_stride, a.cols, F32S ? 4 : 2), rz = row_of(a.z, t * a.z_stride, a.cols, 2);
-        const Row rd = row_of(a.dr, t * a.dr_stride, a.cols, F32S ? 4 : 2), ry = row_of(a.dy, t * a.dy_stride, a.cols, 2);
+        constexpr uint32_t size = F32S ? 4 : 2;
+        const Row rx = row_of(a.x, t * a.x_stride, whole, size), rz = row_of(a.z, t * a.z_stride, whole, 2);
+        const Row rd = row_of(a.dr, t * a.dr_stride, whole, size), ry = row_of(a.dy, t * a.dy_stride, whole, 2);
 #pragma unroll
         for (uint32_t i = 0; i < CHUNKS; ++i) {
             const uint32_t c = (i * TEAM + sub) * 8;
-            load_row<F32S>(rx, c, v.x[i]);
-            load_row<false>(rz, c, v.z[i]);
-            load_row<false>(ry, c, v.dy[i]);
-            load_row<F32S>(rd, c, v.dr[i]);
+            load_row<F32S, WIDE>(rx, c, v.x[i]);
+            load_row<false, WIDE>(rz, c, v.z[i]);
+            load_row<false, WIDE>(ry, c, v.dy[i]);
+            load_row<F32S, WIDE>(rd, c, v.dr[i]);
+        }
+        v.xt = v.drt = v.zt = v.dyt = 0.0f;
+        if (!WIDE) {
+            v.xt = load_tail<F32S>(row_of(a.x, t * a.x_stride, a.cols, size), ct);
+            v.zt = load_tail<false>(row_of(a.z, t * a.z_stride, a.cols, 2), ct);
+            v.dyt = load_tail<false>(row_of(a.dy, t * a.dy_stride, a.cols, 2), ct);
+            v.drt = load_tail<F32S>(row_of(a.dr, t * a.dr_stride, a.cols, size), ct);
         }
     };
     const uint32_t step = gridDim.x * block_teams(TEAM);
@@ -270,14 +193,14 @@ __global__ __launch_bounds__(block_threads(TEAM)) void norm_backward_whole_kerne
         Loaded next;
         fetch(row + step < a.rows ? row + step : a.rows - 1, next);
 #pragma unroll
-        for (uint32_t i = 0; i < CHUNKS; ++i) {
+        for (uint32_t i = 0; i < kRegs; ++i) {
             stay_packed(w1[i]);
             stay_packed(gate[i]);
             stay_packed(w2[i]);
         }
         const float rg = ANY && a.row_gate ? a.row_gate[row] : 1.0f;
         Stat sx = {0.0f, 0.0f, 1.0f}, sz = sx;
-        if (pre || post) both_stats<ANY, TEAM, CHUNKS>(v.x, v.z, n, a, pre, post, sx, sz, team);
+        if (pre || post) both_stats<ANY, TEAM, CHUNKS>(v.x, v.z, n, a, pre, post, sx, sz, team, v.xt, v.zt, in_tail);
 #pragma unroll
         for (uint32_t i = 0; i < CHUNKS; ++i) {
             stay_packed(v.x[i]);
@@ -286,19 +209,31 @@ __global__ __launch_bounds__(block_threads(TEAM)) void norm_backward_whole_kerne
             stay_packed(v.dr[i]);
         }
         float g[CHUNKS][8];  // the gradient of r
+        float gt = 0.0f;
         if (pre) {
             float t[2] = {0.0f, 0.0f};
+            const float ht = WIDE ? 0.0f : normed<ANY>(v.xt, sx);
+            if (!WIDE) {
+                dw2t = fmaf(v.dyt, ht, dw2t);
+                if (ANY) db2t += v.dyt;
+                gt = v.dyt * w2t;
+                t[0] = gt * ht;
+                if (ANY) t[1] = gt;
+            }
 #pragma unroll
-            for (uint32_t i = 0; i < CHUNKS; ++i)
+            for (uint32_t i = 0; i < CHUNKS; ++i) {
+                float w[8];
+                values(W2{}, i, w);
 #pragma unroll
                 for (uint32_t j = 0; j < 8; ++j) {
                     const float h = normed<ANY>(v.x[i][j], sx), d = v.dy[i][j];
                     dw2[i][j] = fmaf(d, h, dw2[i][j]);
                     if (ANY) db2[ANY ? i : 0][j] += d;
-                    g[i][j] = d * w2[i][j];
+                    g[i][j] = d * w[j];
                     t[0] = fmaf(g[i][j], h, t[0]);
                     if (ANY) t[1] += g[i][j];
                 }
+            }
             float m0, m1 = 0.0f;
             if (ANY) {
                 team.sum(t);
@@ -308,6 +243,10 @@ __global__ __launch_bounds__(block_threads(TEAM)) void norm_backward_whole_kerne
                 float u[1] = {t[0]};
                 team.sum(u);
                 m0 = u[0] * a.inv_cols;
+            }
+            if (!WIDE) {
+                const float u = fmaf(-ht, m0, gt);
+                gt = fmaf(ANY ? u - m1 : u, sx.k, v.drt);
             }
 #pragma unroll
             for (uint32_t i = 0; i < CHUNKS; ++i) stay_packed(v.x[i]);
@@ -319,31 +258,46 @@ __global__ __launch_bounds__(block_threads(TEAM)) void norm_backward_whole_kerne
                     g[i][j] = fmaf(ANY ? u - m1 : u, sx.k, v.dr[i][j]);
                 }
         } else {
+            gt = v.drt + v.dyt;
 #pragma unroll
             for (uint32_t i = 0; i < CHUNKS; ++i)
 #pragma unroll
                 for (uint32_t j = 0; j < 8; ++j) g[i][j] = v.dr[i][j] + v.dy[i][j];
         }
-        const Row rr = row_of(a.r, row * a.r_stride, a.cols, F32S ? 4 : 2);
+        const Row rr = row_of(a.r, row * a.r_stride, whole, F32S ? 4 : 2);
 #pragma unroll
-        for (uint32_t i = 0; i < CHUNKS; ++i) store_row<F32S>(rr, (i * TEAM + sub) * 8, g[i]);
+        for (uint32_t i = 0; i < CHUNKS; ++i) store_row<F32S, WIDE>(rr, (i * TEAM + sub) * 8, g[i]);
+        if (!WIDE) store_tail<F32S>(row_of(a.r, row * a.r_stride, a.cols, F32S ? 4 : 2), ct, gt);
         const float share = ANY ? a.scale * rg : a.scale;
         float t[3] = {0.0f, 0.0f, 0.0f};
+        const float zht = WIDE ? 0.0f : normed<ANY>(v.zt, sz);
+        if (!WIDE) {
+            const float e = in_tail ? gt : 0.0f, q = e * fmaf(zht, w1t, b1t), dh = gatet * e * share;
+            dgatet = fmaf(share, q, dgatet);
+            if (ANY) t[2] = gatet * q;
+            dw1t = fmaf(dh, zht, dw1t);
+            if (ANY) db1t += dh;
+            gt = dh * w1t;
+            t[0] = gt * zht;
+            if (ANY) t[1] = gt;
+        }
 #pragma unroll
         for (uint32_t i = 0; i < CHUNKS; ++i) {
-            float b[8];
-            if (ANY && post && a.after.b.p) load_param(a.after.b, (i * TEAM + sub) * 8, n[i], 0.0f, b);
+            float b[8], w[8], gate_v[8];
+            values(W1{}, i, w);
+            values(Gate{}, i, gate_v);
+            values(B1{}, i, b);
 #pragma unroll
             for (uint32_t j = 0; j < 8; ++j) {
                 const float zh = normed<ANY>(v.z[i][j], sz);  // z itself without a norm
-                const float h = ANY && post && a.after.b.p ? fmaf(zh, w1[i][j], b[j]) : zh * w1[i][j];
+                const float h = ANY ? fmaf(zh, w[j], b[j]) : zh * w[j];
                 const float e = ANY ? (n[i] ? g[i][j] : 0.0f) : g[i][j], q = e * h;
                 dgate[i][j] = fmaf(share, q, dgate[i][j]);
-                if (ANY) t[2] = fmaf(gate[i][j], q, t[2]);
-                const float dh = gate[i][j] * e * share;
+                if (ANY) t[2] = fmaf(gate_v[j], q, t[2]);
+                const float dh = gate_v[j] * e * share;
                 dw1[i][j] = fmaf(dh, zh, dw1[i][j]);
                 if (ANY) db1[ANY ? i : 0][j] += dh;
-                g[i][j] = dh * w1[i][j];
+                g[i][j] = dh * w[j];
                 t[0] = fmaf(g[i][j], zh, t[0]);
                 if (ANY) t[1] += g[i][j];
             }
@@ -359,7 +313,14 @@ __global__ __launch_bounds__(block_threads(TEAM)) void norm_backward_whole_kerne
             team.sum(u);
             m0 = u[0] * a.inv_cols;
         }
-        const Row rz = row_of(a.dz, row * a.dz_stride, a.cols, 2);
+        const Row rz = row_of(a.dz, row * a.dz_stride, whole, 2);
+        if (!WIDE) {
+            if (post) {
+                const float u = fmaf(-zht, m0, gt);
+                gt = (ANY ? u - m1 : u) * sz.k;
+            }
+            store_tail<false>(row_of(a.dz, row * a.dz_stride, a.cols, 2), ct, gt);
+        }
 #pragma unroll
         for (uint32_t i = 0; i < CHUNKS; ++i) {
             stay_packed(v.z[i]);
@@ -369,16 +330,16 @@ __global__ __launch_bounds__(block_threads(TEAM)) void norm_backward_whole_kerne
                     const float u = fmaf(-normed<ANY>(v.z[i][j], sz), m0, g[i][j]);
                     g[i][j] = (ANY ? u - m1 : u) * sz.k;
                 }
-            store_row<false>(rz, (i * TEAM + sub) * 8, g[i]);
+            store_row<false, WIDE>(rz, (i * TEAM + sub) * 8, g[i]);
         }
         row += step;
         v = next;
     }
+    const auto part = [&](uint32_t sum, uint32_t c) { return a.parts + sum * a.part_stride + (uint64_t)index * a.cols + c; };
 #pragma unroll
     for (uint32_t i = 0; i < CHUNKS; ++i) {
         const auto leave = [&](uint32_t sum, const float (&s)[8]) {
-            if (a.sums >> sum & 1)
-                store_floats(a.parts + sum * a.part_stride + (uint64_t)index * a.cols + (i * TEAM + sub) * 8, n[i], s);
+            if (a.sums >> sum & 1) store_floats(part(sum, (i * TEAM + sub) * 8), n[i], s);
         };
         leave(kDW1, dw1[i]);
         leave(kDGate, dgate[i]);
@@ -387,6 +348,17 @@ __global__ __launch_bounds__(block_threads(TEAM)) void norm_backward_whole_kerne
             leave(kDB1, db1[ANY ? i : 0]);
             leave(kDB2, db2[ANY ? i : 0]);
         }
+    }
+    if (!in_tail) return;
+    const auto leave = [&](uint32_t sum, float s) {
+        if (a.sums >> sum & 1) *part(sum, ct) = s;
+    };
+    leave(kDW1, dw1t);
+    leave(kDGate, dgatet);
+    leave(kDW2, dw2t);
+    if (ANY) {
+        leave(kDB1, db1t);
+        leave(kDB2, db2t);
     }
 }
 
@@ -423,15 +395,15 @@ __global__ __launch_bounds__(kLanes * kSumRuns) void norm_sums_kernel(SumArgs a)
 // host
 // ---------------------------------------------------------------------------
 
-static void launch_backward(const NormArgs &a, const Shape &s, bool whole, bool f32, bool f32p, bool any, dim3 grid,
+static void launch_backward(const NormArgs &a, const Shape &s, bool wide, bool f32, bool f32p, bool any, dim3 grid,
                             Launches &on) {
     with_shape(s, [&](auto team, auto chunks) {
         constexpr uint32_t T = decltype(team)::value, C = decltype(chunks)::value;
         const auto pick = [&](auto f32_t, auto any_t) {
-            constexpr bool S = decltype(f32_t)::value, B = decltype(any_t)::value;
-            on.launch(!whole ? norm_backward_kernel<S, B, T, C>
-                      : f32p ? norm_backward_whole_kernel<S, true, B, T, C>
-                             : norm_backward_whole_kernel<S, false, B, T, C>,
+            constexpr bool S = decltype(f32_t)::value, A = decltype(any_t)::value;
+            // (with ANY the parameters' type in registers does not matter)
+            on.launch(f32p && !A ? (wide ? norm_backward_kernel<S, !A, true, A, T, C> : norm_backward_kernel<S, !A, false, A, T, C>)
+                                 : (wide ? norm_backward_kernel<S, false, true, A, T, C> : norm_backward_kernel<S, false, false, A, T, C>),
                       grid, dim3(block_threads(T)), a);
         };
         if (f32)
@@ -518,17 +490,13 @@ extern "C" zc_status zc_norm_backward(const void *d_r, uint32_t stream_type, uin
         sum.parts = a.parts;
     }
     const bool f32 = stream_type == ZC_F32;
-    a.wide = cols % 8 == 0 && wide8(d_dx, dx_stride, f32) && wide8(d_dz, dz_stride);
-    const bool whole = a.wide && wide8(d_r, r_stride, f32) && wide8(d_dr, dr_stride, f32) && wide8(d_dy, dy_stride) &&
-                       wide8(d_z, z_stride);
-    // sums of the biases; in whole rows also means, biases and the rows' gates
-    bool any = a.sums & (1u << kDB1 | 1u << kDB2);
-    if (whole)
-        any |= (d_dy && a.before.kind == ZC_NORM_LAYER) || (d_z && (a.after.kind == ZC_NORM_LAYER || a.after.b.p)) ||
-               (d_z && a.row_gate) || row_gate;
+    const bool wide = cols % 8 == 0 && wide8(d_dx, dx_stride, f32) && wide8(d_dz, dz_stride) && wide8(d_r, r_stride, f32) &&
+                      wide8(d_dr, dr_stride, f32) && wide8(d_dy, dy_stride) && wide8(d_z, z_stride);
+    const bool any = a.sums & (1u << kDB1 | 1u << kDB2) || a.before.kind == ZC_NORM_LAYER || a.after.kind == ZC_NORM_LAYER ||
+                     (a.after.kind != ZC_NORM_NONE && a.after.b.p) || a.row_gate || row_gate;
     Launches on(stream);
     if (rows && (a.sums || d_dx || d_dz || row_gate))
-        launch_backward(a, s, whole, f32, any_float(*cfg, d_z != nullptr), any, dim3((uint32_t)blocks), on);
+        launch_backward(a, s, wide, f32, any_float(*cfg, d_z != nullptr), any, dim3((uint32_t)blocks), on);
     if (asked) on.launch(norm_sums_kernel, dim3((uint32_t)ceil_div(cols, kLanes), kSums), dim3(kLanes * kSumRuns), sum);
     return on.status();
 }

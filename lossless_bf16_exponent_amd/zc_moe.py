@@ -238,45 +238,50 @@ def zc_swiglu_backward(d_kept, d_kept_scales, rows, cols, d_dh, dh_stride, d_dga
                                    _ptr(d_dgate_up), gu_stride, _stream(stream)), "zc_swiglu_backward")
 
 
+_types = {}  # of torch, once it is loaded
+
+
 def _type_of(x, given) -> int:
     """The ZC_ type of a parameter: as given, or that of a float32 or bfloat16 tensor; ZC_F32 where there is none."""
     if given is not None:
-        return int(given)
+        return given
     if x is None:
         return ZC_F32
     if isinstance(x, int):
         raise TypeError("the type of an address has to be given")
-    return {"torch.float32": ZC_F32, "torch.bfloat16": ZC_BF16}[str(x.dtype)]
+    if not _types:
+        import torch
+        _types.update({torch.float32: ZC_F32, torch.bfloat16: ZC_BF16})
+    return _types[x.dtype]
 
 
-def _same_type(w, b, given) -> int:
-    t = _type_of(b if w is None else w, given)
-    if given is None and w is not None and b is not None and _type_of(b, None) != t:
-        raise TypeError("weight and bias have different types")
-    return t
-
-
-# The structures hold addresses: `keep` holds what they belong to for as long.
+# The structures hold addresses: `keep` holds what they belong to for as long.  They are made within a few
+# microseconds too.
 
 def norm_params(kind, weight=None, bias=None, eps=1e-6, type=None) -> zc_norm_params:
     """One norm; kind: a ZC_NORM_ value; type: of weight and bias, by default their tensors'."""
-    p = zc_norm_params(_ptr(weight), _ptr(bias), int(kind), _same_type(weight, bias, type), float(eps))
-    p.keep = (weight, bias)
+    t = _type_of(bias if weight is None else weight, type)
+    if type is None and weight is not None and bias is not None and _type_of(bias, None) != t:
+        raise TypeError("weight and bias have different types")
+    p = zc_norm_params(_ptr(weight), _ptr(bias), kind, t, eps)
+    p.keep = weight, bias
     return p
+
+
+_no_norm = norm_params(ZC_NORM_NONE)
 
 
 def norm_config(after=None, before=None, gate=None, row_gate=None, scale=1.0, gate_type=None) -> zc_norm_config:
     """after, before: norm_params, or None for no norm."""
-    after, before = after or norm_params(ZC_NORM_NONE), before or norm_params(ZC_NORM_NONE)
-    c = zc_norm_config(after, before, _ptr(gate), _ptr(row_gate), _type_of(gate, gate_type), float(scale))
-    c.keep = (after.keep, before.keep, gate, row_gate)
+    c = zc_norm_config(after or _no_norm, before or _no_norm, _ptr(gate), _ptr(row_gate), _type_of(gate, gate_type), scale)
+    c.keep = after, before, gate, row_gate
     return c
 
 
 def norm_grads(weight_after=None, bias_after=None, gate=None, weight_before=None, bias_before=None,
                row_gate=None) -> zc_norm_grads:
-    g = zc_norm_grads(*(_ptr(v) for v in (weight_after, bias_after, gate, weight_before, bias_before, row_gate)))
-    g.keep = (weight_after, bias_after, gate, weight_before, bias_before, row_gate)
+    g = zc_norm_grads(_ptr(weight_after), _ptr(bias_after), _ptr(gate), _ptr(weight_before), _ptr(bias_before), _ptr(row_gate))
+    g.keep = weight_after, bias_after, gate, weight_before, bias_before, row_gate
     return g
 
 
@@ -284,8 +289,8 @@ def epilogue(bias=None, activation=ZC_ACT_NONE, residual=None, residual_stride=0
              bias_type=None, residual_type=None) -> zc_epilogue:
     """bias_type, residual_type: by default those of their tensors."""
     e = zc_epilogue(_ptr(bias), _ptr(residual), _ptr(pre), residual_stride, pre_stride, _type_of(bias, bias_type),
-                    _type_of(residual, residual_type), int(activation), float(scale))
-    e.keep = (bias, residual, pre)
+                    _type_of(residual, residual_type), activation, scale)
+    e.keep = bias, residual, pre
     return e
 
 
