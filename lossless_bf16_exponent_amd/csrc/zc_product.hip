@@ -35,7 +35,9 @@ struct ProductArgs {
     uint32_t m, n, k;   // results' rows and columns, contraction
     uint32_t blocks;    // blocks of 64 along the contraction
     uint32_t direct;    // of which the first so many may be loaded whole, 16 bytes at a time
-    float *parts;       // a split contraction's sums, gridDim.y of them; or NULL
+    uint32_t whole;     // so many tiles take all of it; of those that follow, each is `splits` parts
+    uint32_t splits;
+    float *parts;       // the sums of the parts, tile by tile
     Epilogue e;
 };
 
@@ -305,12 +307,27 @@ struct Operand {
     }
 };
 
+__device__ __forceinline__ uint32_t up8(uint32_t n) { return (n + 7) / 8 * 8; }
+// The id-th tile in bands of eight rows of tiles, column by column.
+struct TilePlace {
+    uint32_t row, col;
+};
+__device__ __forceinline__ TilePlace tile_place(uint32_t id, uint32_t mtiles, uint32_t ntiles) {
+    const uint32_t band = id / (8 * ntiles), in_band = id % (8 * ntiles), band_rows = min(8u, mtiles - 8 * band);
+    return {8 * band + in_band % band_rows, in_band / band_rows};
+}
+
 // BM x BN tile of four waves (2 x 2).  DIRECT: whole blocks go from memory straight
 // into LDS, STAGES of them under way, in the order of the 8-bit products' tiles: the
 // fragments of half a block are in registers while the other half's come out
 // of LDS, and one barrier in the middle of a block frees its place and hands over
-// the next.  Without DIRECT (operands at any element, rows far apart) a block goes
-// through registers while the one before it is multiplied, and so does the contraction's ragged end.
+// the next.  Without DIRECT (operands at any element, rows far apart) blocks go
+// through registers, two on their way while the one before them is multiplied, and so does the
+// contraction's ragged end.  Rates, operands from memory: 8192^3 774 us (1420 TFLOP/s; the library
+// reaches 1365), 8192 x 4096 x 7168 347 us (1390 TFLOP/s, bound by the matrix instructions and, past
+// those, by the clock under them), 8192 x 256 x 7168 in two parts 34 us (bound by reading 121 MB),
+// 48 x 14336 x 4096 21.6 us (117 MB); without DIRECT 1024 x 4096 x 7168 105 us, rows at odd elements
+// 125: a wave's loads, its reads of LDS and its products then follow each other with one wave a SIMD.
 template <uint32_t BM, uint32_t BN, uint32_t STAGES, bool XA, bool XB, bool DIRECT>
 __global__ __launch_bounds__(kPThreads, STAGES * (BM + BN) * kPBytes > 80 * 1024 ? 1 : 2) void product_kernel(ProductArgs p) {
     typedef Operand<BM, XA> OA;
@@ -326,13 +343,24 @@ __global__ __launch_bounds__(kPThreads, STAGES * (BM + BN) * kPBytes > 80 * 1024
     // tiles, in bands of eight rows of tiles, column by column, so that its CUs
     // share rows of both operands in its L2.
     const uint32_t mtiles = (p.m + BM - 1) / BM, ntiles = (p.n + BN - 1) / BN, total = mtiles * ntiles;
-    const uint32_t xcd = blockIdx.x % 8, local = blockIdx.x / 8, per = total / 8, rest = total % 8;
+    // The tiles past p.whole are split: first the whole tiles, then part after part.
+    uint32_t group = blockIdx.x, count = p.whole, part = 0;
+    const bool split = group >= up8(p.whole);
+    if (split) {
+        count = total - p.whole;
+        group -= up8(p.whole);
+        part = group / up8(count);
+        group -= part * up8(count);
+    }
+    const uint32_t xcd = group % 8, local = group / 8, per = count / 8, rest = count % 8;
     if (local >= per + (xcd < rest)) return;
-    const uint32_t id = xcd * per + min(xcd, rest) + local;
-    const uint32_t band = id / (8 * ntiles), in_band = id % (8 * ntiles), band_rows = min(8u, mtiles - 8 * band);
-    const uint32_t m0 = (8 * band + in_band % band_rows) * BM, n0 = in_band / band_rows * BN;
-    const uint32_t kb0 = (uint32_t)((uint64_t)p.blocks * blockIdx.y / gridDim.y);
-    const uint32_t kb1 = (uint32_t)((uint64_t)p.blocks * (blockIdx.y + 1) / gridDim.y);
+    const uint32_t nth = xcd * per + min(xcd, rest) + local;
+    const TilePlace place = tile_place(split ? p.whole + nth : nth, mtiles, ntiles);
+    // (the same in every lane, which the loads into LDS need known)
+    const auto same = [](uint32_t v) { return (uint32_t)__builtin_amdgcn_readfirstlane(v); };
+    const uint32_t m0 = same(place.row * BM), n0 = same(place.col * BN);
+    const uint32_t kb0 = same(split ? (uint32_t)((uint64_t)p.blocks * part / p.splits) : 0u);
+    const uint32_t kb1 = same(split ? (uint32_t)((uint64_t)p.blocks * (part + 1) / p.splits) : p.blocks);
 
     OA oa = {p.a, p.lda, m0, p.m - 1, p.k};
     OB ob = {p.b, p.ldb, n0, p.n - 1, p.k};
@@ -433,7 +461,7 @@ __global__ __launch_bounds__(kPThreads, STAGES * (BM + BN) * kPBytes > 80 * 1024
             const uint32_t to = i < LA ? (wave * LA + i) * 1024 : BM * kPBytes + (wave * LB + i - LA) * 1024;
             *reinterpret_cast<u32v4 *>(sh + at + to + 16 * lane) = w[i];
         }
-        __syncthreads();
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // (the loads under way are not waited for)
     };
     const auto take_block = [&](uint32_t at) {
 #pragma unroll
@@ -447,25 +475,29 @@ __global__ __launch_bounds__(kPThreads, STAGES * (BM + BN) * kPBytes > 80 * 1024
         }
     };
     if constexpr (!DIRECT) if (kb0 < whole) {
-        // two places in turn: one is written while other waves may still read the other
+        // two places in turn: one is written while other waves may still read the other; two blocks on their way
         static_assert(STAGES == 2, "two places");
         const uint16_t *from[LOADS];
-        u32v4 w[LOADS];
+        u32v4 w[2][LOADS];
 #pragma unroll
-        for (uint32_t i = 0; i < LOADS; ++i) {
-            from[i] = i < LA ? oa.source(kb0, wave, i) : ob.source(kb0, wave, i - LA);
-            w[i] = *reinterpret_cast<const u32v4a2 *>(from[i]);
-        }
-        for (uint32_t kb = kb0; kb < whole; ++kb) {
-            const uint32_t at = ((kb - kb0) & 1) * kStage;
-            lay_block(at, w);
-            if (kb + 1 < whole)
+        for (uint32_t i = 0; i < LOADS; ++i) from[i] = i < LA ? oa.source(kb0, wave, i) : ob.source(kb0, wave, i - LA);
+        const uint64_t last = whole - 1 - kb0;
+        // (past the last whole block that one again: no branch around the loads, so that each is waited for by itself)
+        const auto fetch_block = [&](uint64_t t, u32v4 (&to)[LOADS]) {
 #pragma unroll
-                for (uint32_t i = 0; i < LOADS; ++i) {
-                    from[i] += (i < LA ? oa.step() : ob.step()) / 2;
-                    w[i] = *reinterpret_cast<const u32v4a2 *>(from[i]);
-                }
-            take_block(at);
+            for (uint32_t i = 0; i < LOADS; ++i)
+                to[i] = *reinterpret_cast<const u32v4a2 *>(from[i] + min(t, last) * ((i < LA ? oa.step() : ob.step()) / 2));
+        };
+        fetch_block(0, w[0]);
+        fetch_block(1, w[1]);
+        for (uint32_t kb = kb0; kb < whole; kb += 2) {
+            lay_block(0, w[0]);
+            fetch_block(kb + 2 - kb0, w[0]);
+            take_block(0);
+            if (kb + 1 == whole) break;
+            lay_block(kStage, w[1]);
+            fetch_block(kb + 3 - kb0, w[1]);
+            take_block(kStage);
         }
     }
     for (uint32_t kb = max(whole, kb0); kb < kb1; ++kb) {
@@ -483,10 +515,11 @@ __global__ __launch_bounds__(kPThreads, STAGES * (BM + BN) * kPBytes > 80 * 1024
     // (8192 x 7168 x 4096 with a residual: 500 us instead of 381).
     __syncthreads();
     Epilogue e = p.e;
-    if (p.parts) {
+    if (split) {
         e = {};
-        e.out = p.parts + (uint64_t)blockIdx.y * p.m * p.n;
-        e.out_stride = p.n;
+        const uint64_t first = ((uint64_t)part * count + nth) * BM * BN - (uint64_t)m0 * BN - n0;
+        e.out = reinterpret_cast<float *>(reinterpret_cast<uint64_t>(p.parts) + first * 4);
+        e.out_stride = BN;
         e.out_f32 = 1;
         e.scale = 1.0f;
     }
@@ -540,7 +573,7 @@ __global__ __launch_bounds__(kPThreads, STAGES * (BM + BN) * kPBytes > 80 * 1024
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         }
     };
-    if (!acts && m0 + BM <= p.m && n0 + BN <= p.n) {
+    if (split || (!acts && m0 + BM <= p.m && n0 + BN <= p.n)) {  // (a part has room for the whole tile)
         typedef std::integral_constant<uint32_t, 0> None;
         typedef std::integral_constant<uint32_t, 1> Halves;
         typedef std::integral_constant<uint32_t, 2> Floats;
@@ -612,22 +645,26 @@ __global__ __launch_bounds__(kPThreads, STAGES * (BM + BN) * kPBytes > 80 * 1024
     }
 }
 
-// The parts of a split contraction, added in order.
-__global__ __launch_bounds__(256) void product_join_kernel(const float *parts, uint32_t splits, uint32_t m, uint32_t n,
-                                                           Epilogue e) {
-    const uint32_t per_row = (n + 7) / 8;
-    const uint64_t all = (uint64_t)m * per_row, part = (uint64_t)m * n;
+// The parts of split tiles of 1 << row_bits rows and 1 << col_bits columns, added in order.
+__global__ __launch_bounds__(256) void product_join_kernel(ProductArgs p, uint32_t row_bits, uint32_t col_bits) {
+    const uint32_t bits = row_bits + col_bits - 3;  // of eights of a tile
+    const uint32_t mtiles = (p.m + (1u << row_bits) - 1) >> row_bits, ntiles = (p.n + (1u << col_bits) - 1) >> col_bits;
+    const uint64_t all = (uint64_t)(mtiles * ntiles - p.whole) << bits;
     for (uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (uint64_t)gridDim.x * 256) {
-        const uint64_t r = i / per_row;
-        const uint32_t c = (uint32_t)(i % per_row) * 8, k = min(n - c, 8u);
-        float v[8], w[8];
-        load8(parts, 1, r * n + c, k, v);
-        for (uint32_t s = 1; s < splits; ++s) {
-            load8(parts, 1, s * part + r * n + c, k, w);
-#pragma unroll
-            for (uint32_t j = 0; j < 8; ++j) v[j] += w[j];
+        const TilePlace place = tile_place(p.whole + (uint32_t)(i >> bits), mtiles, ntiles);
+        const uint32_t in = (uint32_t)i & ((1u << bits) - 1);
+        const uint32_t r = (place.row << row_bits) + (in >> (col_bits - 3));
+        const uint32_t c = (place.col << col_bits) + (in & ((1u << (col_bits - 3)) - 1)) * 8;
+        if (r >= p.m || c >= p.n) continue;
+        const f32v4 *from = reinterpret_cast<const f32v4 *>(p.parts + i * 8);
+        f32v4 lo = from[0], hi = from[1];
+#pragma unroll 2
+        for (uint32_t s = 1; s < p.splits; ++s) {
+            lo += from[s * all * 2];
+            hi += from[s * all * 2 + 1];
         }
-        finish8(e, r, c, k, v);
+        float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        finish8(p.e, r, c, min(p.n - c, 8u), v);
     }
 }
 
@@ -821,7 +858,11 @@ enum Tile { kT128, kT128Deep, kT256x128, kT256, kT128x64, kT64, kTAny, kTAny64 }
 struct ProductChoice {
     uint32_t rows_mt;  // > 0: product_rows_kernel with so many tiles of 16 rows
     Tile tile;
-    uint32_t splits;
+    uint32_t tm, tn, splits;
+    uint64_t tiles, whole;  // the first so many tiles are not split
+
+    uint64_t groups() const { return splits > 1 ? ceil_div(whole, 8) * 8 + splits * (ceil_div(tiles - whole, 8) * 8) : ceil_div(tiles, 8) * 8; }
+    uint64_t part_bytes() const { return splits > 1 ? (tiles - whole) * tm * tn * 4 * splits : 0; }
 };
 
 // Few rows: product_rows_kernel.  At 4096 x 14336, weights from memory, it takes 22.9 us for 1
@@ -830,54 +871,66 @@ struct ProductChoice {
 // Else the shape and split with the least time by this model: the workgroups of one turn of
 // the CUs cost `start` us, and each block of 64 of their contraction `alone` us a turn or
 // `shared` us a workgroup of the busiest CU, whichever is more; the parts of a split cost a
-// launch and their bytes.  The figures are fitted, for the order of the choices and not for
+// launch and their bytes.  All tiles are split, or none, or those that overhang the last whole
+// turn of one tile a CU (1021 x 4099 x 7173, 264 tiles: 174 us whole, 161 with all in two
+// parts, 133 with the last eight in four).  The figures are fitted, for the order of the choices and not for
 // their times, to every shape and split timed at 17 to 8192 rows, 256 to 8192 columns and
-// contractions of 512 to 14336, operands from memory, in all three directions: of those 480
-// products the choice is within 5 % of the fastest in 415 and within 20 % in 468 (of 480 with operands off the wide
-// path in 394 and 454); at worst it takes twice as long, at 17 x 1024 x 2048 (16 us with eight
-// parts where no split takes 9).
+// contractions of 512 to 14336, operands from memory, in all three directions: of 484
+// products the choice is within 5 % of the fastest in 424 and within 20 % in 470; at worst it takes
+// 1.8 times as long, at 17 x 1024 x 2048 (16 us with eight parts where no split takes 9).  With
+// operands off the wide path, of 324 products 311 and 324.
 struct TileRate {
     Tile tile;
     uint32_t tm, tn, at_once;
     double start, alone, shared;
 };
 constexpr TileRate kDirectTiles[] = {
-    {kT128, 128, 128, 512, 0.2, 2.33, 0.975},    {kT128Deep, 128, 128, 256, 4.65, 0.88, 0.0},
-    {kT256x128, 256, 128, 256, 24.3, 0.96, 0.0}, {kT256, 256, 256, 256, 16.3, 1.38, 1.65},
-    {kT128x64, 128, 64, 256, 0.2, 0.0, 0.83},    {kT64, 64, 64, 512, 0.06, 0.13, 0.48}};
-constexpr TileRate kAnyTiles[] = {{kTAny, 128, 128, 512, 3.4, 0.0, 1.05}, {kTAny64, 64, 64, 1024, 0.0, 0.65, 0.44}};
+    {kT128, 128, 128, 512, 0.0, 1.64, 1.07},      {kT128Deep, 128, 128, 256, 3.35, 0.96, 0.107},
+    {kT256x128, 256, 128, 256, 9.7, 1.314, 0.26}, {kT256, 256, 256, 256, 11.06, 2.124, 1.744},
+    {kT128x64, 128, 64, 256, 3.21, 0.18, 0.774},  {kT64, 64, 64, 512, 0.0, 0.24, 0.551}};
+constexpr TileRate kAnyTiles[] = {{kTAny, 128, 128, 512, 1.52, 0.0, 0.801}, {kTAny64, 64, 64, 1024, 0.0, 0.01, 0.395}};
 constexpr uint32_t kMostSplits = 8;
-constexpr double kJoinStart = 3.64, kJoinBytes = 0.66e6, kAnyJoinStart = 4.56, kAnyJoinBytes = 8.9e6;  // us; bytes a us
+constexpr double kJoinStart = 4.27, kJoinBytes = 0.895e6, kAnyJoinStart = 2.94, kAnyJoinBytes = 2.9e6;  // us; bytes a us
+
+static uint32_t log2_of(uint32_t n) { return 31 - (uint32_t)__builtin_clz(n); }
 
 static ProductChoice product_choice(uint64_t m, uint64_t n, uint64_t k, bool along, bool direct, uint32_t most_splits) {
-    ProductChoice c = {0, direct ? kT128 : kTAny, 1};
+    ProductChoice c = {};
     const uint64_t rows_tiles = ceil_div(n, 16) * ceil_div(m, 16);
     if (along && rows_tiles < (1u << 22) && (m <= 16 || (m <= 32 && (!direct || n * k <= (1u << 24))))) {
         c.rows_mt = m <= 16 ? 1 : 2;
+        c.splits = 1;
         return c;
     }
     const double blocks = (double)ceil_div(k, kPBlock);
     double best = 0.0;
-    const auto offer = [&](const TileRate &t, uint32_t splits) {
-        const uint64_t groups = ceil_div(m, t.tm) * ceil_div(n, t.tn) * splits;
-        const double turns = (double)ceil_div(groups, t.at_once), busiest = (double)ceil_div(groups, 256);
-        const double each = t.alone * turns > t.shared * busiest ? t.alone * turns : t.shared * busiest;
-        double us = t.start * turns + blocks / splits * each;
+    const auto offer = [&](const TileRate &t, uint32_t splits, uint64_t tiles, uint64_t whole) {
+        const ProductChoice o = {0, t.tile, t.tm, t.tn, splits, tiles, whole};
+        if (o.part_bytes() > ZC_MATMUL_WORKSPACE_MAX) return;
+        const uint64_t parts = (tiles - whole) * splits, turns = ceil_div(whole, t.at_once), beside = turns * t.at_once - whole;
+        const double more = (double)ceil_div(parts > beside ? parts - beside : 0, t.at_once);
+        const double alone = (double)turns + more / splits;
+        const double busiest = (double)ceil_div(whole, 256) + (double)ceil_div(parts, 256) / splits;
+        double us = t.start * ((double)turns + more) + blocks * (t.alone * alone > t.shared * busiest ? t.alone * alone : t.shared * busiest);
         if (splits > 1)
-            us += (direct ? kJoinStart : kAnyJoinStart) + (double)(m * n * 4 * splits) / (direct ? kJoinBytes : kAnyJoinBytes);
+            us += (direct ? kJoinStart : kAnyJoinStart) + (double)o.part_bytes() / (direct ? kJoinBytes : kAnyJoinBytes);
         if (best == 0.0 || us < best) {
             best = us;
-            c.tile = t.tile;
-            c.splits = splits;
+            c = o;
         }
     };
-    for (uint32_t s = 1; s <= most_splits; s *= 2) {
-        if (s > 1 && (m * n > ZC_MATMUL_WORKSPACE_MAX / (4 * s) || blocks < 2 * s)) break;
-        if (direct)
-            for (const TileRate &t : kDirectTiles) offer(t, s);
-        else
-            for (const TileRate &t : kAnyTiles) offer(t, s);
-    }
+    const auto offer_tile = [&](const TileRate &t) {
+        const uint64_t tiles = ceil_div(m, t.tm) * ceil_div(n, t.tn), turns = tiles / 256 * 256;
+        offer(t, 1, tiles, tiles);
+        for (uint32_t s = 2; s <= most_splits && blocks >= 2 * s; s *= 2) {
+            offer(t, s, tiles, 0);
+            if (turns && turns < tiles) offer(t, s, tiles, turns);
+        }
+    };
+    if (direct)
+        for (const TileRate &t : kDirectTiles) offer_tile(t);
+    else
+        for (const TileRate &t : kAnyTiles) offer_tile(t);
     return c;
 }
 
@@ -912,17 +965,11 @@ static zc_status launch_product(ProductArgs p, uint64_t m, uint64_t n, uint64_t 
     if ((xa && p.lda < 8) || (xb && p.ldb < 8)) p.direct = 0;
     const bool room = ws && ws_bytes >= zc_matmul_workspace_bytes(m, n, k);
     const ProductChoice c = product_choice(m, n, k, !xa && !xb, direct, room ? kMostSplits : 1);
-    uint64_t tiles = c.rows_mt ? ceil_div(m, 16 * c.rows_mt) * ceil_div(n, 16) : 0;
-    if (!c.rows_mt) {
-        for (const TileRate &t : kDirectTiles)
-            if (t.tile == c.tile) tiles = ceil_div(m, t.tm) * ceil_div(n, t.tn);
-        for (const TileRate &t : kAnyTiles)
-            if (t.tile == c.tile) tiles = ceil_div(m, t.tm) * ceil_div(n, t.tn);
-    }
-    if (tiles > 0xFFFFFFFFull / kPThreads - 8) return ZC_ERR_INVALID_ARG;
+    const uint64_t groups = c.rows_mt ? ceil_div(m, 16 * c.rows_mt) * ceil_div(n, 16) : c.groups();
+    if (groups > 0xFFFFFFFFull / kPThreads) return ZC_ERR_INVALID_ARG;
     Launches on(stream);
     if (c.rows_mt) {
-        const dim3 grid((uint32_t)tiles);
+        const dim3 grid((uint32_t)groups);
         // (8 waves, 2, or turns of 2, 6 or 8 blocks took 1 to 1.2 times as long, loads marked for single use 1.3)
         if (c.rows_mt == 1)
             on.launch((product_rows_kernel<1, 4, 4>), grid, dim3(256), p);
@@ -930,15 +977,16 @@ static zc_status launch_product(ProductArgs p, uint64_t m, uint64_t n, uint64_t 
             on.launch((product_rows_kernel<2, 4, 4>), grid, dim3(256), p);
         return on.status();
     }
-    if (c.splits > 1) p.parts = static_cast<float *>(ws);
-    const dim3 grid((uint32_t)(ceil_div(tiles, 8) * 8), c.splits);
+    p.whole = (uint32_t)c.whole;
+    p.splits = c.splits;
+    p.parts = static_cast<float *>(ws);
+    const dim3 grid((uint32_t)groups);
     if (!xa && !xb) launch_tiles<false, false>(p, c.tile, grid, on);
     if (!xa && xb) launch_tiles<false, true>(p, c.tile, grid, on);
     if (xa && xb) launch_tiles<true, true>(p, c.tile, grid, on);
     if (c.splits > 1) {
-        const uint64_t units = ceil_div(m * ceil_div(n, 8), 256);
-        on.launch(product_join_kernel, dim3((uint32_t)(units < 4096 ? units : 4096)), dim3(256), p.parts, c.splits, p.m,
-                  p.n, p.e);
+        const uint64_t units = (c.tiles - c.whole) * c.tm * c.tn / 8 / 256;
+        on.launch(product_join_kernel, dim3((uint32_t)(units < 4096 ? units : 4096)), dim3(256), p, log2_of(c.tm), log2_of(c.tn));
     }
     return on.status();
 }
@@ -982,7 +1030,7 @@ extern "C" uint64_t zc_matmul_workspace_bytes(uint64_t rows, uint64_t cols, uint
     for (int along = 0; along < 2; ++along)
         for (int direct = 0; direct < 2; ++direct) {
             const ProductChoice c = product_choice(rows, cols, contraction, along != 0, direct != 0, kMostSplits);
-            if (c.splits > 1 && rows * cols * 4 * c.splits > most) most = rows * cols * 4 * c.splits;
+            if (c.part_bytes() > most) most = c.part_bytes();
         }
     return most;
 }

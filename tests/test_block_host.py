@@ -50,7 +50,7 @@ def test_sizes(moe):
     for _ in range(500):
         r, c, k = (int(2 ** g.uniform(0, 15)) for _ in range(3))
         n = moe.zc_matmul_workspace_bytes(r, c, k)
-        assert n <= moe.ZC_MATMUL_WORKSPACE_MAX and n % (4 * r * c) == 0
+        assert n <= moe.ZC_MATMUL_WORKSPACE_MAX and n % 16 == 0
     assert moe.zc_matmul_workspace_bytes(0, 5, 5) == 0 and moe.zc_matmul_workspace_bytes(1 << 31, 5, 5) == 0
     assert moe.zc_matmul_workspace_bytes(256, 256, 8192) > 0
     assert moe.zc_activation_backward_workspace_bytes(8192, 4096) % 256 == 0

@@ -92,6 +92,30 @@ def test_whole_numbers_are_exact(zc, m, n, k, which):
     assert np.array_equal(got.numpy(), ref.bf16(want))
 
 
+# every shape of tile with all of its tiles whole, with all split and with those past the last whole turn of the CUs
+# split, on the wide path and off it
+LARGER = [(1000, 2056, 264), (1000, 4100, 520), (1000, 4100, 1032), (1000, 4100, 2056), (1000, 8200, 520), (1000, 8200, 2056),
+          (100, 8200, 1032), (130, 6000, 640), (130, 6000, 1032), (260, 4100, 2056), (2000, 4100, 640), (2000, 8200, 1032),
+          (1032, 2900, 136), (2056, 260, 7168), (777, 1104, 7168)]
+
+
+@pytest.mark.parametrize("which", [0, 1, 2])
+@pytest.mark.parametrize("m,n,k", LARGER)
+def test_larger_whole_numbers_are_exact(zc, m, n, k, which):
+    g = np.random.default_rng([m, n, k, which])
+    a, b = operands(which, m, n, k, lambda *s: whole_numbers(g, *s))
+    add = whole_numbers(g, m, n)
+    want = exact(which, a, b)
+    for gap, offset in ((-1, 8), (3, 1)):
+        for room in (True, False):
+            got = product(zc, which, a, b, m, n, k, gap=gap, offset=offset, room=room)
+            assert np.array_equal(got.numpy()[:, :n], want), (gap, offset, room)
+            assert bool((got.t[:, n:].contiguous().view(torch.uint8) == 0xA5).all())
+    if which:
+        got = product(zc, which, a, b, m, n, k, out_f32=False, add=add, gap=-1, offset=8)
+        assert np.array_equal(got.numpy()[:, :n], ref.bf16(want + add))
+
+
 def sum_error(k, size):
     """Every addition of a 32-bit sum may be off by half a step of what is summed so far (a whole one where an instruction
     cuts): at most all k of them in a row."""
