@@ -396,7 +396,8 @@ uint64_t zc_matmul_workspace_bytes(uint64_t rows, uint64_t cols, uint64_t contra
  * k) BF16; products are exact, sums in 32 bits, d_out (out_type ZC_BF16 or
  * ZC_F32) and pre rounded once.  epilogue NULL: the sum itself.  k = 0: a sum of nothing
  * is 0, and the epilogue is applied.  A workspace smaller than
- * zc_matmul_workspace_bytes is not used; NULL: no split.  n and k are at most 2^28. */
+ * zc_matmul_workspace_bytes is not used; NULL: no split.  n and k are at most 2^28, and results of
+ * more than 2^24 tiles of 128 x 128 (256 x 256 on 16-byte aligned rows) are refused. */
 zc_status zc_matmul(const void *d_a, uint64_t m, uint64_t a_stride, const void *d_w, uint64_t n, uint64_t k,
                     uint64_t w_stride, const zc_epilogue *epilogue, void *d_out, uint32_t out_type,
                     uint64_t out_stride, void *d_workspace, uint64_t workspace_bytes, void *stream);

@@ -320,7 +320,8 @@ __global__ __launch_bounds__(256) void balance_zero_kernel(BalanceArgs a) {
 
 // A wave takes `run` consecutive tokens.  The sequence of token t ends at the first
 // offset above t, whatever the offsets before it are; an index of 0, or none,
-// means that no sequence holds it.
+// means that no sequence holds it.  8192 tokens of 256 experts 9.0 us (17 MB), 65536 of 160 in 37 sequences 26 us
+// (84 MB, 3.2 TB/s): bound by the exponentials, one a value, and the sums over the lanes beside the memory.
 template <bool BF16, bool SIGMOID, uint32_t V>
 __global__ __launch_bounds__(256) void balance_backward_kernel(BalanceArgs a) {
     const uint32_t lane = lane_id();

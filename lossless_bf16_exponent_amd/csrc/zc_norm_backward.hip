@@ -370,6 +370,8 @@ struct SumArgs {
     uint64_t part_stride;
     uint32_t count, cols, live;  // live: sums that have parts; the others are zeros
 };
+// 64 columns of one sum a block, its parts in order, in 16 runs side by side: 256 parts of three sums of 7168 columns
+// 4.9 us (22 MB), of five of 5125 6.1: a launch and the latency of 16 loads in a row.
 constexpr uint32_t kSumRuns = 16;
 __global__ __launch_bounds__(kLanes * kSumRuns) void norm_sums_kernel(SumArgs a) {
     __shared__ float run[kSumRuns][kLanes];

@@ -324,9 +324,9 @@ __device__ __forceinline__ TilePlace tile_place(uint32_t id, uint32_t mtiles, ui
 // the next.  Without DIRECT (operands at any element, rows far apart) blocks go
 // through registers, two on their way while the one before them is multiplied, and so does the
 // contraction's ragged end.  Rates, operands from memory: 8192^3 774 us (1420 TFLOP/s; the library
-// reaches 1365), 8192 x 4096 x 7168 347 us (1390 TFLOP/s, bound by the matrix instructions and, past
-// those, by the clock under them), 8192 x 256 x 7168 in two parts 34 us (bound by reading 121 MB),
-// 48 x 14336 x 4096 21.6 us (117 MB); without DIRECT 1024 x 4096 x 7168 105 us, rows at odd elements
+// reaches 1365), 8192 x 4096 x 7168 347 us (1390 TFLOP/s), both bound by the matrix
+// instructions; 8192 x 256 x 7168 in two parts 34 us (121 MB, and 56 blocks a workgroup), 48 x 14336 x
+// 4096 21.6 us (117 MB, 5.4 TB/s); without DIRECT 1024 x 4096 x 7168 105 us, rows at odd elements
 // 125: a wave's loads, its reads of LDS and its products then follow each other with one wave a SIMD.
 template <uint32_t BM, uint32_t BN, uint32_t STAGES, bool XA, bool XB, bool DIRECT>
 __global__ __launch_bounds__(kPThreads, STAGES * (BM + BN) * kPBytes > 80 * 1024 ? 1 : 2) void product_kernel(ProductArgs p) {
@@ -645,7 +645,8 @@ __global__ __launch_bounds__(kPThreads, STAGES * (BM + BN) * kPBytes > 80 * 1024
     }
 }
 
-// The parts of split tiles of 1 << row_bits rows and 1 << col_bits columns, added in order.
+// The parts of split tiles of 1 << row_bits rows and 1 << col_bits columns, added in order: bound by
+// a launch and by the parts, 8192 x 256 in two parts 6.4 us (25 MB), eight tiles of 128 x 128 in eight 6.2.
 __global__ __launch_bounds__(256) void product_join_kernel(ProductArgs p, uint32_t row_bits, uint32_t col_bits) {
     const uint32_t bits = row_bits + col_bits - 3;  // of eights of a tile
     const uint32_t mtiles = (p.m + (1u << row_bits) - 1) >> row_bits, ntiles = (p.n + (1u << col_bits) - 1) >> col_bits;
@@ -833,7 +834,8 @@ __global__ __launch_bounds__(kSWaves * kLanes) void slope_kernel(SlopeArgs a) {
         if (col < a.cols) a.parts[(uint64_t)blockIdx.y * a.cols + col] = s;
     }
 }
-// The parts of a column's sum, added in order: 64 columns a block, in 16 runs of parts.
+// The parts of a column's sum, added in order: 64 columns a block, in 16 runs of parts.  256 parts
+// of 4096 columns 7.3 us, a launch and the latency of 16 loads in a row.
 constexpr uint32_t kRuns = 16;
 __global__ __launch_bounds__(kLanes * kRuns) void column_sums_kernel(const float *parts, uint32_t count, uint32_t cols,
                                                                      float *out) {
@@ -890,6 +892,7 @@ constexpr TileRate kDirectTiles[] = {
     {kT128x64, 128, 64, 256, 3.21, 0.18, 0.774},  {kT64, 64, 64, 512, 0.0, 0.24, 0.551}};
 constexpr TileRate kAnyTiles[] = {{kTAny, 128, 128, 512, 1.52, 0.0, 0.801}, {kTAny64, 64, 64, 1024, 0.0, 0.01, 0.395}};
 constexpr uint32_t kMostSplits = 8;
+constexpr uint64_t kMostGroups = 0xFFFFFFFFull / kPThreads;  // of one launch
 constexpr double kJoinStart = 4.27, kJoinBytes = 0.895e6, kAnyJoinStart = 2.94, kAnyJoinBytes = 2.9e6;  // us; bytes a us
 
 static uint32_t log2_of(uint32_t n) { return 31 - (uint32_t)__builtin_clz(n); }
@@ -906,7 +909,7 @@ static ProductChoice product_choice(uint64_t m, uint64_t n, uint64_t k, bool alo
     double best = 0.0;
     const auto offer = [&](const TileRate &t, uint32_t splits, uint64_t tiles, uint64_t whole) {
         const ProductChoice o = {0, t.tile, t.tm, t.tn, splits, tiles, whole};
-        if (o.part_bytes() > ZC_MATMUL_WORKSPACE_MAX) return;
+        if (o.part_bytes() > ZC_MATMUL_WORKSPACE_MAX || o.groups() > kMostGroups) return;
         const uint64_t parts = (tiles - whole) * splits, turns = ceil_div(whole, t.at_once), beside = turns * t.at_once - whole;
         const double more = (double)ceil_div(parts > beside ? parts - beside : 0, t.at_once);
         const double alone = (double)turns + more / splits;
@@ -966,7 +969,7 @@ static zc_status launch_product(ProductArgs p, uint64_t m, uint64_t n, uint64_t 
     const bool room = ws && ws_bytes >= zc_matmul_workspace_bytes(m, n, k);
     const ProductChoice c = product_choice(m, n, k, !xa && !xb, direct, room ? kMostSplits : 1);
     const uint64_t groups = c.rows_mt ? ceil_div(m, 16 * c.rows_mt) * ceil_div(n, 16) : c.groups();
-    if (groups > 0xFFFFFFFFull / kPThreads) return ZC_ERR_INVALID_ARG;
+    if (!groups) return ZC_ERR_INVALID_ARG;  // more tiles than a launch takes
     Launches on(stream);
     if (c.rows_mt) {
         const dim3 grid((uint32_t)groups);

@@ -252,6 +252,8 @@ def _type_of(x, given) -> int:
     if not _types:
         import torch
         _types.update({torch.float32: ZC_F32, torch.bfloat16: ZC_BF16})
+    if x.dtype not in _types:
+        raise TypeError("a parameter is float32 or bfloat16, not %s" % x.dtype)
     return _types[x.dtype]
 
 

@@ -189,3 +189,12 @@ def test_types_come_from_tensors(moe):
     assert (e.bias_type, e.residual_type, e.d_bias, e.d_residual) == (moe.ZC_BF16, moe.ZC_F32, b.data_ptr(), f.data_ptr())
     c = moe.norm_config(moe.norm_params(2, f), None, gate=b)
     assert (c.after.kind, c.before.kind, c.gate_type, c.d_gate) == (2, 0, moe.ZC_BF16, b.data_ptr())
+
+
+def test_types_of_parameters(moe):
+    torch = pytest.importorskip("torch")
+    with pytest.raises(TypeError):
+        moe.norm_params(moe.ZC_NORM_RMS, torch.ones(8, dtype=torch.float16))
+    with pytest.raises(TypeError):
+        moe.epilogue(bias=torch.ones(8, dtype=torch.float64))
+    assert moe.norm_params(moe.ZC_NORM_RMS, torch.ones(8, dtype=torch.bfloat16)).type == moe.ZC_BF16

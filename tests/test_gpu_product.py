@@ -364,3 +364,12 @@ def test_repeats_itself(zc):
         first = product(zc, which, a, b, m, n, k).numpy()
         for _ in range(3):
             assert np.array_equal(product(zc, which, a, b, m, n, k).numpy(), first)
+
+
+def test_more_rows_than_small_tiles_fit_a_launch(zc):
+    """A product by 1: every row has to come out as it went in."""
+    m = (1 << 30) + 5
+    a = (torch.arange(m, device="cuda", dtype=torch.int32) % 251 - 125).bfloat16()
+    out = torch.full((m,), -1.0, dtype=torch.bfloat16, device="cuda")
+    zc.zc_matmul(a, m, 1, torch.ones(1, dtype=torch.bfloat16, device="cuda"), 1, 1, 1, None, out, zc.ZC_BF16, 1)
+    assert torch.equal(out.view(torch.int16), a.view(torch.int16))
