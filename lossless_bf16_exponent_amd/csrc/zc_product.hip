@@ -673,11 +673,31 @@ __global__ __launch_bounds__(256) void product_join_kernel(ProductArgs p, uint32
 // few rows: bound by reading the weights
 // ---------------------------------------------------------------------------
 
+// 16 bytes at any value.  A wave's 16-byte loads take three times as long where an address is not on 4 bytes (2 x 4096 x
+// 10880 with rows at odd values 47.8 us, on 4 bytes 19.8): then the words they lie in are loaded, the first with the
+// value before, and the last value by itself, and shifted into
+// place (29.6 us; in tiles, whose waves have more loads than they can issue, this took 1.2 times as long as loads at any value).
+template <bool ODD>
+struct Loose {
+    u32v4 w;
+    uint32_t last;
+    __device__ __forceinline__ static uint32_t shift(const uint16_t *p) { return (uint32_t)(uintptr_t)p & 2u; }
+    __device__ __forceinline__ void load(const uint16_t *p) {
+        w = *reinterpret_cast<const u32v4a4 *>(p - (ODD ? shift(p) / 2 : 0u));
+        if (ODD) last = p[7];
+    }
+    __device__ __forceinline__ u32v4 value(uint32_t by) const {
+        if (!ODD) return w;
+        return u32v4{__builtin_amdgcn_alignbyte(w[1], w[0], by), __builtin_amdgcn_alignbyte(w[2], w[1], by),
+                     __builtin_amdgcn_alignbyte(w[3], w[2], by), __builtin_amdgcn_alignbyte(last, w[3], by)};
+    }
+};
+
 // 16 rows of B against 16 MT rows of A, both along the contraction.  The waves of a
 // block take its blocks of 64 in turn, STEP at a time, straight from memory into
 // the registers of the matrix instructions, and add their sums through LDS.  1 x
 // 4096 x 14336, weights from memory: 22.9 us, 5.1 TB/s, what a large copy reaches.
-template <uint32_t MT, uint32_t WAVES, uint32_t STEP>
+template <uint32_t MT, uint32_t WAVES, uint32_t STEP, bool ODD>
 __global__ __launch_bounds__(WAVES * 64) void product_rows_kernel(ProductArgs p) {
     __shared__ f32v4 part[WAVES][MT][kLanes];
     const uint32_t lane = lane_id(), wave = (uint32_t)__builtin_amdgcn_readfirstlane(threadIdx.x / kLanes);
@@ -693,8 +713,12 @@ __global__ __launch_bounds__(WAVES * 64) void product_rows_kernel(ProductArgs p)
     const uint32_t whole = p.k / kPBlock;
     // two turns' values in registers: one on its way while the other is multiplied
     struct Turn {
-        u32v4 b[STEP][2], a[STEP][MT][2];
+        Loose<ODD> b[STEP][2], a[STEP][MT][2];
     };
+    const uint32_t byb = Loose<ODD>::shift(b);
+    uint32_t bya[MT];
+#pragma unroll
+    for (uint32_t i = 0; i < MT; ++i) bya[i] = Loose<ODD>::shift(a[i]);
     Turn turns[2];
     const auto load = [&](Turn &t, uint32_t kb) {
 #pragma unroll
@@ -702,9 +726,9 @@ __global__ __launch_bounds__(WAVES * 64) void product_rows_kernel(ProductArgs p)
 #pragma unroll
             for (uint32_t h = 0; h < 2; ++h) {
                 const uint64_t at = (uint64_t)(kb + u) * kPBlock + 32 * h + fc;
-                t.b[u][h] = *reinterpret_cast<const u32v4a2 *>(b + at);
+                t.b[u][h].load(b + at);
 #pragma unroll
-                for (uint32_t i = 0; i < MT; ++i) t.a[u][i][h] = *reinterpret_cast<const u32v4a2 *>(a[i] + at);
+                for (uint32_t i = 0; i < MT; ++i) t.a[u][i][h].load(a[i] + at);
             }
     };
     const auto take = [&](const Turn &t) {
@@ -714,8 +738,8 @@ __global__ __launch_bounds__(WAVES * 64) void product_rows_kernel(ProductArgs p)
             for (uint32_t h = 0; h < 2; ++h)
 #pragma unroll
                 for (uint32_t i = 0; i < MT; ++i)
-                    acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16v8, t.b[u][h]),
-                                                                     __builtin_bit_cast(bf16v8, t.a[u][i][h]), acc[i], 0, 0, 0);
+                    acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16v8, t.b[u][h].value(byb)),
+                                                                     __builtin_bit_cast(bf16v8, t.a[u][i][h].value(bya[i])), acc[i], 0, 0, 0);
     };
     uint32_t kb = wave * STEP;
     constexpr uint32_t kTurn = WAVES * STEP;
@@ -867,10 +891,11 @@ struct ProductChoice {
     uint64_t part_bytes() const { return splits > 1 ? (tiles - whole) * tm * tn * 4 * splits : 0; }
 };
 
-// Few rows: product_rows_kernel.  At 4096 x 14336, weights from memory, it takes 22.9 us for 1
-// row and 28.7 for 16 (tiles 27.3 and 27.3), at 4096 x 4096 8.3 for 1 and 13.5 for 32 (12.0, 13.1), and
-// for 4 rows at 256 x 7168 10.8 (10.3 with eight parts).
-// Else the shape and split with the least time by this model: the workgroups of one turn of
+// Up to 32 rows: product_rows_kernel, if the model beneath it puts no tile before it.  2 x 4096 x 10880 takes 20.9 us
+// there and 25.1 in tiles in eight parts, 2 x 162 x 10880 16.1 and 10.5, with rows at odd values 25.6 and 15.9.  Of 240
+// products of 1 to 32 rows, 162 to 8192 columns and contractions of 512 to 13312 the choice is within 5 % of the
+// faster in 218 and within 20 % in 236; at worst it takes 1.4 times as long (24 x 8192 x 2560 at odd values).
+// The shape and split with the least time by this model: the workgroups of one turn of
 // the CUs cost `start` us, and each block of 64 of their contraction `alone` us a turn or
 // `shared` us a workgroup of the busiest CU, whichever is more; the parts of a split cost a
 // launch and their bytes.  All tiles are split, or none, or those that overhang the last whole
@@ -891,6 +916,11 @@ constexpr TileRate kDirectTiles[] = {
     {kT256x128, 256, 128, 256, 9.7, 1.314, 0.26}, {kT256, 256, 256, 256, 11.06, 2.124, 1.744},
     {kT128x64, 128, 64, 256, 3.21, 0.18, 0.774},  {kT64, 64, 64, 512, 0.0, 0.24, 0.551}};
 constexpr TileRate kAnyTiles[] = {{kTAny, 128, 128, 512, 1.52, 0.0, 0.801}, {kTAny64, 64, 64, 1024, 0.0, 0.01, 0.395}};
+// of product_rows_kernel: a block of the contraction, a row beside it (us), bytes of the weights a us
+struct RowsRate {
+    double block, row, bytes;
+};
+constexpr RowsRate kDirectRows = {0.1, 0.008, 3.2e6}, kAnyRows = {0.1, 0.006, 4.2e6};
 constexpr uint32_t kMostSplits = 8;
 constexpr uint64_t kMostGroups = 0xFFFFFFFFull / kPThreads;  // of one launch
 constexpr double kJoinStart = 4.27, kJoinBytes = 0.895e6, kAnyJoinStart = 2.94, kAnyJoinBytes = 2.9e6;  // us; bytes a us
@@ -899,14 +929,15 @@ static uint32_t log2_of(uint32_t n) { return 31 - (uint32_t)__builtin_clz(n); }
 
 static ProductChoice product_choice(uint64_t m, uint64_t n, uint64_t k, bool along, bool direct, uint32_t most_splits) {
     ProductChoice c = {};
-    const uint64_t rows_tiles = ceil_div(n, 16) * ceil_div(m, 16);
-    if (along && rows_tiles < (1u << 22) && (m <= 16 || (m <= 32 && (!direct || n * k <= (1u << 24))))) {
-        c.rows_mt = m <= 16 ? 1 : 2;
-        c.splits = 1;
-        return c;
-    }
     const double blocks = (double)ceil_div(k, kPBlock);
     double best = 0.0;
+    if (along && m <= 32 && ceil_div(n, 16) < (1u << 22)) {
+        const RowsRate &r = direct ? kDirectRows : kAnyRows;
+        const double alone = blocks * (r.block + r.row * (double)m), bytes = (double)(n * k * 2) / r.bytes;
+        c.rows_mt = m <= 16 ? 1 : 2;
+        c.splits = 1;
+        best = 1.0 + (alone > bytes ? alone : bytes);
+    }
     const auto offer = [&](const TileRate &t, uint32_t splits, uint64_t tiles, uint64_t whole) {
         const ProductChoice o = {0, t.tile, t.tm, t.tn, splits, tiles, whole};
         if (o.part_bytes() > ZC_MATMUL_WORKSPACE_MAX || o.groups() > kMostGroups) return;
@@ -962,6 +993,7 @@ static zc_status launch_product(ProductArgs p, uint64_t m, uint64_t n, uint64_t 
     p.k = (uint32_t)k;
     p.blocks = (uint32_t)ceil_div(k, kPBlock);
     const bool direct = direct_ok(p.a, p.lda) && direct_ok(p.b, p.ldb);
+    const bool odd = !aligned(p.a, 4) || !aligned(p.b, 4) || p.lda % 2 || p.ldb % 2;
     // a whole block may be loaded unless its last chunks pass the end of the operand
     p.direct = p.k / kPBlock;
     if (k % kPBlock == 0 && p.direct && ((xa && m % 8) || (xb && n % 8))) --p.direct;
@@ -975,9 +1007,9 @@ static zc_status launch_product(ProductArgs p, uint64_t m, uint64_t n, uint64_t 
         const dim3 grid((uint32_t)groups);
         // (8 waves, 2, or turns of 2, 6 or 8 blocks took 1 to 1.2 times as long, loads marked for single use 1.3)
         if (c.rows_mt == 1)
-            on.launch((product_rows_kernel<1, 4, 4>), grid, dim3(256), p);
+            on.launch((odd ? product_rows_kernel<1, 4, 4, true> : product_rows_kernel<1, 4, 4, false>), grid, dim3(256), p);
         else
-            on.launch((product_rows_kernel<2, 4, 4>), grid, dim3(256), p);
+            on.launch((odd ? product_rows_kernel<2, 4, 4, true> : product_rows_kernel<2, 4, 4, false>), grid, dim3(256), p);
         return on.status();
     }
     p.whole = (uint32_t)c.whole;

@@ -96,7 +96,7 @@ def test_whole_numbers_are_exact(zc, m, n, k, which):
 # split, on the wide path and off it
 LARGER = [(1000, 2056, 264), (1000, 4100, 520), (1000, 4100, 1032), (1000, 4100, 2056), (1000, 8200, 520), (1000, 8200, 2056),
           (100, 8200, 1032), (130, 6000, 640), (130, 6000, 1032), (260, 4100, 2056), (2000, 4100, 640), (2000, 8200, 1032),
-          (1032, 2900, 136), (2056, 260, 7168), (777, 1104, 7168)]
+          (1032, 2900, 136), (2056, 260, 7168), (777, 1104, 7168), (3, 200, 4200), (20, 200, 4200), (16, 4100, 2200), (2, 162, 10889)]
 
 
 @pytest.mark.parametrize("which", [0, 1, 2])
