@@ -676,7 +676,7 @@ __global__ __launch_bounds__(256) void product_join_kernel(ProductArgs p, uint32
 // 16 bytes at any value.  A wave's 16-byte loads take three times as long where an address is not on 4 bytes (2 x 4096 x
 // 10880 with rows at odd values 47.8 us, on 4 bytes 19.8): then the words they lie in are loaded, the first with the
 // value before, and the last value by itself, and shifted into
-// place (29.6 us; in tiles, whose waves have more loads than they can issue, this took 1.2 times as long as loads at any value).
+// place (29.6 to 33.9 us; in tiles, whose waves have more loads than they can issue, this took 1.2 times as long as loads at any value).
 template <bool ODD>
 struct Loose {
     u32v4 w;
