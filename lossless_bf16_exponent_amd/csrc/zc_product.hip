@@ -108,13 +108,14 @@ __device__ __forceinline__ float activation(float v, uint32_t act) {
     }
 }
 
-// d times the slope at v.
+// d times the slope at v.  The factor that may be large meets a vanishing one before d does, so that finite values have finite
+// products: 4 * -1e38 has left the range of a float before it meets a 0.
 __device__ __forceinline__ float sloped(float d, float v, uint32_t act) {
     switch (act) {
         case ZC_ACT_RELU: return v > 0.0f ? d : v != v ? v : 0.0f;
         case ZC_ACT_SILU: {
             const Parts p = sigmoid_parts(v);
-            return d * fmaf(v, p.rest, 1.0f) * p.s * p.t;
+            return fmaf(v, p.rest, 1.0f) * p.s * (d * p.t);
         }
         case ZC_ACT_GELU: {
             // Phi(v) + v phi(v)
@@ -127,7 +128,7 @@ __device__ __forceinline__ float sloped(float d, float v, uint32_t act) {
             // from 30 on the slope is 1 or 0 in 32 bits
             const float x = v != v ? v : fminf(fmaxf(v, -30.0f), 30.0f), y = kCubic * x * x;
             const Parts p = sigmoid_parts(kTanh * fmaf(y, x, x));
-            return d * fmaf(x * p.rest, kTanh * fmaf(3.0f, y, 1.0f), 1.0f) * p.s * p.t;
+            return fmaf(x * p.rest, kTanh * fmaf(3.0f, y, 1.0f), 1.0f) * p.s * (d * p.t);
         }
         case ZC_ACT_SIGMOID: {
             const Parts p = sigmoid_parts(v != v ? v : -fabsf(v));
