@@ -374,7 +374,8 @@ zc_status zc_norm_backward(const void *d_r, uint32_t stream_type, uint64_t rows,
  *   pre = v + bias;  out = residual + scale * activation(pre)
  * activation: NONE, RELU, SILU v * sigmoid(v), GELU v * Phi(v) (the normal
  * distribution), GELU_TANH v * (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2,
- * SIGMOID. */
+ * SIGMOID.  At infinities all but NONE have their limits, and so have their slopes: 0 and
+ * 0 at -inf, +inf and 1 at +inf (SIGMOID: 1 and 0); NaN stays NaN. */
 typedef struct zc_epilogue {
     const void *d_bias;       /* cols values of bias_type, or NULL: 0 */
     const void *d_residual;   /* rows of residual_type, or NULL: 0; may be the output, with its type and stride */

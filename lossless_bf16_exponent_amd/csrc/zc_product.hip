@@ -84,21 +84,25 @@ __device__ __forceinline__ Tail normal_tail(float v) {
 constexpr float kTanh = 1.59576912f, kCubic = 0.044715f;  // 2 sqrt(2 / pi): (1 + tanh(u)) / 2 = sigmoid(2 u)
 constexpr float kDensity = 0.39894228f;                   // 1 / sqrt(2 pi)
 
+// At infinities the activations are their limits: a factor that stands beside one that vanishes is kept finite.  (NaN comes
+// through the other one.)
+constexpr float kMost = 3.40282347e38f, kNoTail = 40.0f;  // the largest float; beyond 40 the normal tail is 0 in 32 bits
+
 __device__ __forceinline__ float activation(float v, uint32_t act) {
     switch (act) {
         case ZC_ACT_RELU: return v > 0.0f ? v : v != v ? v : 0.0f;
         case ZC_ACT_SILU: {
             const Parts p = sigmoid_parts(v);
-            return v * p.s * p.t;
+            return fmaxf(v, -kMost) * p.s * p.t;
         }
         case ZC_ACT_GELU: {
             const Tail n = normal_tail(v);
-            const float q = n.m * n.root;
-            return v >= 0.0f ? fmaf(-v * q, n.root, v) : v * q * n.root;
+            const float x = fminf(fmaxf(v, -kNoTail), kNoTail), q = n.m * n.root;
+            return v >= 0.0f ? fmaf(-x * q, n.root, v) : x * q * n.root;
         }
         case ZC_ACT_GELU_TANH: {
             const Parts p = sigmoid_parts(kTanh * fmaf(kCubic * v * v, v, v));
-            return v * p.s * p.t;
+            return fmaxf(v, -kMost) * p.s * p.t;
         }
         case ZC_ACT_SIGMOID: {
             const Parts p = sigmoid_parts(v);
@@ -115,14 +119,14 @@ __device__ __forceinline__ float sloped(float d, float v, uint32_t act) {
         case ZC_ACT_RELU: return v > 0.0f ? d : v != v ? v : 0.0f;
         case ZC_ACT_SILU: {
             const Parts p = sigmoid_parts(v);
-            return fmaf(v, p.rest, 1.0f) * p.s * (d * p.t);
+            return fmaf(fminf(fmaxf(v, -kMost), kMost), p.rest, 1.0f) * p.s * (d * p.t);
         }
         case ZC_ACT_GELU: {
             // Phi(v) + v phi(v)
             const Tail n = normal_tail(v);
-            const float near = d * n.root;
-            return v >= 0.0f ? fmaf(near * fmaf(v, kDensity, -n.m), n.root, d)
-                             : near * fmaf(v, kDensity, n.m) * n.root;
+            const float x = fminf(fmaxf(v, -kNoTail), kNoTail);
+            return v >= 0.0f ? d * fmaf(fmaf(x, kDensity, -n.m) * n.root, n.root, 1.0f)
+                             : d * n.root * fmaf(x, kDensity, n.m) * n.root;
         }
         case ZC_ACT_GELU_TANH: {
             // from 30 on the slope is 1 or 0 in 32 bits

@@ -51,3 +51,42 @@ def test_large_gradients_beside_vanishing_slopes(zc, act, d):
     assert np.array_equal(got[far], want[far])
     # |slope - its limit| <= (1 + |v|) e^-|v| < 1e-37 past 90
     close(got[~far], want[~far], 2 * EPS * np.abs(want[~far]) + abs(d) * 1e-37, "slopes")
+
+
+@pytest.mark.parametrize("act", [RELU, SILU, GELU, GELU_TANH, SIGMOID])
+def test_infinities(zc, act):
+    """The activations' limits, and their slopes'; NaN stays, beside values that are what they are without it."""
+    v = np.array([np.inf, 1.0, -np.inf, -1.0, np.nan, 2.0, LOWEST, -LOWEST])
+    got = values(zc, v, act)
+    plain = values(zc, np.array([1.0, -1.0, 2.0]), act)
+    top = 1.0 if act == SIGMOID else np.inf
+    assert np.array_equal(got[[0, 2]], [top, 0.0])
+    assert np.isnan(got[4]) and np.array_equal(got[[1, 3, 5]], plain)
+    assert np.array_equal(got[[6, 7]], [0.0, 1.0 if act == SIGMOID else -LOWEST])
+    for d in (1.0, -3.0, 2.0 ** 100):
+        got = slopes(zc, d, v, act)
+        plain = slopes(zc, d, np.array([1.0, -1.0, 2.0]), act)
+        one = 0.0 if act == SIGMOID else d
+        assert np.array_equal(got[[0, 2]], [one, 0.0]) and np.array_equal(got[[6, 7]], [0.0, one])
+        assert np.isnan(got[4]) and np.array_equal(got[[1, 3, 5]], plain)
+
+
+@pytest.mark.parametrize("act", [RELU, SILU, GELU, GELU_TANH])
+def test_infinite_gradients(zc, act):
+    """A gradient that has left the range of a float is multiplied by the slope: an infinity of its sign right of 0."""
+    v = ref.bf16(np.array([0.5, 3.0, 20.0, 30.0, 100.0, 1e30]))
+    for d in (np.inf, -np.inf):
+        assert np.array_equal(slopes(zc, d, v, act), np.full(v.size, d))
+
+
+@pytest.mark.parametrize("m", [1, 40, 200])
+def test_infinite_sums(zc, m):
+    """GELU of an infinite sum in the kernels of few rows, of tiles and of split contractions."""
+    for n, k in ((40, 64), (128, 8192)):
+        a, w = torch.zeros(m, k, dtype=torch.bfloat16, device="cuda"), torch.ones(n, k, dtype=torch.bfloat16, device="cuda")
+        a[0, 3] = float("inf")
+        ws = torch.full((max(16, zc.zc_matmul_workspace_bytes(m, n, k)),), 0xFF, dtype=torch.uint8, device="cuda")
+        out = Out((m, n), torch.bfloat16)
+        zc.zc_matmul(a, m, k, w, n, k, k, zc.epilogue(activation=GELU), out, zc.ZC_BF16, n, ws, ws.numel())
+        got = out.numpy()
+        assert np.isposinf(got[0]).all() and not got[1:].any()
