@@ -45,98 +45,105 @@ struct ProductArgs {
 // activations
 // ---------------------------------------------------------------------------
 
-// sigmoid(v) = s * t and 1 - sigmoid(v), from e^(-|v| / 2) and its square, which do not
-// overflow.  Left of 0, t is that root: a product with a large value keeps its digits
-// where the exponential has none left.  The hardware exponential and reciprocal are off by a
-// unit of 32 bits, as much as rounding their argument is; the library's took 4 to 5 times as many
-// instructions, in tiles of one wave a SIMD (8192 x 4096 x 7168 with SILU: 76 us of 511).
-struct Parts {
-    float s, t, rest;
+// Left and right of 0 the activations are each other's mirror image: beside v or 1, and v * 0 or 0, stands a tail that is even in v.
+// A tail comes as the product of `s` and `t`, both as small as its root, so that where the exponential has no digits left,
+// each meets a factor of its own before they meet each other: a large gradient keeps the tail's digits, and finite values have finite
+// products.  What stands beside a tail is bounded (`x`), so that infinities give the limits; NaN comes through the tail.
+
+// sigmoid(-|v|) = s * t and sigmoid(|v|) = r from e^-|v| = m 4^h, a whole number h, |log2 m| <= 1: the whole part is taken off the
+// exponent exactly, and 32 bits of it are left for m.  h is rounded by adding a number whose last bit is 1, and its lowest bits
+// become t's exponent.  The hardware's exponential and reciprocal are off by a unit of 32 bits: the sigmoid by less than 7 half
+// steps at any v.  (8192 x 4096 x 7168 with SILU: 50 of 410 us; the library's exponential and a division took 76.)
+struct Sigmoid {
+    float s, t, r, x;
 };
-__device__ __forceinline__ Parts sigmoid_parts(float v) {
-    const float root = __builtin_amdgcn_exp2f(fabsf(v) * -0.72134752f), e = root * root;
-    const float r = __builtin_amdgcn_rcpf(1.0f + e);
-    const bool right = v >= 0.0f;
-    return {right ? r : root * r, right ? 1.0f : root, right ? e * r : r};
+__device__ __forceinline__ Sigmoid sigmoid_of(float v) {
+    constexpr float kWhole = 12582912.0f;  // 1.5 * 2^23
+    Sigmoid g;
+    g.x = fminf(fabsf(v), 174.0f);  // from there on h is -126, and m goes on to 0
+    const float y = fmaf(g.x, -0.721347520f, kWhole), h2 = fmaf(2.0f, y, -2.0f * kWhole);
+    const float m = __builtin_amdgcn_exp2f(fmaf(fabsf(v), -1.92596299e-8f, fmaf(fabsf(v), -1.44269502f, -h2)));
+    g.t = __uint_as_float((__float_as_uint(y) << 23) + 0x3F800000u);
+    const float mt = m * g.t;
+    g.r = __builtin_amdgcn_rcpf(fmaf(mt, g.t, 1.0f));
+    g.s = mt * g.r;
+    return g;
 }
-// The normal distribution's tail beyond |v| is q * root, with root = e^(-v^2 / 4) and,
-// for x = |v| / sqrt(2), q = root * t * (erfc(x) e^(x^2) / t) / 2, t = 1 / (1 + x / 2): the
-// quotient is a polynomial of t to 1e-8 of itself on all of 0..1 (fitted here to its values
-// at Chebyshev's points with weights that level the error).
+// The normal distribution's tail beyond |v| is m * t^2, with t = e^(-v^2 / 4) and,
+// for x = |v| / sqrt(2), m = u * (erfc(x) e^(x^2) / u) / 2, u = 1 / (1 + x / 2): the
+// quotient is a polynomial of u to 1e-8 of itself on all of 0..1 (fitted here to its values
+// at Chebyshev's points with weights that level the error).  What the square and the exponent of 2 lose
+// in rounding, |v|^2 times as much in the tail, is carried on.
 struct Tail {
-    float m, root;  // q = m * root
+    float m, t, x;
 };
 __device__ __forceinline__ Tail normal_tail(float v) {
-    const float t = __builtin_amdgcn_rcpf(fmaf(fabsf(v), 0.35355339f, 1.0f));
+    const float u = __builtin_amdgcn_rcpf(fmaf(fabsf(v), 0.35355339f, 1.0f));
     float p = 0.0423526122f;
-    p = fmaf(p, t, -0.230857749f);
-    p = fmaf(p, t, 0.486179082f);
-    p = fmaf(p, t, -0.446977725f);
-    p = fmaf(p, t, 0.127089673f);
-    p = fmaf(p, t, -0.0572325763f);
-    p = fmaf(p, t, 0.093000611f);
-    p = fmaf(p, t, 0.175376827f);
-    p = fmaf(p, t, 0.246880587f);
-    p = fmaf(p, t, 0.282093853f);
-    p = fmaf(p, t, 0.282094795f);
-    return {0.5f * t * p, __builtin_amdgcn_exp2f(v * v * -0.36067376f)};
+    p = fmaf(p, u, -0.230857749f);
+    p = fmaf(p, u, 0.486179082f);
+    p = fmaf(p, u, -0.446977725f);
+    p = fmaf(p, u, 0.127089673f);
+    p = fmaf(p, u, -0.0572325763f);
+    p = fmaf(p, u, 0.093000611f);
+    p = fmaf(p, u, 0.175376827f);
+    p = fmaf(p, u, 0.246880587f);
+    p = fmaf(p, u, 0.282093853f);
+    p = fmaf(p, u, 0.282094795f);
+    constexpr float c = -0.360673760f, c_rest = -4.81490747e-9f;  // of -log2(e) / 4
+    const float x = fminf(fabsf(v), 40.0f);                        // from there on the tail is 0
+    const float sq = x * x, of2 = sq * c, e = __builtin_amdgcn_exp2f(of2);
+    const float rest = fmaf(fmaf(x, x, -sq), c, fmaf(sq, c_rest, fmaf(sq, c, -of2)));
+    return {0.5f * u * p, fmaf(e, rest * 0.693147181f, e), x};
 }
 constexpr float kTanh = 1.59576912f, kCubic = 0.044715f;  // 2 sqrt(2 / pi): (1 + tanh(u)) / 2 = sigmoid(2 u)
 constexpr float kDensity = 0.39894228f;                   // 1 / sqrt(2 pi)
-
-// At infinities the activations are their limits: a factor that stands beside one that vanishes is kept finite.  (NaN comes
-// through the other one.)
-constexpr float kMost = 3.40282347e38f, kNoTail = 40.0f;  // the largest float; beyond 40 the normal tail is 0 in 32 bits
 
 __device__ __forceinline__ float activation(float v, uint32_t act) {
     switch (act) {
         case ZC_ACT_RELU: return v > 0.0f ? v : v != v ? v : 0.0f;
         case ZC_ACT_SILU: {
-            const Parts p = sigmoid_parts(v);
-            return fmaxf(v, -kMost) * p.s * p.t;
+            const Sigmoid g = sigmoid_of(v);
+            return fmaf(-g.x * g.s, g.t, fmaxf(v, 0.0f));
         }
         case ZC_ACT_GELU: {
             const Tail n = normal_tail(v);
-            const float x = fminf(fmaxf(v, -kNoTail), kNoTail), q = n.m * n.root;
-            return v >= 0.0f ? fmaf(-x * q, n.root, v) : x * q * n.root;
+            return fmaf(-n.x * (n.m * n.t), n.t, fmaxf(v, 0.0f));
         }
         case ZC_ACT_GELU_TANH: {
-            const Parts p = sigmoid_parts(kTanh * fmaf(kCubic * v * v, v, v));
-            return fmaxf(v, -kMost) * p.s * p.t;
+            const Sigmoid g = sigmoid_of(kTanh * fmaf(kCubic * v * v, v, v));
+            return fmaf(-fminf(fabsf(v), 174.0f) * g.s, g.t, fmaxf(v, 0.0f));
         }
         case ZC_ACT_SIGMOID: {
-            const Parts p = sigmoid_parts(v);
-            return p.s * p.t;
+            const Sigmoid g = sigmoid_of(v);
+            return v >= 0.0f ? g.r : g.s * g.t;
         }
         default: return v;
     }
 }
 
-// d times the slope at v.  The factor that may be large meets a vanishing one before d does, so that finite values have finite
-// products: 4 * -1e38 has left the range of a float before it meets a 0.
+// d times the slope at v: left of 0 the slope is q, right of it 1 - q, where q is the tail less |v| times its density.
+__device__ __forceinline__ float beside(float d, float v, float s, float t) { return v >= 0.0f ? d * fmaf(-s, t, 1.0f) : s * (d * t); }
 __device__ __forceinline__ float sloped(float d, float v, uint32_t act) {
     switch (act) {
         case ZC_ACT_RELU: return v > 0.0f ? d : v != v ? v : 0.0f;
         case ZC_ACT_SILU: {
-            const Parts p = sigmoid_parts(v);
-            return fmaf(fminf(fmaxf(v, -kMost), kMost), p.rest, 1.0f) * p.s * (d * p.t);
+            const Sigmoid g = sigmoid_of(v);
+            return beside(d, v, g.s * fmaf(-g.x, g.r, 1.0f), g.t);
         }
         case ZC_ACT_GELU: {
-            // Phi(v) + v phi(v)
             const Tail n = normal_tail(v);
-            const float x = fminf(fmaxf(v, -kNoTail), kNoTail);
-            return v >= 0.0f ? d * fmaf(fmaf(x, kDensity, -n.m) * n.root, n.root, 1.0f)
-                             : d * n.root * fmaf(x, kDensity, n.m) * n.root;
+            return beside(d, v, n.t * fmaf(-n.x, kDensity, n.m), n.t);
         }
         case ZC_ACT_GELU_TANH: {
             // from 30 on the slope is 1 or 0 in 32 bits
-            const float x = v != v ? v : fminf(fmaxf(v, -30.0f), 30.0f), y = kCubic * x * x;
-            const Parts p = sigmoid_parts(kTanh * fmaf(y, x, x));
-            return fmaf(x * p.rest, kTanh * fmaf(3.0f, y, 1.0f), 1.0f) * p.s * (d * p.t);
+            const float x = v != v ? v : fminf(fabsf(v), 30.0f), y = kCubic * x * x;
+            const Sigmoid g = sigmoid_of(kTanh * fmaf(y, x, x));
+            return beside(d, v, g.s * fmaf(-x * g.r, kTanh * fmaf(3.0f, y, 1.0f), 1.0f), g.t);
         }
         case ZC_ACT_SIGMOID: {
-            const Parts p = sigmoid_parts(v != v ? v : -fabsf(v));
-            return d * p.s * p.t * p.rest;
+            const Sigmoid g = sigmoid_of(v);
+            return g.s * (d * g.t) * g.r;
         }
         default: return d;
     }

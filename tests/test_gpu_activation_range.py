@@ -90,3 +90,45 @@ def test_infinite_sums(zc, m):
         zc.zc_matmul(a, m, k, w, n, k, k, zc.epilogue(activation=GELU), out, zc.ZC_BF16, n, ws, ws.numel())
         got = out.numpy()
         assert np.isposinf(got[0]).all() and not got[1:].any()
+
+
+def far_and_near(low, high):
+    """32-bit values, spread evenly and towards 0."""
+    g = np.random.default_rng(11)
+    v = np.concatenate([g.uniform(low, high, 20000), [-5.0, -20.0, -80.0], np.geomspace(1e-6, 1, 500), -np.geomspace(1e-6, 1, 500)])
+    return ref.f32(v[(v >= low) & (v <= high)])
+
+
+@pytest.mark.parametrize("act", [SILU, SIGMOID])
+def test_digits_of_sigmoids(zc, act):
+    """sigmoid = m r 2^2h, m = 2^f with |f| <= 1 known to 2^-24 (0.7 half steps of m), the hardware's 2^f and 1 / x a unit each (2 half
+    steps), one for 1 + e and one for m r, e's own 2.7 in 1 + e: 6.7 half steps, and one for the product with v."""
+    v = far_and_near(-86.0, 30.0)
+    want = ref.activation(v, act)[0]
+    close(values(zc, v, act), want, 8 * EPS * np.abs(want), "activation %d" % act)
+
+
+@pytest.mark.parametrize("act", [SILU, SIGMOID])
+def test_digits_of_their_slopes(zc, act):
+    """SILU: q = s (1 - |v| r) left of 0 and 1 - q right of it, with s = sigmoid(-|v|) off by 5.7 half steps, r = 1 - s by 4.4, one for the
+    difference and each product.  SIGMOID: s r."""
+    v = np.unique(ref.bf16(far_and_near(-85.0, 30.0)))
+    want = ref.activation(v, act)[1]
+    s, q = ref._sigmoid(v), ref._sigmoid(-v)
+    tol = 14 * EPS * np.abs(want) if act == SIGMOID else EPS * (12 * np.abs(want) + 8 * np.abs(v) * q * s)
+    close(slopes(zc, 1.0, v, act), want, tol, "slope %d" % act)
+
+
+def test_digits_of_gelu(zc):
+    """v Phi(v), left of 0 the tail m root^2: t = 1 / (1 + x / 2) is off by 3.5 half steps, which count 1 + |t p'(t) / p(t)| <= 2.26
+    times; the polynomial's steps and coefficients by 5.6, its fit by 0.2, m's product by one, each root by 3 (the hardware's unit and the
+    carried rest), three products, and half of one for a constant: 25 half steps.  Right of 0 the tail is taken off v."""
+    v = far_and_near(-12.5, 12.5)
+    want = ref.activation(v, GELU)[0]
+    tail = np.abs(v) * (0.5 * ref._erfc(np.abs(v) / 2 ** 0.5))
+    close(values(zc, v, GELU), want, EPS * (25 * tail + 2 * np.where(v > 0, want, 0)), "gelu")
+    v = np.unique(ref.bf16(v))
+    want = ref.activation(v, GELU)[1]
+    tail, bell = 0.5 * ref._erfc(np.abs(v) / 2 ** 0.5), np.abs(v) * np.exp(-v * v / 2) / (2 * np.pi) ** 0.5
+    # the tail's 16 half steps before its roots, six for the roots and three products for both terms, three for sum and result
+    close(slopes(zc, 1.0, v, GELU), want, EPS * (13 * np.abs(want) + 25 * tail + 13 * bell), "slope")
