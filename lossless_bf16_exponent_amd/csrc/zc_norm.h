@@ -117,6 +117,12 @@ struct Team {
 struct Stat {
     float mean, off, k;
 };
+// A row's mean, rounded: without the pragma the product would go unrounded into one difference and rounded into another,
+// and what the sums of the differences say of it would be of another mean.
+__device__ __forceinline__ float mean_of(float sum, float inv_cols) {
+#pragma clang fp contract(off)
+    return sum * inv_cols;
+}
 // MEAN: there may be a mean.
 template <bool MEAN = true>
 __device__ __forceinline__ float normed(float v, const Stat &s) {
@@ -137,7 +143,7 @@ __device__ __forceinline__ Stat row_stat(const V &v, const uint32_t (&n)[CHUNKS]
 #pragma unroll
                 for (uint32_t j = 0; j < 8; ++j) t[0] = fmaf(v[i][j], unit, t[0]);
             team.sum(t);
-            mean = t[0] * inv_cols;
+            mean = mean_of(t[0], inv_cols);
             const float last = in_tail ? fmaf(tail, unit, -mean) : 0.0f;
             float u[2] = {last * last, last};
 #pragma unroll

@@ -28,8 +28,8 @@ __device__ __forceinline__ void both_stats(const X &x, const Z &z, const uint32_
                 m[1] += z[i][j];
             }
         team.sum(m);
-        sx.mean = lx ? m[0] * a.inv_cols : 0.0f;
-        sz.mean = lz ? m[1] * a.inv_cols : 0.0f;
+        sx.mean = lx ? mean_of(m[0], a.inv_cols) : 0.0f;
+        sz.mean = lz ? mean_of(m[1], a.inv_cols) : 0.0f;
         u[2] = in_tail ? xt - sx.mean : 0.0f;
         u[3] = in_tail ? zt - sz.mean : 0.0f;
         u[0] = u[2] * u[2];
