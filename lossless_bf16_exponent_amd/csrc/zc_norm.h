@@ -80,6 +80,7 @@ __device__ __forceinline__ void load_param(const Param &q, uint32_t c, uint32_t 
 // ---------------------------------------------------------------------------
 
 constexpr uint32_t kMaxWaves = 16;
+constexpr float kMost = 3.40282347e38f;  // the largest float
 
 // A team of TEAM lanes holds a row.  Sums of K values over it: over each wave,
 // then over the waves in order.  Two places in turn, so that one barrier a sum is
@@ -110,12 +111,10 @@ struct Team {
 };
 
 // The normed value of v is (v - mean) * k - off: k is 1 / deviation, and off what rounding the
-// mean left of it, which counts where the deviation is small beside the mean.  Where the
-// squares would leave the range of a float (above 2^120 in sum, infinities and NaN among
-// them, or below 2^-80 with an eps that does not cover them), the row is measured
-// 2^-80 or 2^80 times as large, which is exact for all values that matter.
+// mean left of it, which counts where the deviation is small beside the mean.  slope is k too, but a constant row, whose
+// normed values are 0, has a k of 0: lanes past its end hold zeros, which could leave the range of a float.
 struct Stat {
-    float mean, off, k;
+    float mean, off, k, slope;
 };
 // A row's mean, rounded: without the pragma the product would go unrounded into one difference and rounded into another,
 // and what the sums of the differences say of it would be of another mean.
@@ -128,58 +127,125 @@ template <bool MEAN = true>
 __device__ __forceinline__ float normed(float v, const Stat &s) {
     return MEAN ? fmaf(v - s.mean, s.k, -s.off) : v * s.k;
 }
+// A value that is the same in all lanes, in a scalar register.
+__device__ __forceinline__ float uniform(float v) {
+    return __uint_as_float((uint32_t)__builtin_amdgcn_readfirstlane((int)__float_as_uint(v)));
+}
+// What the mean's rounding left of a row's deviations, and the sum of their squares without it and with it.
+struct Deviations {
+    float rest, var, spread;
+};
+__device__ __forceinline__ Deviations beside_rest(float squares, float sum, float inv_cols) {
+    // (where the difference is lost in rounding: not below 0, and NaN stays)
+    const float rest = sum * inv_cols, left = fmaf(-rest, sum, squares);
+    return {rest, left < 0.0f ? 0.0f : left, squares};
+}
+// Next to nothing is left beside the mean's rounding.
+__device__ __forceinline__ bool lost(const Deviations &s) { return s.var < s.spread * 0x1p-16f; }
+// Whether a row has to be measured again: where that is so, or squares leave the range of a float (above 2^120 in sum, infinities and
+// NaN among them, or below 2^-80 with an eps that does not cover them).  Measured 2^-80 or 2^80 times as large it keeps all
+// digits that matter.  (The same in all of a team's lanes, and rarely.)
+__device__ __forceinline__ bool out_of_range(const Deviations &s, float eps) {
+    const bool out = !(s.var <= 0x1p120f) || (s.var < 0x1p-80f && eps < 0x1p-58f) || lost(s);
+    return __builtin_expect(__builtin_amdgcn_readfirstlane(out) != 0, 0);
+}
 
+// Keeps packed values packed: the compiler would unpack what does not change once for all rows.
+template <bool F32>
+__device__ __forceinline__ void stay_packed(Eight<F32> &v) {
+    if (!F32) asm volatile("" : "+v"(v.w[0]));
+}
+template <bool F32, uint32_t CHUNKS>
+__device__ __forceinline__ void apart(Eight<F32> (&v)[CHUNKS]) {
+#pragma unroll
+    for (uint32_t i = 0; i < CHUNKS; ++i) stay_packed(v[i]);
+}
+template <uint32_t CHUNKS>
+__device__ __forceinline__ void apart(float (&)[CHUNKS][8]) {}
+
+// A row's values in a team's lanes, with what it takes to measure them.
 template <uint32_t TEAM, uint32_t CHUNKS, typename V>
-__device__ __forceinline__ Stat row_stat(const V &v, const uint32_t (&n)[CHUNKS], uint32_t kind, float eps,
-                                         float inv_cols, Team<TEAM> &team, float tail = 0.0f, bool in_tail = false) {
-    float mean = 0.0f, rest = 0.0f, unit = 1.0f;
-    float var = 0.0f;
-    const auto measure = [&]() {
-        mean = rest = 0.0f;
+struct Measured {
+    V &v;
+    const uint32_t (&n)[CHUNKS];
+    Team<TEAM> &team;
+    uint32_t kind;
+    float eps, inv_cols, tail;
+    bool in_tail;
+
+    __device__ __forceinline__ float average(float unit) const {
+        float t[1] = {tail * unit};
+#pragma unroll
+        for (uint32_t i = 0; i < CHUNKS; ++i)
+#pragma unroll
+            for (uint32_t j = 0; j < 8; ++j) t[0] = fmaf(v[i][j], unit, t[0]);
+        team.sum(t);
+        return mean_of(t[0], inv_cols);
+    }
+    // Deviations `less` * `more` times as large: values and mean are made `less` times as large before the difference.
+    __device__ __forceinline__ Deviations deviations(float mean, float less, float more) const {
         if (kind == ZC_NORM_LAYER) {
-            float t[1] = {tail * unit};
-#pragma unroll
-            for (uint32_t i = 0; i < CHUNKS; ++i)
-#pragma unroll
-                for (uint32_t j = 0; j < 8; ++j) t[0] = fmaf(v[i][j], unit, t[0]);
-            team.sum(t);
-            mean = mean_of(t[0], inv_cols);
-            const float last = in_tail ? fmaf(tail, unit, -mean) : 0.0f;
+            const float middle = mean * less;
+            const float last = in_tail ? fmaf(tail, less, -middle) * more : 0.0f;
             float u[2] = {last * last, last};
 #pragma unroll
             for (uint32_t i = 0; i < CHUNKS; ++i)
 #pragma unroll
                 for (uint32_t j = 0; j < 8; ++j) {
-                    const float d = j < n[i] ? fmaf(v[i][j], unit, -mean) : 0.0f;
+                    const float d = j < n[i] ? fmaf(v[i][j], less, -middle) * more : 0.0f;
                     u[0] = fmaf(d, d, u[0]);
                     u[1] += d;
                 }
             team.sum(u);
-            rest = u[1] * inv_cols;
-            // (where the difference is lost in rounding: not below 0, and NaN stays)
-            const float left = fmaf(-rest, u[1], u[0]);
-            var = left < 0.0f ? 0.0f : left;
-        } else {
-            float t[1] = {tail * unit * (tail * unit)};
-#pragma unroll
-            for (uint32_t i = 0; i < CHUNKS; ++i)
-#pragma unroll
-                for (uint32_t j = 0; j < 8; ++j) {
-                    const float d = v[i][j] * unit;
-                    t[0] = fmaf(d, d, t[0]);
-                }
-            team.sum(t);
-            var = t[0];
+            return beside_rest(u[0], u[1], inv_cols);
         }
-    };
-    measure();
-    if (!(var <= 0x1p120f) || (var < 0x1p-80f && eps < 0x1p-58f)) {
-        unit = var < 1.0f ? 0x1p80f : 0x1p-80f;
-        measure();
+        const float unit = less * more;
+        float t[1] = {tail * unit * (tail * unit)};
+#pragma unroll
+        for (uint32_t i = 0; i < CHUNKS; ++i)
+#pragma unroll
+            for (uint32_t j = 0; j < 8; ++j) {
+                const float d = v[i][j] * unit;
+                t[0] = fmaf(d, d, t[0]);
+            }
+        team.sum(t);
+        return {0.0f, t[0], 0.0f};
     }
-    // eps in the row's unit (for large rows it is nothing beside their squares)
-    const float rs = __builtin_amdgcn_rsqf(fmaf(var, inv_cols, eps * unit * unit));
-    return {mean / unit, rest * rs, rs * unit};
+    // The statistics from a mean and the deviations from it, measured again where they have to be.
+    __device__ __forceinline__ Stat settle(float mean, Deviations s) const {
+        float unit = 1.0f;
+        if (out_of_range(s, eps)) {
+            apart(v);
+            if (!(s.var <= 0x1p120f)) unit = 0x1p-80f;
+            if (kind == ZC_NORM_LAYER && unit < 1.0f) {
+                // (the values' sum may have left the range too, which their mean does not)
+                const float small = average(unit);
+                mean = fabsf(small) < 0x1p50f ? fminf(fmaxf(small / unit, -kMost), kMost) : small;
+                s = deviations(mean, unit, 1.0f);
+                apart(v);
+            }
+            // The mean takes what its rounding left: a constant row then has no deviation at all.  What still deviates does so by a
+            // step of the mean at least, whose square is in range where the mean is not tiny itself.
+            const bool centre = lost(s);
+            if (centre) mean += s.rest / unit;
+            if (s.var < 0x1p-80f && eps < 0x1p-58f && unit == 1.0f && !(centre && fabsf(mean) > 0x1p-20f)) unit = 0x1p80f;
+            s = deviations(mean, fminf(unit, 1.0f), fmaxf(unit, 1.0f));
+            if (s.var == 0.0f) unit = 1.0f, s.rest = 0.0f;  // no deviation: what is left is eps, as it is
+        }
+        // eps in the row's unit (for large rows it is nothing beside their squares)
+        const float rs = __builtin_amdgcn_rsqf(fmaf(s.var, inv_cols, eps * unit * unit));
+        // (one step of the mean as the only deviation makes a product of 2^33 at most)
+        const float k = rs * unit;
+        return {uniform(mean), s.rest * rs, fabsf(mean) * k < 0x1p100f ? k : 0.0f, uniform(k)};
+    }
+};
+
+template <uint32_t TEAM, uint32_t CHUNKS, typename V>
+__device__ __forceinline__ Stat row_stat(V &v, const uint32_t (&n)[CHUNKS], uint32_t kind, float eps, float inv_cols,
+                                         Team<TEAM> &team, float tail = 0.0f, bool in_tail = false) {
+    const Measured<TEAM, CHUNKS, V> m = {v, n, team, kind, eps, inv_cols, tail, in_tail};
+    const float mean = kind == ZC_NORM_LAYER ? m.average(1.0f) : 0.0f;
+    return m.settle(mean, m.deviations(mean, 1.0f, 1.0f));
 }
 
 // ---------------------------------------------------------------------------
@@ -237,11 +303,6 @@ __device__ __forceinline__ float keep_tail(const Param &q, uint32_t c, bool on, 
     return q.f32 ? static_cast<const float *>(q.p)[c] : bf_one(static_cast<const uint16_t *>(q.p)[c]);
 }
 
-// Keeps packed values packed: the compiler would unpack what does not change once for all rows.
-template <bool F32>
-__device__ __forceinline__ void stay_packed(Eight<F32> &v) {
-    if (!F32) asm volatile("" : "+v"(v.w[0]));
-}
 // A parameter's values of a lane for all rows: floats, or BF16 pairs where every
 // parameter is BF16.  `otherwise` where there is no parameter, 0 past the row's end.
 template <bool F32>

@@ -13,10 +13,13 @@ namespace moe {
 // Both halves' statistics at once: x before the norm `before`, z before the norm `after`.
 // MEAN: one of them may be a LAYER norm.
 template <bool MEAN, uint32_t TEAM, uint32_t CHUNKS, typename X, typename Z>
-__device__ __forceinline__ void both_stats(const X &x, const Z &z, const uint32_t (&n)[CHUNKS], const NormArgs &a, bool pre,
+__device__ __forceinline__ void both_stats(X &x, Z &z, const uint32_t (&n)[CHUNKS], const NormArgs &a, bool pre,
                                            bool post, Stat &sx, Stat &sz, Team<TEAM> &team, float xt, float zt, bool in_tail) {
-    float t[2] = {0.0f, 0.0f}, rest[2] = {0.0f, 0.0f};
+    const Measured<TEAM, CHUNKS, X> mx = {x, n, team, MEAN ? a.before.kind : ZC_NORM_RMS, a.before.eps, a.inv_cols, xt, in_tail};
+    const Measured<TEAM, CHUNKS, Z> mz = {z, n, team, MEAN ? a.after.kind : ZC_NORM_RMS, a.after.eps, a.inv_cols, zt, in_tail};
     const bool lx = MEAN && pre && a.before.kind == ZC_NORM_LAYER, lz = MEAN && post && a.after.kind == ZC_NORM_LAYER;
+    float mean[2] = {0.0f, 0.0f};
+    Deviations s[2];
     if (MEAN && (lx || lz)) {
         float u[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         float m[2] = {xt, zt};
@@ -28,32 +31,27 @@ __device__ __forceinline__ void both_stats(const X &x, const Z &z, const uint32_
                 m[1] += z[i][j];
             }
         team.sum(m);
-        sx.mean = lx ? mean_of(m[0], a.inv_cols) : 0.0f;
-        sz.mean = lz ? mean_of(m[1], a.inv_cols) : 0.0f;
-        u[2] = in_tail ? xt - sx.mean : 0.0f;
-        u[3] = in_tail ? zt - sz.mean : 0.0f;
+        mean[0] = lx ? mean_of(m[0], a.inv_cols) : 0.0f;
+        mean[1] = lz ? mean_of(m[1], a.inv_cols) : 0.0f;
+        u[2] = in_tail ? xt - mean[0] : 0.0f;
+        u[3] = in_tail ? zt - mean[1] : 0.0f;
         u[0] = u[2] * u[2];
         u[1] = u[3] * u[3];
 #pragma unroll
         for (uint32_t i = 0; i < CHUNKS; ++i)
 #pragma unroll
             for (uint32_t j = 0; j < 8; ++j) {
-                const float dx = n[i] ? x[i][j] - sx.mean : 0.0f, dz = n[i] ? z[i][j] - sz.mean : 0.0f;
+                const float dx = n[i] ? x[i][j] - mean[0] : 0.0f, dz = n[i] ? z[i][j] - mean[1] : 0.0f;
                 u[0] = fmaf(dx, dx, u[0]);
                 u[1] = fmaf(dz, dz, u[1]);
                 u[2] += dx;
                 u[3] += dz;
             }
         team.sum(u);
-        rest[0] = lx ? u[2] * a.inv_cols : 0.0f;
-        rest[1] = lz ? u[3] * a.inv_cols : 0.0f;
-        t[0] = fmaf(-rest[0], u[2], u[0]);
-        t[1] = fmaf(-rest[1], u[3], u[1]);
-#pragma unroll
-        for (uint32_t k = 0; k < 2; ++k) t[k] = t[k] < 0.0f ? 0.0f : t[k];
+        s[0] = beside_rest(u[0], lx ? u[2] : 0.0f, a.inv_cols);
+        s[1] = beside_rest(u[1], lz ? u[3] : 0.0f, a.inv_cols);
     } else {
-        t[0] = xt * xt;
-        t[1] = zt * zt;
+        float t[2] = {xt * xt, zt * zt};
 #pragma unroll
         for (uint32_t i = 0; i < CHUNKS; ++i)
 #pragma unroll
@@ -62,20 +60,11 @@ __device__ __forceinline__ void both_stats(const X &x, const Z &z, const uint32_
                 t[1] = fmaf(z[i][j], z[i][j], t[1]);
             }
         team.sum(t);
+        s[0] = {0.0f, t[0], 0.0f};
+        s[1] = {0.0f, t[1], 0.0f};
     }
-    if (pre) {
-        sx.k = __builtin_amdgcn_rsqf(fmaf(t[0], a.inv_cols, a.before.eps));
-        sx.off = rest[0] * sx.k;
-    }
-    if (post) {
-        sz.k = __builtin_amdgcn_rsqf(fmaf(t[1], a.inv_cols, a.after.eps));
-        sz.off = rest[1] * sz.k;
-    }
-    // squares outside the range of a float: one row at a time
-    if (pre && (!(t[0] <= 0x1p120f) || (t[0] < 0x1p-80f && a.before.eps < 0x1p-58f)))
-        sx = row_stat<TEAM, CHUNKS>(x, n, a.before.kind, a.before.eps, a.inv_cols, team, xt, in_tail);
-    if (post && (!(t[1] <= 0x1p120f) || (t[1] < 0x1p-80f && a.after.eps < 0x1p-58f)))
-        sz = row_stat<TEAM, CHUNKS>(z, n, a.after.kind, a.after.eps, a.inv_cols, team, zt, in_tail);
+    if (pre) sx = mx.settle(mean[0], s[0]);
+    if (post) sz = mz.settle(mean[1], s[1]);
 }
 
 // With v^ the normed value and u = dy * w the gradient there, that of v is
@@ -199,7 +188,9 @@ __global__ __launch_bounds__(block_threads(TEAM)) void norm_backward_kernel(Norm
             stay_packed(w2[i]);
         }
         const float rg = ANY && a.row_gate ? a.row_gate[row] : 1.0f;
-        Stat sx = {0.0f, 0.0f, 1.0f}, sz = sx;
+        Stat sx = {0.0f, 0.0f, 1.0f, 1.0f}, sz = sx;
+        // (one register where there is no mean)
+        const auto slope = [](const Stat &s) { return ANY ? s.slope : s.k; };
         if (pre || post) both_stats<ANY, TEAM, CHUNKS>(v.x, v.z, n, a, pre, post, sx, sz, team, v.xt, v.zt, in_tail);
 #pragma unroll
         for (uint32_t i = 0; i < CHUNKS; ++i) {
@@ -246,7 +237,7 @@ __global__ __launch_bounds__(block_threads(TEAM)) void norm_backward_kernel(Norm
             }
             if (!WIDE) {
                 const float u = fmaf(-ht, m0, gt);
-                gt = fmaf(ANY ? u - m1 : u, sx.k, v.drt);
+                gt = fmaf(ANY ? u - m1 : u, slope(sx), v.drt);
             }
 #pragma unroll
             for (uint32_t i = 0; i < CHUNKS; ++i) stay_packed(v.x[i]);
@@ -255,7 +246,7 @@ __global__ __launch_bounds__(block_threads(TEAM)) void norm_backward_kernel(Norm
 #pragma unroll
                 for (uint32_t j = 0; j < 8; ++j) {
                     const float u = fmaf(-normed<ANY>(v.x[i][j], sx), m0, g[i][j]);
-                    g[i][j] = fmaf(ANY ? u - m1 : u, sx.k, v.dr[i][j]);
+                    g[i][j] = fmaf(ANY ? u - m1 : u, slope(sx), v.dr[i][j]);
                 }
         } else {
             gt = v.drt + v.dyt;
@@ -317,7 +308,7 @@ __global__ __launch_bounds__(block_threads(TEAM)) void norm_backward_kernel(Norm
         if (!WIDE) {
             if (post) {
                 const float u = fmaf(-zht, m0, gt);
-                gt = (ANY ? u - m1 : u) * sz.k;
+                gt = (ANY ? u - m1 : u) * slope(sz);
             }
             store_tail<false>(row_of(a.dz, row * a.dz_stride, a.cols, 2), ct, gt);
         }
@@ -328,7 +319,7 @@ __global__ __launch_bounds__(block_threads(TEAM)) void norm_backward_kernel(Norm
 #pragma unroll
                 for (uint32_t j = 0; j < 8; ++j) {
                     const float u = fmaf(-normed<ANY>(v.z[i][j], sz), m0, g[i][j]);
-                    g[i][j] = (ANY ? u - m1 : u) * sz.k;
+                    g[i][j] = (ANY ? u - m1 : u) * slope(sz);
                 }
             store_row<false, WIDE>(rz, (i * TEAM + sub) * 8, g[i]);
         }

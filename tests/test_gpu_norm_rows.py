@@ -38,3 +38,42 @@ def test_nearly_constant_rows(zc):
         rs = ref.stat(x, ref.LAYER, 1e-12)[1]
         tol = ref.BF16_HALF_STEP * np.abs(hat) + ref.EPS32 * 128 * (np.abs(hat) + 1 + 0.0625 * 64 * rs)
         close(y, hat, tol, "y of %d columns" % n)
+
+
+# constant rows: sums that fit a float and sums that do not, of either sign, small and 0
+CONSTANTS = [2.0 ** 50, 1e20, -1e30, 1e37, -3e38, 3.0, 2.0 ** -100, 0.0]
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("eps", [1e-6, 1e-20, 1e-30])
+@pytest.mark.parametrize("n", [1, 64, 700, 1030, 2500, 5125, 7168, 16384])
+def test_constant_rows_under_a_layer_norm(zc, n, eps, f32):
+    """A constant row differs from its mean nowhere: its norm is the bias, whatever its size and that of eps."""
+    v = (ref.f32 if f32 else ref.bf16)(np.repeat(np.array(CONSTANTS)[:, None], n, axis=1))
+    # beside rows that are not
+    v[5] = ref.bf16(np.random.default_rng(n).standard_normal(n))
+    still = [i for i in range(len(CONSTANTS)) if i != 5]
+    for bias in (True, False):
+        c = with_rows(zc, v, None, f32, after=ref.NONE, before=ref.LAYER, eps=eps, bias=bias)
+        y = c.forward(q=True)["y"].numpy()
+        want = ref.bf16(c.before.b) if bias else np.zeros(n)
+        assert np.array_equal(y[still], np.broadcast_to(want, y[still].shape))
+        assert np.array_equal(c.forward()["y"].numpy(), y)
+        o = c.backward(dr=False)
+        assert np.isfinite(o["dx"].numpy()).all()
+        if n > 1:  # (of one column the gradient is what rounding leaves of 0)
+            c.check_backward()
+        c.dy = c.dy * (np.arange(len(CONSTANTS)) != 5)[:, None]
+        assert not c.backward()["dw2"].numpy().any()
+    # the block's output
+    z = ref.bf16(v)
+    c = with_rows(zc, np.zeros_like(v), z, f32, after=ref.LAYER, before=ref.NONE, eps=eps, gate=False, scale=1.0, bias=True)
+    for q in (False, True):
+        r = c.forward(q=q)["r"].numpy()
+        assert np.array_equal(r[still], np.broadcast_to(half(c.after.b, f32), r[still].shape))
+    if n > 1:
+        c.check_backward()
+
+
+def half(v, f32):
+    return ref.f32(v) if f32 else ref.bf16(v)
