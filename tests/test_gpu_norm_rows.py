@@ -23,6 +23,43 @@ def with_rows(zc, x, z, f32, **kw):
     return c
 
 
+def check_plain(c):
+    """Sum and norm without the 8-bit blocks, and nothing written between the rows."""
+    o = c.forward()
+    r, er, y, ey = ref.norm(c.x, c.z, c.after, c.before, c.gate, c.row_gate, c.scale)
+    close(o["r"].numpy()[:, :c.cols], r, half_step(c.f32) * np.abs(r) + 2 * er, "r")
+    close(o["y"].numpy()[:, :c.cols], y, ref.BF16_HALF_STEP * np.abs(y) + 2 * ey, "y")
+    if c.gap:
+        for v in (o["r"], o["y"]):
+            assert bool((v.t[:, c.cols:].contiguous().view(torch.uint8) == 0xA5).all())
+
+
+# rows on 16 bytes and off them, whole pieces of eight and tails, every team, and more rows than the blocks take at once
+FORMS = SHAPES + [(5, 7168, 8, 8), (4, 7168, 1, 0), (3, 4097, 7, 5), (3, 16383, 2, 1), (5000, 72, 0, 0), (1500, 1100, 3, 1)]
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("m,n,gap,offset", FORMS)
+def test_forward_without_blocks(zc, m, n, gap, offset, f32):
+    check_plain(Case(zc, m, n, gap=gap, offset=offset, f32=f32, params_f32=f32, row_gate=True))
+    check_plain(Case(zc, m, n, gap=gap, offset=offset, f32=f32, params_f32=not f32, bias=True, after=ref.LAYER, before=ref.LAYER))
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("kw", KINDS + [dict(weights=False), dict(gate=False), dict(z=False), dict(z=False, before=ref.LAYER),
+                                        dict(gate=False, row_gate=True, bias=True), dict(scale=0.0), dict(scale=-3.0),
+                                        dict(params_f32=True, bias=True)])
+def test_kinds_without_blocks(zc, kw, f32):
+    for m, n, gap, offset in ((5, 200, 0, 0), (5, 203, 2, 1), (3, 2500, 0, 0), (3, 2504, 8, 8)):
+        check_plain(Case(zc, m, n, gap=gap, offset=offset, f32=f32, **kw))
+
+
+def test_rows_in_turn(zc):
+    """More rows than the grid's teams: every row is what it is alone."""
+    c = Case(zc, 2300, 4100, gap=1, offset=1, row_gate=True, bias=True)
+    check_plain(c)
+
+
 def test_nearly_constant_rows(zc):
     """One value of a row a few steps from the others: the deviation is theirs, not that of a rounded mean."""
     for n in (300, 700, 5125, 7168):
