@@ -110,12 +110,14 @@ struct Team {
     }
 };
 
-// The normed value of v is (v - mean) * k - off: k is 1 / deviation, and off what rounding the
-// mean left of it, which counts where the deviation is small beside the mean.  slope is k too, but a constant row, whose
-// normed values are 0, has a k of 0: lanes past its end hold zeros, which could leave the range of a float.
+// The normed value of v is (v / 2 - mean / 2) * k - off, in halves so that no difference leaves the range of a float: slope is
+// 1 / deviation, k twice that, and off what rounding the mean left, which counts where the deviation is small beside the
+// mean.  A constant row, whose normed values are 0, has a k of 0: lanes past its end hold zeros, which could leave the
+// range.
 struct Stat {
-    float mean, off, k, slope;
+    float middle, off, k, slope;
 };
+constexpr Stat kNoNorm = {0.0f, 0.0f, 2.0f, 1.0f};
 // A row's mean, rounded: without the pragma the product would go unrounded into one difference and rounded into another,
 // and what the sums of the differences say of it would be of another mean.
 __device__ __forceinline__ float mean_of(float sum, float inv_cols) {
@@ -125,7 +127,7 @@ __device__ __forceinline__ float mean_of(float sum, float inv_cols) {
 // MEAN: there may be a mean.
 template <bool MEAN = true>
 __device__ __forceinline__ float normed(float v, const Stat &s) {
-    return MEAN ? fmaf(v - s.mean, s.k, -s.off) : v * s.k;
+    return MEAN ? fmaf(fmaf(v, 0.5f, -s.middle), s.k, -s.off) : v * s.slope;
 }
 // A value that is the same in all lanes, in a scalar register.
 __device__ __forceinline__ float uniform(float v) {
@@ -235,8 +237,8 @@ struct Measured {
         // eps in the row's unit (for large rows it is nothing beside their squares)
         const float rs = __builtin_amdgcn_rsqf(fmaf(s.var, inv_cols, eps * unit * unit));
         // (one step of the mean as the only deviation makes a product of 2^33 at most)
-        const float k = rs * unit;
-        return {uniform(mean), s.rest * rs, fabsf(mean) * k < 0x1p100f ? k : 0.0f, uniform(k)};
+        const float slope = rs * unit;
+        return {uniform(0.5f * mean), s.rest * rs, fabsf(mean) * slope < 0x1p100f ? 2.0f * slope : 0.0f, uniform(slope)};
     }
 };
 

@@ -35,7 +35,7 @@ __global__ __launch_bounds__(block_threads(TEAM)) void norm_kernel(NormArgs a) {
             for (uint32_t i = 0; i < CHUNKS; ++i) z[i].load(a.z, row * a.z_stride + (i * TEAM + sub) * 8, n[i], true);
             const float share = a.row_gate ? a.scale * a.row_gate[row] : a.scale;
             const bool on = a.after.kind != ZC_NORM_NONE;
-            Stat s = {0.0f, 0.0f, 1.0f, 1.0f};
+            Stat s = kNoNorm;
             if (on) s = row_stat<TEAM, CHUNKS>(z, n, a.after.kind, a.after.eps, a.inv_cols, team);
 #pragma unroll
             for (uint32_t i = 0; i < CHUNKS; ++i) {
@@ -166,7 +166,7 @@ __global__ __launch_bounds__(block_threads(TEAM), whole_waves(TEAM)) void norm_r
         }
         float v[CHUNKS][8];
         const float share = a.row_gate ? a.scale * a.row_gate[row] : a.scale;
-        Stat s = {0.0f, 0.0f, 1.0f, 1.0f};
+        Stat s = kNoNorm;
         if (post) s = row_stat<TEAM, CHUNKS>(z, n, a.after.kind, a.after.eps, a.inv_cols, team, zt, in_tail);
         float vt = 0.0f;
         if (!WIDE) vt = a.z ? fmaf(share, gatet * (post ? fmaf(normed(zt, s), w1t, b1t) : zt), xt) : xt;

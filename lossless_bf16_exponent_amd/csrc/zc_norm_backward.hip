@@ -188,9 +188,7 @@ __global__ __launch_bounds__(block_threads(TEAM)) void norm_backward_kernel(Norm
             stay_packed(w2[i]);
         }
         const float rg = ANY && a.row_gate ? a.row_gate[row] : 1.0f;
-        Stat sx = {0.0f, 0.0f, 1.0f, 1.0f}, sz = sx;
-        // (one register where there is no mean)
-        const auto slope = [](const Stat &s) { return ANY ? s.slope : s.k; };
+        Stat sx = kNoNorm, sz = kNoNorm;
         if (pre || post) both_stats<ANY, TEAM, CHUNKS>(v.x, v.z, n, a, pre, post, sx, sz, team, v.xt, v.zt, in_tail);
 #pragma unroll
         for (uint32_t i = 0; i < CHUNKS; ++i) {
@@ -237,7 +235,7 @@ __global__ __launch_bounds__(block_threads(TEAM)) void norm_backward_kernel(Norm
             }
             if (!WIDE) {
                 const float u = fmaf(-ht, m0, gt);
-                gt = fmaf(ANY ? u - m1 : u, slope(sx), v.drt);
+                gt = fmaf(ANY ? u - m1 : u, sx.slope, v.drt);
             }
 #pragma unroll
             for (uint32_t i = 0; i < CHUNKS; ++i) stay_packed(v.x[i]);
@@ -246,7 +244,7 @@ __global__ __launch_bounds__(block_threads(TEAM)) void norm_backward_kernel(Norm
 #pragma unroll
                 for (uint32_t j = 0; j < 8; ++j) {
                     const float u = fmaf(-normed<ANY>(v.x[i][j], sx), m0, g[i][j]);
-                    g[i][j] = fmaf(ANY ? u - m1 : u, slope(sx), v.dr[i][j]);
+                    g[i][j] = fmaf(ANY ? u - m1 : u, sx.slope, v.dr[i][j]);
                 }
         } else {
             gt = v.drt + v.dyt;
@@ -308,7 +306,7 @@ __global__ __launch_bounds__(block_threads(TEAM)) void norm_backward_kernel(Norm
         if (!WIDE) {
             if (post) {
                 const float u = fmaf(-zht, m0, gt);
-                gt = (ANY ? u - m1 : u) * slope(sz);
+                gt = (ANY ? u - m1 : u) * sz.slope;
             }
             store_tail<false>(row_of(a.dz, row * a.dz_stride, a.cols, 2), ct, gt);
         }
@@ -319,7 +317,7 @@ __global__ __launch_bounds__(block_threads(TEAM)) void norm_backward_kernel(Norm
 #pragma unroll
                 for (uint32_t j = 0; j < 8; ++j) {
                     const float u = fmaf(-normed<ANY>(v.z[i][j], sz), m0, g[i][j]);
-                    g[i][j] = (ANY ? u - m1 : u) * slope(sz);
+                    g[i][j] = (ANY ? u - m1 : u) * sz.slope;
                 }
             store_row<false, WIDE>(rz, (i * TEAM + sub) * 8, g[i]);
         }

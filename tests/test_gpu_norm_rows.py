@@ -114,3 +114,32 @@ def test_constant_rows_under_a_layer_norm(zc, n, eps, f32):
 
 def half(v, f32):
     return ref.f32(v) if f32 else ref.bf16(v)
+
+
+def wide_rows(n, f32):
+    """Rows whose values lie further from their mean than the largest float."""
+    big = 3e38
+    x = np.full((5, n), -big)
+    x[0, 0] = big
+    x[1] = big
+    x[1, n // 2] = -big
+    x[2, ::2] = big
+    x[3] = np.random.default_rng(n).uniform(-big, big, n)
+    x[4] = np.random.default_rng(n).standard_normal(n)
+    return (ref.f32 if f32 else ref.bf16)(x)
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("n", [9, 700, 1030, 5125, 7168])
+def test_layer_norm_over_the_whole_range(zc, n, f32):
+    x = wide_rows(n, f32)
+    c = with_rows(zc, x, None, f32, after=ref.NONE, before=ref.LAYER, bias=True)
+    c.check_forward()
+    check_plain(c)
+    c.check_backward()
+    z = wide_rows(n, False)
+    # (a large scale: the gradient, divided by the deviation, stays above the smallest normal number)
+    c = with_rows(zc, np.zeros((5, n)), z, f32, after=ref.LAYER, before=ref.NONE, scale=2.0 ** 60, gate=False)
+    c.check_forward()
+    check_plain(c)
+    c.check_backward()
