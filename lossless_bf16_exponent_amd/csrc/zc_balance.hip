@@ -31,6 +31,7 @@ struct BalanceArgs {
     const float *dloss, *dzloss;
     uint64_t stride, add_stride, out_stride;
     uint32_t tokens, experts, top_k, sequences, tile_rows, run;
+    double experts_each;  // experts / top_k
 };
 
 constexpr uint32_t kJoinZ = ZC_MAX_EXPERTS / kLanes, kJoinUsed = kJoinZ + 1, kJoinDone = kJoinUsed + 1, kJoinWords = kJoinDone + 1;
@@ -304,9 +305,10 @@ __global__ __launch_bounds__(kJThreads) void balance_join_kernel(BalanceArgs a) 
     const float z = __uint_as_float(word(kJoinZ));
     const uint32_t n = word(kJoinUsed);
     a.used[s] = (int32_t)n;
-    const float each = n ? 1.0f / (float)n : 0.0f;
-    if (a.loss) a.loss[s] = n ? share * each * each * ((float)a.experts / (float)a.top_k) : 0.0f;
-    if (a.zloss) a.zloss[s] = n ? z * each : 0.0f;
+    // (quotients in 64 bits: the sums' own error is all that they have)
+    const double each = n ? 1.0 / (double)n : 0.0;
+    if (a.loss) a.loss[s] = n ? (float)((double)share * each * each * a.experts_each) : 0.0f;
+    if (a.zloss) a.zloss[s] = n ? (float)((double)z * each) : 0.0f;
 }
 // Without tokens there are no tiles.
 __global__ __launch_bounds__(256) void balance_zero_kernel(BalanceArgs a) {
@@ -508,6 +510,7 @@ extern "C" zc_status zc_balance(const void *d_logits, uint32_t logits_type, uint
     a.top_k = cfg->top_k;
     a.sequences = sequences;
     a.tile_rows = tile_rows_of(tokens);
+    a.experts_each = (double)a.experts / (double)a.top_k;
     Launches on(stream);
     if (!tokens) {
         on.launch(balance_zero_kernel, dim3((uint32_t)ceil_div((uint64_t)sequences * a.experts, 256)), dim3(256), a);
