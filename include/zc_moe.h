@@ -447,7 +447,8 @@ uint64_t zc_balance_workspace_bytes(uint64_t tokens, uint32_t experts, uint32_t 
  *   d_loss[s]       experts / (top_k n^2) * sum over e of counts[s, e] * sum over its tokens of p[t, e]
  *   d_zloss[s]      1 / n * sum over its tokens of (log of the sum over e of exp(logits[t, e]))^2
  * Without tokens the losses are 0.  The losses may be NULL, and then d_logits
- * too.  A token whose logits are all -inf has p = 0 and no part in the z loss.
+ * too.  A token whose logits are all -inf has p = 0 and no part in the z loss; +inf makes its
+ * sequence's z loss infinite, and the softmax of its token NaN, NaN all of its sequence's.
  * sequences is at most ZC_MAX_SEQUENCES; with tokens = 0 everything is written (zeros). */
 zc_status zc_balance(const void *d_logits, uint32_t logits_type, uint64_t tokens, uint64_t logits_stride,
                      const zc_route_config *cfg, const int32_t *d_ids, const uint8_t *d_mask, uint32_t sequences,

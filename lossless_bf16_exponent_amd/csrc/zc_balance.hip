@@ -85,8 +85,8 @@ __device__ __forceinline__ float exp_of(float v) {
     return fmaf(e, rest * 0.69314718f, e);
 }
 
-// Softmax of the wave's logits, and the logarithm of its sum of exponentials: 0 and
-// 0 where all are -inf.  NaN and +inf make all of it NaN.
+// Softmax of the team's logits, and the logarithm of its sum of exponentials: 0 and
+// 0 where all are -inf.  NaN makes all of it NaN; +inf the softmax, and the logarithm is +inf.
 template <uint32_t LANES, uint32_t V>
 __device__ __forceinline__ float softmax(const float (&l)[V], float (&p)[V]) {
     float top = l[0];
@@ -104,6 +104,12 @@ __device__ __forceinline__ float softmax(const float (&l)[V], float (&p)[V]) {
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
     for (uint32_t i = 0; i < V; ++i) p[i] *= inv;
+    if (top == __builtin_inff()) {
+        sum = 0.0f;
+#pragma unroll
+        for (uint32_t i = 0; i < V; ++i) sum += l[i] != l[i] ? l[i] : 0.0f;
+        return top + team_sum<LANES>(sum);
+    }
     return sum == 0.0f ? 0.0f : top + logf(sum);
 }
 // Sigmoids over their sum; rest: 1 - sigmoid.

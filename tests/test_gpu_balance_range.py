@@ -30,3 +30,28 @@ def test_losses_of_exact_sums_are_rounded_once(zc, experts, top_k, sigmoid):
     assert np.array_equal(o["loss"].numpy(), ref.f32(loss))
     if experts == 1:
         assert np.array_equal(o["zloss"].numpy(), ref.f32(z))
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("experts", [12, 200, 300])
+def test_infinite_logits(zc, experts, sigmoid):
+    """The logarithm of a sum that is infinite: infinite.  A sigmoid score of +inf is 1, a softmax has no value; NaN stays NaN, and
+    all of it in its sequence."""
+    c = Case(zc, 100, experts, 2, sigmoid, offsets=[0, 20, 40, 60, 80, 100])
+    clean = {k: v.numpy().copy() for k, v in c.forward().items()}
+    c.d["x"][25, 3] = float("inf")
+    c.d["x"][45, [1, 11]] = float("inf")
+    c.d["x"][45, 2] = float("-inf")
+    c.d["x"][65, 3], c.d["x"][65, 7] = float("inf"), float("nan")
+    o = c.forward()
+    z, loss = o["zloss"].numpy(), o["loss"].numpy()
+    assert np.isposinf(z[[1, 2]]).all() and np.isnan(z[3])
+    assert np.array_equal(z[[0, 4]], clean["zloss"][[0, 4]]) and np.array_equal(loss[[0, 4]], clean["loss"][[0, 4]])
+    assert np.array_equal(o["counts"].numpy(), clean["counts"])
+    assert np.isnan(loss[3]) and (np.isfinite(loss[[1, 2]]).all() if sigmoid else np.isnan(loss[[1, 2]]).all())
+    if sigmoid:
+        x = c.x.copy()
+        x[25, 3] = x[45, 1] = x[45, 11] = 200.0  # whose sigmoid is 1 too
+        x[45, 2] = -np.inf
+        want = ref.balance(x, c.ids, c.mask, c.offsets, experts, 2, True)[2]
+        assert (np.abs(loss - want)[[1, 2]] <= 500 * ref.EPS32 * want[[1, 2]]).all()
