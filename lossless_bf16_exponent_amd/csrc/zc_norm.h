@@ -323,8 +323,8 @@ __device__ __forceinline__ void keep_param(const Param &q, uint32_t c, uint32_t 
 
 constexpr uint32_t block_threads(uint32_t team) { return team < 256 ? 256 : team; }
 constexpr uint32_t block_teams(uint32_t team) { return team < 256 ? 256 / team : 1; }
-// Waves that a SIMD holds of the forward kernel of whole rows.
-constexpr uint32_t whole_waves(uint32_t team) { return 4; }
+// Waves that a SIMD holds of the forward kernel of whole rows, whatever its team.
+constexpr uint32_t kRowsWaves = 4;
 
 // ---------------------------------------------------------------------------
 // host

@@ -75,7 +75,7 @@ __device__ __forceinline__ void both_stats(X &x, Z &z, const uint32_t (&n)[CHUNK
 // and weights and gate stay in registers.  Values past a row's end read as 0, have a gradient of 0, and add nothing.
 //
 // ANY: with biases, means and the rows' gates; without, about 34 instructions a value, which bound the kernel
-// beside the memory: 8192 x 7168 takes 184 us with ANY and 128 without, 5.5 TB/s, past what a large copy
+// beside the memory: 8192 x 7168 takes 178 us with ANY and 128 without, 5.5 TB/s, past what a large copy
 // reaches (246 without the loads ahead, and with loads under conditions).  Its registers would not hold the parameters
 // beside five sums: ANY has them as floats in LDS, or, of rows past 8192, in memory.  WIDE: as in the forward kernel.
 template <bool F32S, bool F32P, bool WIDE, bool ANY, uint32_t TEAM, uint32_t CHUNKS>
