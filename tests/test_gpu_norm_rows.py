@@ -143,3 +143,14 @@ def test_layer_norm_over_the_whole_range(zc, n, f32):
     c.check_forward()
     check_plain(c)
     c.check_backward()
+
+
+@pytest.mark.parametrize("after", [ref.RMS, ref.LAYER])
+@pytest.mark.parametrize("n", [64, 700, 5125, 7168])
+def test_both_halves_out_of_range_at_once(zc, n, after):
+    """Both norms measured again, in some of the rows that a workgroup holds and not in others."""
+    x, z = wide_rows(n, True), wide_rows(n, False)[[4, 0, 1, 4, 2]]
+    c = with_rows(zc, x, z, True, after=after, before=ref.LAYER, scale=2.0 ** 60, bias=True, row_gate=True)
+    c.check_forward()
+    check_plain(c)
+    c.check_backward()
